@@ -1,5 +1,6 @@
 """Python binding of libdf11 (include/df11.h): DFloat11 block encoding on the
-host and block decoding on an MI355X.
+host and block decoding on an MI355X; and, in the step module, the operators
+of include/df11_step.h (4-bit weights, paged key-value cache).
 
 Argument marshalling only: every step of the encoder runs in the library's
 C++ code and every step of the decode runs in its HIP kernel.  PyTorch is used
@@ -16,6 +17,13 @@ import ctypes
 import os
 
 import numpy as np
+
+from . import step
+from .step import (  # noqa: F401
+    DF11_CACHE_BF16, DF11_CACHE_E4M3, STEP_EXPORTS, df11_mx4_dequantize, df11_mx4_matmul,
+    df11_mx4_matmul_workspace_bytes, df11_mx4_quantize, df11_paged_append, df11_paged_attention,
+    df11_paged_attention_workspace_bytes,
+)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdf11.so")
@@ -169,6 +177,7 @@ def lib():
     L.df11_last_hip_error.restype = ctypes.c_int32
     L.df11_hip_error_name.argtypes = [ctypes.c_int32]
     L.df11_hip_error_name.restype = ctypes.c_char_p
+    step.declare(L)
     _lib = L
     return L
 
@@ -662,4 +671,7 @@ __all__ = [
     "GpuEncoded", "df11_bandwidth_reference", "df11_gpu_encode_noalloc", "DF11_NOALLOC_WORKSPACE_BYTES", "DF11_REFERENCE_SKELETON", "DF11_REFERENCE_STREAM", "DF11_REFERENCE_WRITES", "DF11_REFERENCE_READS",
     "Encoded", "Sections",
     "DeviceBlock", "DF11Error", "matrix_views", "lib", "library_stamp",
+    "df11_mx4_quantize", "df11_mx4_dequantize", "df11_mx4_matmul", "df11_mx4_matmul_workspace_bytes",
+    "df11_paged_append", "df11_paged_attention", "df11_paged_attention_workspace_bytes",
+    "DF11_CACHE_BF16", "DF11_CACHE_E4M3",
 ]

@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libdf11.so")
 STAMP = LIB + ".stamp"
 
 HOST_SOURCES = ["df11_encode.cpp", "df11_tables.cpp", "df11_capi.cpp"]
-HIP_SOURCES = ["df11_decode.hip", "df11_gpu_encode.hip", "df11_reference.hip"]
+HIP_SOURCES = ["df11_decode.hip", "df11_gpu_encode.hip", "df11_reference.hip", "df11_mx4.hip", "df11_paged.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -1,0 +1,605 @@
+// Paged key-value cache (gfx950): writing new tokens into it and the
+// attention of one new token for each sequence (include/df11_step.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "df11_internal.h"
+#include "df11_step.h"
+#include "df11_wave.h"
+
+namespace {
+
+using df11w::v2u;
+using df11w::v4u;
+
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Pages {
+    uint8_t *base;
+    uint64_t page, head, row;  // strides in bytes
+    const float *scale;
+};
+
+// ---- Append ----------------------------------------------------------------
+// A lane moves 8 values of K and the same 8 of V.  Bound by latency for the
+// tokens of a step, by HBM for a prompt.
+
+struct AppendParams {
+    Pages k, v;
+    const uint16_t *ks, *vs;
+    uint64_t k_token, k_head, v_token, v_head;  // source strides, elements
+    const int64_t *slots;
+    uint64_t lanes;  // tokens * kv_heads * head_dim / 8
+    uint64_t n_slots;
+    uint32_t kv_heads, dim_shift, page_shift;  // head_dim / 8 = 1 << dim_shift
+};
+
+__device__ __forceinline__ v4u load8(const uint16_t *p, bool aligned) {
+    if (aligned) return *reinterpret_cast<const v4u *>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | (uint32_t{p[2 * i + 1]} << 16);
+    return v4u{w[0], w[1], w[2], w[3]};
+}
+
+// E4M3 of x / scale, saturating: the conversion itself turns magnitudes over
+// 448 into NaN, so they are held to 448 before it, and NaN is let through.
+__device__ __forceinline__ float to_e4m3_range(uint32_t bits, float scale) {
+    const float v = __builtin_bit_cast(float, bits) / scale;
+    return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
+}
+
+__device__ __forceinline__ v2u e4m3x8(v4u x, float scale) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int r = 0;
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i] << 16, scale),
+                                            to_e4m3_range(w[2 * i] & 0xFFFF0000u, scale), r, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i + 1] << 16, scale),
+                                            to_e4m3_range(w[2 * i + 1] & 0xFFFF0000u, scale), r, true);
+        o[i] = static_cast<uint32_t>(r);
+    }
+    return v2u{o[0], o[1]};
+}
+
+template <bool kE4M3, bool kAligned>
+__global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
+    const uint32_t per_head = 1u << p.dim_shift;
+    for (uint64_t i = uint64_t{blockIdx.x} * 256 + threadIdx.x; i < p.lanes; i += uint64_t{gridDim.x} * 256) {
+        const uint32_t d = static_cast<uint32_t>(i) & (per_head - 1);
+        const uint64_t th = i >> p.dim_shift;
+        const uint64_t t = th / p.kv_heads;
+        const uint32_t h = static_cast<uint32_t>(th - t * p.kv_heads);
+        const int64_t slot = p.slots[t];
+        if (slot < 0 || static_cast<uint64_t>(slot) >= p.n_slots) continue;
+        const v4u kv = load8(p.ks + t * p.k_token + h * p.k_head + 8 * d, kAligned);
+        const v4u vv = load8(p.vs + t * p.v_token + h * p.v_head + 8 * d, kAligned);
+        const uint64_t page = static_cast<uint64_t>(slot) >> p.page_shift;
+        const uint64_t row = static_cast<uint64_t>(slot) & ((uint64_t{1} << p.page_shift) - 1);
+        uint8_t *ko = p.k.base + page * p.k.page + h * p.k.head + row * p.k.row;
+        uint8_t *vo = p.v.base + page * p.v.page + h * p.v.head + row * p.v.row;
+        if (kE4M3) {
+            *reinterpret_cast<v2u *>(ko + 8 * d) = e4m3x8(kv, p.k.scale[h]);
+            *reinterpret_cast<v2u *>(vo + 8 * d) = e4m3x8(vv, p.v.scale[h]);
+        } else {
+            *reinterpret_cast<v4u *>(ko + 16 * d) = kv;
+            *reinterpret_cast<v4u *>(vo + 16 * d) = vv;
+        }
+    }
+}
+
+// ---- Attention of one token ------------------------------------------------
+// A sequence's positions are cut into chunks of `chunk`; a workgroup takes one
+// chunk of one cache head for up to 16 of its query heads, its four waves the
+// chunk's steps of 32 positions in turn.  Each wave keeps the running maximum,
+// sum and weighted values of what it has seen, the waves join in LDS, and a
+// second kernel joins the chunks.
+//
+// Products are matrix instructions of 16 x 16 x 32 in this orientation:
+//   scores^T [position, head] = K [position, d] Q^T [d, head]
+//   out^T    [d, head]        = V^T [d, position] W^T [position, head]
+// A lane (r = lane % 16, q = lane / 16) receives the scores of head r at
+// positions 4 q + 0..3 of each half of the step, and the second product wants
+// of it, for head r, eight positions of the lane's choice, as long as V^T uses
+// the same ones: the weights stay in their lane.  For V^T the lane needs, for
+// each of its d, those eight positions: it loads a piece of head_dim / 16
+// values of each of the eight rows and transposes inside its own registers
+// (byte permutes), d = r * head_dim / 16 + j being the row r of the j-th tile.
+// No operand goes through LDS.
+//
+// The weights exp(s - m) lie in [0, 1]; one BF16 number would add an error as
+// large as the output's own rounding, so they are given as two, high part and
+// remainder.  The matrix unit has time for it: the kernel is bound by reading
+// K and V.
+
+constexpr uint32_t kWaves = 4;
+constexpr uint32_t kStep = 32;
+constexpr uint32_t kMaxChunk = 1024;
+constexpr uint32_t kMinPage = 8, kMaxPage = 1024;
+constexpr uint32_t kHeadTile = 16;
+
+struct AttnParams {
+    Pages k, v;
+    const uint16_t *q;
+    const int32_t *table, *lens, *starts;
+    uint16_t *out;
+    float *lse;
+    float *part;   // [batch * q_heads][splits][head_dim], weighted values over their sum
+    float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
+    uint64_t q_batch, q_head, table_stride, n_pages;
+    uint32_t batch, q_heads, kv_heads, group, tiles, splits, chunk, page_shift, positions;  // positions: table_width * page_size
+    float scale;  // times log2 e
+};
+
+struct Range {
+    uint32_t start, len, base;  // base: start down to a multiple of the step
+};
+
+__device__ __forceinline__ Range range_of(const AttnParams &p, uint32_t b) {
+    Range r;
+    const int32_t len = p.lens[b], start = p.starts ? p.starts[b] : 0;
+    r.len = min(static_cast<uint32_t>(max(len, 0)), p.positions);
+    r.start = min(static_cast<uint32_t>(max(start, 0)), r.len);
+    r.base = r.start & ~(kStep - 1);
+    return r;
+}
+
+// Two BF16 values from two bytes of E4M3 (exact).
+template <bool kHigh>
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh));
+}
+
+__device__ __forceinline__ v4u from_e4m3x8(uint32_t a, uint32_t b) {
+    return v4u{from_e4m3<false>(a), from_e4m3<true>(a), from_e4m3<false>(b), from_e4m3<true>(b)};
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    bf2 v;
+    v.x = static_cast<__bf16>(a);
+    v.y = static_cast<__bf16>(b);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int kDim, bool kE4M3>
+__global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
+    constexpr int kPiece = kDim / 16;              // values of a V row in a lane; tiles of out^T
+    constexpr int kKChunks = kDim / 32;            // matrix instructions over d
+    constexpr int kKLoads = kE4M3 ? kDim / 64 : kKChunks;  // 16-byte loads of a K row in a lane
+    constexpr int kVWords = kPiece * (kE4M3 ? 1 : 2) / 4;  // dwords of a V piece
+    __shared__ int32_t s_page[kMaxChunk / kMinPage + 1];
+    __shared__ float s_stat[kWaves][2][kHeadTile];
+    __shared__ float s_out[kWaves][kHeadTile][kDim + 4];
+
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t split = blockIdx.x % p.splits;
+    uint32_t rest = blockIdx.x / p.splits;
+    const uint32_t tile = rest % p.tiles;
+    rest /= p.tiles;
+    const uint32_t h = rest % p.kv_heads, b = rest / p.kv_heads;
+    const Range range = range_of(p, b);
+    const uint32_t c0 = range.base + split * p.chunk;
+    const uint32_t heads = min(kHeadTile, p.group - tile * kHeadTile);
+    const uint32_t head0 = h * p.group + tile * kHeadTile;
+    const bool single = p.splits == 1;
+    if (c0 >= range.len && !(single && split == 0)) return;
+    const uint32_t c1 = min(c0 + p.chunk, range.len);
+
+    // the chunk's pages; -1 masks
+    const uint32_t first = c0 >> p.page_shift;
+    const uint32_t n_pages = c1 > c0 ? ((c1 - 1) >> p.page_shift) - first + 1 : 0;
+    const int32_t *table = p.table + b * p.table_stride + first;
+    for (uint32_t i = threadIdx.x; i < n_pages; i += 64 * kWaves) {
+        const int32_t e = table[i];
+        s_page[i] = e >= 0 && static_cast<uint64_t>(e) < p.n_pages ? e : -1;
+    }
+
+    // Q^T: head r, d in the order in which K's loads give them
+    const bool have = r < heads;
+    const uint16_t *qp = p.q + b * p.q_batch + (head0 + (have ? r : 0)) * p.q_head;
+    bf8 qf[kKChunks];
+#pragma unroll
+    for (int i = 0; i < kKChunks; ++i) {
+        const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = qp[d + 2 * j] | (uint32_t{qp[d + 2 * j + 1]} << 16);
+        qf[i] = __builtin_bit_cast(bf8, have ? v4u{w[0], w[1], w[2], w[3]} : v4u{0, 0, 0, 0});
+    }
+    const float scale = kE4M3 ? p.scale * p.k.scale[h] : p.scale;
+    const uint8_t *kb = p.k.base + h * p.k.head, *vb = p.v.base + h * p.v.head;
+    const uint32_t in_page = (1u << p.page_shift) - 1;
+    __syncthreads();
+
+    float m = -INFINITY, l = 0;  // m over all lanes of a head, l over this lane's positions
+    f4 acc[kPiece] = {};
+    for (uint32_t p0 = c0 + wave * kStep; p0 < c1; p0 += kWaves * kStep) {
+        // K rows: lane r has position r of each half
+        v4u kr[2][kKLoads];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t pos = min(p0 + 16 * t + r, c1 - 1);
+            const int32_t page = max(s_page[(pos >> p.page_shift) - first], 0);
+            const uint8_t *row = kb + static_cast<uint64_t>(page) * p.k.page + uint64_t{pos & in_page} * p.k.row + 16 * q;
+#pragma unroll
+            for (int i = 0; i < kKLoads; ++i) kr[t][i] = *reinterpret_cast<const v4u *>(row + 64 * i);
+        }
+        // V rows: positions 4 q + 0..3 of each half
+        uint32_t vr[8][kVWords];
+        bool live[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t pos = p0 + 16 * (i / 4) + 4 * q + (i & 3);
+            const uint32_t at = min(pos, c1 - 1);
+            const int32_t page = s_page[(at >> p.page_shift) - first];
+            live[i] = pos >= range.start && pos < c1 && page >= 0;
+            const uint8_t *row = vb + static_cast<uint64_t>(max(page, 0)) * p.v.page + uint64_t{at & in_page} * p.v.row +
+                                 r * (kVWords * 4);
+            if constexpr (kVWords == 1) {
+                vr[i][0] = *reinterpret_cast<const uint32_t *>(row);
+            } else if constexpr (kVWords == 2) {
+                const v2u t = *reinterpret_cast<const v2u *>(row);
+                vr[i][0] = t.x, vr[i][1] = t.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVWords / 4; ++j) {
+                    const v4u t = *reinterpret_cast<const v4u *>(row + 16 * j);
+                    vr[i][4 * j] = t.x, vr[i][4 * j + 1] = t.y, vr[i][4 * j + 2] = t.z, vr[i][4 * j + 3] = t.w;
+                }
+            }
+        }
+        // scores
+        f4 s[2] = {};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < kKChunks; ++i) {
+                v4u kw;
+                if (kE4M3)
+                    kw = i & 1 ? from_e4m3x8(kr[t][i / 2].z, kr[t][i / 2].w) : from_e4m3x8(kr[t][i / 2].x, kr[t][i / 2].y);
+                else
+                    kw = kr[t][kE4M3 ? 0 : i];
+                s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[i], s[t], 0, 0, 0);
+            }
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = live[i] ? s[i / 4][i & 3] * scale : -INFINITY;
+            top = fmaxf(top, x[i]);
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m_new = fmaxf(m, top);
+        const float ref = m_new == -INFINITY ? 0.0f : m_new;  // nothing but masked positions so far
+        const float fade = exp2_(m - ref);
+        m = m_new;
+        float w[8];
+        l *= fade;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = exp2_(x[i] - ref);
+            l += w[i];
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = pack2(w[2 * i], w[2 * i + 1]);
+            lo[i] = pack2(w[2 * i] - __builtin_bit_cast(float, hi[i] << 16),
+                          w[2 * i + 1] - __builtin_bit_cast(float, hi[i] & 0xFFFF0000u));
+        }
+        const bf8 w_hi = __builtin_bit_cast(bf8, v4u{hi[0], hi[1], hi[2], hi[3]});
+        const bf8 w_lo = __builtin_bit_cast(bf8, v4u{lo[0], lo[1], lo[2], lo[3]});
+        // a masked row may hold anything, and 0 times NaN is NaN
+        const bool all = live[0] && live[1] && live[2] && live[3] && live[4] && live[5] && live[6] && live[7];
+        if (!__all(all)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < kVWords; ++j) vr[i][j] = live[i] ? vr[i][j] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < kPiece; j += 2) {
+            // values j and j + 1 of the eight rows
+            uint32_t pair[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (kE4M3)
+                    pair[i] = j & 2 ? from_e4m3<true>(vr[i][j / 4]) : from_e4m3<false>(vr[i][j / 4]);
+                else
+                    pair[i] = vr[i][kE4M3 ? 0 : j / 2];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+                const bf8 a = __builtin_bit_cast(
+                    bf8, v4u{__builtin_amdgcn_perm(pair[1], pair[0], sel), __builtin_amdgcn_perm(pair[3], pair[2], sel),
+                             __builtin_amdgcn_perm(pair[5], pair[4], sel), __builtin_amdgcn_perm(pair[7], pair[6], sel)});
+                f4 o = acc[j + e];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] *= fade;
+                o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w_hi, o, 0, 0, 0);
+                acc[j + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w_lo, o, 0, 0, 0);
+            }
+        }
+    }
+
+    // join the waves
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (q == 0) {
+        s_stat[wave][0][r] = m;
+        s_stat[wave][1][r] = l;
+    }
+    // acc[j][c]: d = (4 q + c) * kPiece + j
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) s_out[wave][r][(4 * q + c) * kPiece + j] = acc[j][c];
+    __syncthreads();
+    const float v_scale = kE4M3 ? p.v.scale[h] : 1.0f;
+    for (uint32_t i = threadIdx.x; i < heads * kDim; i += 64 * kWaves) {
+        const uint32_t g = i / kDim, d = i % kDim;
+        float top = -INFINITY;
+#pragma unroll
+        for (uint32_t k = 0; k < kWaves; ++k) top = fmaxf(top, s_stat[k][0][g]);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float sum = 0, o = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kWaves; ++k) {
+            const float f = exp2_(s_stat[k][0][g] - ref);
+            sum += s_stat[k][1][g] * f;
+            o += s_out[k][g][d] * f;
+        }
+        o *= v_scale;
+        const uint64_t row = uint64_t{b} * p.q_heads + head0 + g;
+        if (single) {
+            p.out[row * kDim + d] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum == 0 ? 0.0f : o / sum));
+            if (d == 0 && p.lse) p.lse[row] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        } else {
+            const uint64_t at = row * p.splits + split;
+            p.part[at * kDim + d] = o;
+            if (d == 0) {
+                p.stats[2 * at] = top;
+                p.stats[2 * at + 1] = sum;
+            }
+        }
+    }
+}
+
+// One workgroup joins the chunks of one query head.
+template <int kDim>
+__global__ void __launch_bounds__(kDim) join_kernel(AttnParams p) {
+    const uint64_t row = blockIdx.x;
+    const uint32_t b = static_cast<uint32_t>(row / p.q_heads);
+    const Range range = range_of(p, b);
+    const uint32_t n = (range.len - range.base + p.chunk - 1) / p.chunk;
+    const float *stats = p.stats + 2 * row * p.splits;
+    const float *part = p.part + row * p.splits * kDim + threadIdx.x;
+    const uint32_t used = range.len > range.start ? n : 0;
+    float top = -INFINITY;
+    for (uint32_t i = 0; i < used; ++i) top = fmaxf(top, stats[2 * i]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0, o = 0;
+    for (uint32_t i = 0; i < used; ++i) {
+        const float f = exp2_(stats[2 * i] - ref);
+        sum += stats[2 * i + 1] * f;
+        o += part[uint64_t{i} * kDim] * f;
+    }
+    p.out[row * kDim + threadIdx.x] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum == 0 ? 0.0f : o / sum));
+    if (threadIdx.x == 0 && p.lse) p.lse[row] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// ---- Host ------------------------------------------------------------------
+
+template <class T>
+struct Plain {
+    typedef T type;
+};
+
+template <class... A>
+hipError_t launch(void (*fn)(A...), uint32_t grid, uint32_t threads, hipStream_t st, typename Plain<A>::type... a) {
+    void *args[] = {&a...};
+    return hipLaunchKernel(reinterpret_cast<const void *>(fn), dim3(grid), dim3(threads), args, 0, st);
+}
+
+df11_status launched(hipError_t err) {
+    if (err == hipSuccess) return DF11_OK;
+    df11i::last_hip_error = static_cast<int32_t>(err);
+    return DF11_E_HIP;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool dim_ok(uint32_t d) { return d == 64 || d == 128 || d == 256; }
+
+bool page_ok(uint32_t n) { return n >= kMinPage && n <= kMaxPage && (n & (n - 1)) == 0; }
+
+constexpr uint64_t kMaxStride = uint64_t{1} << 40;  // elements; with the limits on counts no address overflows
+
+df11_status check_cache(const df11_paged_cache *c) {
+    if (!c) return DF11_E_INVALID_ARG;
+    if (c->dtype > DF11_CACHE_E4M3 || !dim_ok(c->head_dim) || !page_ok(c->page_size)) return DF11_E_UNSUPPORTED;
+    if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return DF11_E_INVALID_ARG;
+    if (c->kv_heads == 0 || c->kv_heads > 65536 || c->n_pages == 0 || c->n_pages > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
+    const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
+    const uint64_t unit = e4m3 ? 16 : 8;  // elements in 16 bytes
+    for (uint64_t s : {c->k_page_stride, c->k_head_stride, c->k_row_stride, c->v_page_stride, c->v_head_stride, c->v_row_stride})
+        if (s % unit != 0 || s > kMaxStride) return DF11_E_INVALID_ARG;
+    if (e4m3 && (!c->k_scale || !c->v_scale)) return DF11_E_INVALID_ARG;
+    return DF11_OK;
+}
+
+uint32_t log2_of(uint32_t v) { return 31u - static_cast<uint32_t>(__builtin_clz(v)); }
+
+Pages k_of(const df11_paged_cache *c) {
+    const uint64_t e = c->dtype == DF11_CACHE_E4M3 ? 1 : 2;
+    return Pages{static_cast<uint8_t *>(c->k_pages), c->k_page_stride * e, c->k_head_stride * e, c->k_row_stride * e, c->k_scale};
+}
+
+Pages v_of(const df11_paged_cache *c) {
+    const uint64_t e = c->dtype == DF11_CACHE_E4M3 ? 1 : 2;
+    return Pages{static_cast<uint8_t *>(c->v_pages), c->v_page_stride * e, c->v_head_stride * e, c->v_row_stride * e, c->v_scale};
+}
+
+df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_token, uint64_t k_head, const uint16_t *v,
+                   uint64_t v_token, uint64_t v_head, const int64_t *slots, uint64_t tokens, void *hip_stream) {
+    const df11_status rc = check_cache(c);
+    if (rc != DF11_OK) return rc;
+    if (tokens == 0) return DF11_OK;
+    if (!k || !v || !slots || tokens > 0x7FFFFFFFu || (reinterpret_cast<uintptr_t>(slots) & 7u) ||
+        ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 1u))
+        return DF11_E_INVALID_ARG;
+    for (uint64_t s : {k_token, k_head, v_token, v_head})
+        if (s > kMaxStride) return DF11_E_INVALID_ARG;
+    AppendParams p;
+    p.k = k_of(c);
+    p.v = v_of(c);
+    p.ks = k;
+    p.vs = v;
+    p.k_token = k_token;
+    p.k_head = k_head;
+    p.v_token = v_token;
+    p.v_head = v_head;
+    p.slots = slots;
+    p.kv_heads = c->kv_heads;
+    p.dim_shift = log2_of(c->head_dim / 8);
+    p.page_shift = log2_of(c->page_size);
+    p.n_slots = c->n_pages * c->page_size;
+    p.lanes = (tokens * c->kv_heads) << p.dim_shift;
+    const bool al = aligned16(k) && aligned16(v) && (k_token | k_head | v_token | v_head) % 8 == 0;
+    const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
+    auto fn = e4m3 ? (al ? append_kernel<true, true> : append_kernel<true, false>)
+                   : (al ? append_kernel<false, true> : append_kernel<false, false>);
+    const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((p.lanes + 255) / 256, 1u << 20));
+    return launched(launch(fn, grid, 256, static_cast<hipStream_t>(hip_stream), p));
+}
+
+struct Split {
+    uint32_t chunk, splits;
+};
+
+// Chunks that give every compute unit several workgroups, where there are
+// positions enough.  The page table's width bounds the lengths, which only
+// the device knows.
+Split split_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions) {
+    Split s;
+    s.chunk = 256;
+    while (s.chunk < kMaxChunk && batch * kv_heads * tiles * ((positions + s.chunk - 1) / s.chunk) > 4096) s.chunk *= 2;
+    s.splits = static_cast<uint32_t>((positions + s.chunk - 1) / s.chunk);
+    s.splits = std::max(s.splits, 1u);
+    return s;
+}
+
+uint64_t attention_workspace(uint64_t rows, uint32_t head_dim, uint32_t splits) {
+    return splits <= 1 ? 0 : rows * splits * (head_dim + 2) * sizeof(float);
+}
+
+bool attention_sizes_ok(uint64_t batch, uint64_t q_heads, uint32_t kv_heads, uint32_t page_size, uint64_t width) {
+    return batch <= (1u << 24) && kv_heads > 0 && q_heads > 0 && q_heads <= (1u << 20) && q_heads % kv_heads == 0 &&
+           width > 0 && width <= 0x7FFFFFFFu / page_size;
+}
+
+df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t batch, uint64_t q_heads, uint64_t q_batch,
+                      uint64_t q_head, const int32_t *table, uint64_t table_stride, uint64_t width, const int32_t *lens,
+                      const int32_t *starts, float scale, uint16_t *out, float *lse, void *workspace,
+                      uint64_t workspace_bytes, void *hip_stream) {
+    const df11_status rc = check_cache(c);
+    if (rc != DF11_OK) return rc;
+    if (!attention_sizes_ok(batch, q_heads, c->kv_heads, c->page_size, width) || table_stride < width ||
+        table_stride > kMaxStride || q_batch > kMaxStride || q_head > kMaxStride)
+        return DF11_E_INVALID_ARG;
+    if (batch == 0) return DF11_OK;
+    if (!q || !table || !lens || !out || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 1u) ||
+        ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(starts) |
+          reinterpret_cast<uintptr_t>(lse)) & 3u) ||
+        !aligned16(workspace))
+        return DF11_E_INVALID_ARG;
+    AttnParams p;
+    p.k = k_of(c);
+    p.v = v_of(c);
+    p.q = q;
+    p.table = table;
+    p.lens = lens;
+    p.starts = starts;
+    p.out = out;
+    p.lse = lse;
+    p.q_batch = q_batch;
+    p.q_head = q_head;
+    p.table_stride = table_stride;
+    p.n_pages = c->n_pages;
+    p.batch = static_cast<uint32_t>(batch);
+    p.q_heads = static_cast<uint32_t>(q_heads);
+    p.kv_heads = c->kv_heads;
+    p.group = p.q_heads / p.kv_heads;
+    p.tiles = (p.group + kHeadTile - 1) / kHeadTile;
+    p.page_shift = log2_of(c->page_size);
+    p.positions = static_cast<uint32_t>(width * c->page_size);
+    p.scale = scale * kLog2e;
+    const Split s = split_of(batch, p.kv_heads, p.tiles, p.positions);
+    p.chunk = s.chunk;
+    p.splits = s.splits;
+    const uint64_t rows = batch * q_heads;
+    if (workspace_bytes < attention_workspace(rows, c->head_dim, p.splits)) return DF11_E_BUFFER_TOO_SMALL;
+    if (p.splits > 1 && !workspace) return DF11_E_INVALID_ARG;
+    p.part = static_cast<float *>(workspace);
+    p.stats = p.part + (p.splits > 1 ? rows * p.splits * c->head_dim : 0);
+    const uint64_t groups = batch * p.kv_heads * p.tiles * p.splits;
+    if (groups > 0x7FFFFFFFu || rows > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
+    const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
+    hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    auto fn = attend_kernel<128, false>;
+    switch (c->head_dim) {
+        case 64: fn = e4m3 ? attend_kernel<64, true> : attend_kernel<64, false>; break;
+        case 128: fn = e4m3 ? attend_kernel<128, true> : attend_kernel<128, false>; break;
+        default: fn = e4m3 ? attend_kernel<256, true> : attend_kernel<256, false>; break;
+    }
+    hipError_t err = launch(fn, static_cast<uint32_t>(groups), 64 * kWaves, st, p);
+    if (err == hipSuccess && p.splits > 1)
+        err = launch(c->head_dim == 64    ? join_kernel<64>
+                     : c->head_dim == 128 ? join_kernel<128>
+                                          : join_kernel<256>,
+                     static_cast<uint32_t>(rows), c->head_dim, st, p);
+    return launched(err);
+}
+
+}  // namespace
+
+extern "C" df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, uint64_t k_token_stride,
+                                         uint64_t k_head_stride, const uint16_t *v, uint64_t v_token_stride,
+                                         uint64_t v_head_stride, const int64_t *slots, uint64_t tokens,
+                                         void *hip_stream) {
+    return df11i::guarded([&] {
+        return append(cache, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots, tokens, hip_stream);
+    });
+}
+
+extern "C" uint64_t df11_paged_attention_workspace_bytes(uint64_t batch, uint64_t q_heads, uint32_t kv_heads,
+                                                         uint32_t head_dim, uint32_t page_size, uint64_t table_width) {
+    if (!page_ok(page_size) || !attention_sizes_ok(batch, q_heads, kv_heads, page_size, table_width)) return 0;
+    const uint32_t group = static_cast<uint32_t>(q_heads / kv_heads);
+    const Split s = split_of(batch, kv_heads, (group + kHeadTile - 1) / kHeadTile, table_width * page_size);
+    return attention_workspace(batch * q_heads, head_dim, s.splits);
+}
+
+extern "C" df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch,
+                                            uint64_t q_heads, uint64_t q_batch_stride, uint64_t q_head_stride,
+                                            const int32_t *page_table, uint64_t table_stride, uint64_t table_width,
+                                            const int32_t *lens, const int32_t *starts, float scale, uint16_t *out,
+                                            float *lse, void *workspace, uint64_t workspace_bytes, void *hip_stream) {
+    return df11i::guarded([&] {
+        return attention(cache, q, batch, q_heads, q_batch_stride, q_head_stride, page_table, table_stride, table_width,
+                         lens, starts, scale, out, lse, workspace, workspace_bytes, hip_stream);
+    });
+}

@@ -1,0 +1,280 @@
+"""GPU checks of the 4-bit weights: codes and scales against the definition in
+64 bits (exact, every BF16 pattern), their values (exact, every code under
+every scale), and the product against 64-bit sums.
+
+Bound of the product, for the result y of k exact products summed in 32 bits
+in some order and rounded to BF16 once (8 significant bits: off by at most half
+of 2^-7 of the value): |y - ref| <= 2^-8 |ref| + (1 + 2^-8) k 2^-23 sum |x w| (an
+addition is off by at most 2^-23 of a partial sum, rounding or truncating, and
+no partial sum exceeds sum |x w|).
+"""
+import numpy as np
+import pytest
+
+import huffman_decode_block_amd as hdb
+
+pytestmark = pytest.mark.gpu
+
+GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=np.float64)
+
+
+def say(msg):
+    print(f"[gpu-test] {msg}", flush=True)
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as t
+    assert t.cuda.is_available(), "the GPU tests need a GPU"
+    return t
+
+
+def bf16_values(bits):
+    return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def to_bf16(v):
+    """Nearest BF16 (ties to even) of 64-bit values, as 64-bit values."""
+    v = np.asarray(v, dtype=np.float64)
+    f = v.astype(np.float32)  # exact for what is passed here: at most 24 bits above 2^-149
+    b = f.view(np.uint32).astype(np.uint64)
+    b = (b + 0x7FFF + ((b >> 16) & 1)) >> 16
+    return (b.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def quantise(bits):
+    """Codes and scale bytes of BF16 bit patterns [rows, cols], from the definition."""
+    rows, cols = bits.shape
+    blocks = -(-cols // 32)
+    full = np.zeros((rows, 32 * blocks), dtype=np.uint16)
+    full[:, :cols] = bits
+    full = full.reshape(rows, blocks, 32)
+    v = bf16_values(full)
+    bad = ~np.isfinite(v).all(-1)
+    v = np.where(bad[..., None], 0.0, v)
+    top = np.abs(v).max(-1)
+    e = np.frexp(np.where(top > 0, top, 1.0))[1] - 1 - 2
+    e = np.where(top > 0, np.clip(e, -127, 127), -127)
+    m = np.minimum(np.ldexp(np.abs(v), -e[..., None]), 6.0)
+    lo = np.searchsorted(GRID, m, side="right") - 1
+    hi = np.minimum(lo + 1, 7)
+    mid = (GRID[lo] + GRID[hi]) / 2
+    code = np.where((m > mid) | ((m == mid) & (hi % 2 == 0)), hi, lo)
+    code = code + 8 * (full >> 15)
+    code = np.where(bad[..., None], 0, code).astype(np.uint8).reshape(rows, 16 * blocks, 2)
+    return code[..., 0] | (code[..., 1] << 4), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def values(codes, scales, cols):
+    rows, blocks = scales.shape
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(rows, blocks, 32)
+    v = GRID[c & 7] * np.where(c >= 8, -1.0, 1.0)
+    v = np.ldexp(v, scales.astype(np.int64)[..., None] - 127)
+    v = np.where(scales[..., None] == 255, np.nan, v)
+    return v.reshape(rows, 32 * blocks)[:, :cols]
+
+
+def on_gpu(torch, bits, pad=0, offset=0):
+    """Device BF16 matrix of the bit patterns, `pad` NaNs behind every row, the first row `offset` values into its storage."""
+    rows, cols = bits.shape
+    flat = torch.full((offset + rows * (cols + pad),), 0x7FC1, dtype=torch.int16, device="cuda")
+    x = flat[offset:].view(rows, cols + pad)[:, :cols]
+    x.copy_(torch.from_numpy(bits.view(np.int16)))
+    return x.view(torch.bfloat16)
+
+
+def check_quantise(torch, bits, pad=0, offset=0):
+    codes, scales = hdb.df11_mx4_quantize(on_gpu(torch, bits, pad, offset))
+    want_c, want_s = quantise(bits)
+    assert np.array_equal(scales.cpu().numpy(), want_s)
+    assert np.array_equal(codes.cpu().numpy(), want_c)
+    got = hdb.df11_mx4_dequantize(codes, scales, bits.shape[1]).float().cpu().numpy().astype(np.float64)
+    assert np.array_equal(got, to_bf16(values(want_c, want_s, bits.shape[1])), equal_nan=True)
+
+
+@pytest.mark.parametrize("order", ["sorted", "shuffled", "finite shuffled"])
+def test_quantise_every_bf16_pattern(torch, order):
+    say(f"quantise all patterns, {order}")
+    bits = np.arange(65536, dtype=np.uint16)
+    if order != "sorted":
+        bits = np.random.default_rng(5).permutation(bits)
+    if order == "finite shuffled":
+        bits = np.where((bits & 0x7F80) == 0x7F80, 0x3F80, bits).astype(np.uint16)
+    check_quantise(torch, bits.reshape(512, 128))
+
+
+@pytest.mark.parametrize("rows,cols,pad,offset", [
+    (1, 1, 0, 0), (1, 32, 0, 0), (3, 31, 0, 0), (5, 33, 7, 1), (2, 64, 8, 8), (7, 1000, 0, 0), (129, 257, 3, 4),
+    (66, 96, 0, 1), (4, 8200, 8, 0), (1000, 1, 0, 0), (3, 40, 0, 0),
+])
+def test_quantise_shapes(torch, rows, cols, pad, offset):
+    say(f"quantise {rows}x{cols} pad {pad} offset {offset}")
+    rng = np.random.default_rng(rows * 10007 + cols)
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-20, 20, (rows, 1)))
+    bits = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    bits[rng.random((rows, cols)) < 0.1] = 0x8000  # minus zero
+    if rows > 4:
+        bits[2] = 0
+        bits[3, cols // 2] = 0x7F80
+        bits[4, 0] = 0xFFC0
+    check_quantise(torch, bits, pad, offset)
+
+
+def test_values_of_every_code_and_scale(torch):
+    say("dequantise every code and scale")
+    codes = np.tile((np.arange(16) | (np.arange(16)[::-1] << 4)).astype(np.uint8), (256, 1))
+    scales = np.arange(256, dtype=np.uint8).reshape(256, 1)
+    got = hdb.df11_mx4_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 32)
+    want = to_bf16(np.where(np.isnan(values(codes, scales, 32)), np.nan,
+                            np.clip(values(codes, scales, 32), -3.5e38, 3.5e38)))
+    big = np.abs(values(codes, scales, 32)) > 3.3961775292304e38  # past BF16's largest: an infinity
+    want = np.where(big, np.sign(values(codes, scales, 32)) * np.inf, want)
+    assert np.array_equal(got.float().cpu().numpy().astype(np.float64), want, equal_nan=True)
+
+
+def test_dequantise_into_strided_rows(torch):
+    rng = np.random.default_rng(3)
+    for cols, pad, offset in ((70, 3, 1), (64, 8, 8), (33, 0, 0)):
+        say(f"dequantise into rows of {cols}, pad {pad}")
+        codes = rng.integers(0, 256, (9, 16 * -(-cols // 32))).astype(np.uint8)
+        scales = rng.integers(100, 140, (9, -(-cols // 32))).astype(np.uint8)
+        flat = torch.full((offset + 9 * (cols + pad),), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[offset:].view(9, cols + pad)
+        hdb.df11_mx4_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), cols, out=out[:, :cols])
+        assert np.array_equal(out[:, :cols].float().cpu().numpy(), values(codes, scales, cols))
+        assert bool((out[:, cols:] == 7).all()) and bool((flat[:offset] == 7).all())
+
+
+def product_inputs(torch, m, n, k, pad=0, offset=0, seed=0):
+    rng = np.random.default_rng([m, n, k, seed])
+    x = rng.standard_normal((m, k)) * np.exp2(rng.integers(-3, 4, (m, 1)))
+    xb = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    blocks = -(-k // 32)
+    codes = rng.integers(0, 256, (n, 16 * blocks)).astype(np.uint8)
+    nib = np.stack([codes & 15, codes >> 4], -1).reshape(n, 32 * blocks)
+    nib[:, k:] = 0  # as the quantiser leaves what lies past k
+    nib = nib.reshape(n, 16 * blocks, 2)
+    codes = (nib[..., 0] | (nib[..., 1] << 4)).astype(np.uint8)
+    scales = rng.integers(110, 130, (n, blocks)).astype(np.uint8)
+    return xb, codes, scales, on_gpu(torch, xb, pad, offset), torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+
+
+def product_bound(xb, codes, scales):
+    x, w = bf16_values(xb), values(codes, scales, xb.shape[1])
+    ref = x @ w.T
+    return ref, 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * xb.shape[1] * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+
+
+SHAPES = [
+    (1, 1, 1), (1, 16, 32), (1, 4096, 4096), (2, 17, 31), (3, 100, 33), (15, 64, 100), (16, 130, 128), (17, 129, 96),
+    (31, 33, 1000), (33, 257, 512), (64, 64, 64), (65, 1000, 160), (77, 257, 199), (128, 128, 128), (129, 130, 320),
+    (200, 72, 2048), (256, 256, 256), (257, 511, 65), (300, 1024, 1024), (513, 260, 288), (1, 300, 14336),
+    (1024, 512, 544), (2, 128300, 64), (5, 8, 8192), (48, 2048, 4096), (700, 640, 32),
+]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_product_against_64_bits(torch, m, n, k):
+    say(f"product {m}x{n}x{k}")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k)
+    ref, bound = product_bound(xb, codes, scales)
+    y = hdb.df11_mx4_matmul(x, c, s)
+    assert (np.abs(y.float().cpu().numpy() - ref) <= bound).all()
+    assert torch.equal(y, hdb.df11_mx4_matmul(x, c, s)), "a second call differs"
+
+
+@pytest.mark.parametrize("m,n,k,pad,offset", [
+    (1, 96, 128, 0, 1), (4, 96, 128, 8, 8), (19, 50, 256, 3, 2), (90, 200, 96, 5, 0), (150, 129, 100, 0, 4), (260, 140, 64, 8, 3),
+])
+def test_product_of_strided_rows(torch, m, n, k, pad, offset):
+    """What lies between the rows of x is NaN; the rows of y are strided too."""
+    say(f"product {m}x{n}x{k} pad {pad} offset {offset}")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k, pad, offset)
+    ref, bound = product_bound(xb, codes, scales)
+    flat = torch.full((m, n + 5), 9.0, dtype=torch.bfloat16, device="cuda")
+    y = hdb.df11_mx4_matmul(x, c, s, out=flat[:, 2:2 + n])
+    assert (np.abs(y.float().cpu().numpy() - ref) <= bound).all()
+    assert bool((flat[:, :2] == 9).all()) and bool((flat[:, 2 + n:] == 9).all())
+
+
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_product_keeps_nan_and_infinity_in_their_rows(torch, m):
+    say(f"product with NaN, {m} rows")
+    n, k = 150, 320
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k)
+    scales[7, 3] = 255
+    s[7, 3] = 255
+    if m > 2:
+        xb[1, 5], xb[2, 9] = 0x7FC0, 0x7F80
+        x[1, 5], x[2, 9] = float("nan"), float("inf")
+        codes[:, 4] |= 0x60  # column 9 of no row is zero
+        c |= 0
+        c[:, 4] |= 0x60
+    with np.errstate(invalid="ignore"):
+        ref, bound = product_bound(xb, codes, scales)
+    got = hdb.df11_mx4_matmul(x, c, s).float().cpu().numpy()
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)])
+    assert (np.abs(got - ref)[fine] <= bound[fine]).all()
+
+
+def test_empty_products(torch):
+    say("empty products")
+    _, _, _, x, c, s = product_inputs(torch, 3, 40, 64)
+    assert hdb.df11_mx4_matmul(x[:0], c, s).shape == (0, 40)
+    assert hdb.df11_mx4_matmul(x, c[:0], s[:0]).shape == (3, 0)
+    y = hdb.df11_mx4_matmul(x[:, :0], c[:, :0].contiguous(), s[:, :0].contiguous())
+    assert y.shape == (3, 40) and bool((y == 0).all())
+    codes, scales = hdb.df11_mx4_quantize(x[:0])
+    assert codes.shape == (0, 32) and scales.shape == (0, 2)
+    assert hdb.df11_mx4_dequantize(codes, scales, 64).shape == (0, 64)
+
+
+@pytest.mark.parametrize("m,k", [(2, 512), (90, 333), (400, 512)])
+def test_product_on_another_stream_and_in_a_graph(torch, m, k):
+    say(f"product {m} rows on a side stream and in a graph")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, 500, k)
+    want = hdb.df11_mx4_matmul(x, c, s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = hdb.df11_mx4_matmul(x, c, s, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    got = hdb.df11_mx4_matmul(x, c, s, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hdb.df11_mx4_matmul(x, c, s, out=out)
+    for _ in range(4):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, hdb.df11_mx4_matmul(x, c, s))
+
+
+def test_refusals(torch):
+    say("refusals")
+    _, _, _, x, c, s = product_inputs(torch, 3, 40, 64)
+    with pytest.raises(TypeError):
+        hdb.df11_mx4_matmul(x.float(), c, s)
+    with pytest.raises(TypeError):
+        hdb.df11_mx4_matmul(x.cpu(), c, s)
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_matmul(x[:, :32], c, s)
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_matmul(x.T, c, s)
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_matmul(x, c, s[:-1])
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_matmul(x, c, s, out=torch.empty(3, 41, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_quantize(x[:, :0])
+    with pytest.raises(ValueError):
+        hdb.df11_mx4_dequantize(c, s, 65)
+    with pytest.raises(hdb.DF11Error) as e:
+        hdb.df11_mx4_matmul(x[:, 1:], *hdb.df11_mx4_quantize(x[:, 1:]),
+                            workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == hdb.DF11_E_BUFFER_TOO_SMALL

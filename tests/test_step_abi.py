@@ -1,0 +1,143 @@
+"""The C-ABI of include/df11_step.h: exported symbols, the binding's names and
+what the host-side checks refuse.  No GPU work is started here; the pointers
+handed in are never followed."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import huffman_decode_block_amd as hdb
+from conftest import ROOT
+
+P = 1 << 20  # an aligned address that only the host-side checks see
+
+
+def declared_functions():
+    src = open(os.path.join(ROOT, "include", "df11_step.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    return sorted(set(re.findall(r"\b(df11_[a-z0-9_]+)\s*\(", src)))
+
+
+def test_every_declared_symbol_is_exported_and_bound():
+    names = declared_functions()
+    lib = ctypes.CDLL(hdb.LIB_PATH)
+    for n in names:
+        assert hasattr(lib, n), n
+        assert callable(getattr(hdb, n)), n
+        assert n in hdb.__all__, n
+    assert sorted(hdb.STEP_EXPORTS) == names
+
+
+@pytest.mark.parametrize("change", [
+    dict(x=None), dict(x=P + 1), dict(codes=None), dict(codes=P + 8), dict(scales=None), dict(cols=0),
+    dict(cols=(1 << 24) + 1, stride=(1 << 24) + 1), dict(stride=63), dict(rows=1 << 60), dict(rows=3, stride=1 << 62),
+])
+def test_quantise_refusals(change):
+    a = dict(x=P, rows=2, cols=64, stride=64, codes=P, scales=P)
+    a.update(change)
+    L = hdb.lib()
+    assert L.df11_mx4_quantize(a["x"], a["rows"], a["cols"], a["stride"], a["codes"], a["scales"], None) == \
+        hdb.DF11_E_INVALID_ARG
+    assert L.df11_mx4_dequantize(a["codes"], a["scales"], a["rows"], a["cols"], a["x"], a["stride"], None) == \
+        hdb.DF11_E_INVALID_ARG
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), hdb.DF11_E_INVALID_ARG), (dict(x=P + 1), hdb.DF11_E_INVALID_ARG),
+    (dict(y=None), hdb.DF11_E_INVALID_ARG), (dict(y=P + 1), hdb.DF11_E_INVALID_ARG),
+    (dict(codes=P + 4), hdb.DF11_E_INVALID_ARG), (dict(scales=None), hdb.DF11_E_INVALID_ARG),
+    (dict(xs=63), hdb.DF11_E_INVALID_ARG), (dict(ys=39), hdb.DF11_E_INVALID_ARG),
+    (dict(m=1 << 31), hdb.DF11_E_INVALID_ARG), (dict(n=1 << 31, ys=1 << 31), hdb.DF11_E_INVALID_ARG),
+    (dict(k=(1 << 24) + 1, xs=1 << 25), hdb.DF11_E_INVALID_ARG), (dict(xs=1 << 25), hdb.DF11_E_INVALID_ARG),
+    (dict(k=63), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(x=P + 2), hdb.DF11_E_BUFFER_TOO_SMALL),
+    (dict(xs=65), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(k=63, ws=P + 8, size=1 << 20), hdb.DF11_E_INVALID_ARG),
+    (dict(k=63, ws=None, size=1 << 20), hdb.DF11_E_INVALID_ARG),
+])
+def test_product_refusals(change, status):
+    a = dict(x=P, m=3, k=64, xs=64, codes=P, scales=P, n=40, y=P, ys=40, ws=None, size=0)
+    a.update(change)
+    got = hdb.lib().df11_mx4_matmul(a["x"], a["m"], a["k"], a["xs"], a["codes"], a["scales"], a["n"], a["y"], a["ys"],
+                                    a["ws"], a["size"], None)
+    assert got == status
+
+
+def test_empty_calls_need_no_pointers():
+    L = hdb.lib()
+    assert L.df11_mx4_quantize(None, 0, 64, 64, None, None, None) == hdb.DF11_OK
+    assert L.df11_mx4_dequantize(None, None, 0, 64, None, 64, None) == hdb.DF11_OK
+    assert L.df11_mx4_matmul(None, 0, 64, 64, None, None, 40, None, 40, None, 0, None) == hdb.DF11_OK
+    assert L.df11_mx4_matmul(None, 3, 64, 64, None, None, 0, None, 0, None, 0, None) == hdb.DF11_OK
+    c = cache()
+    assert L.df11_paged_append(ctypes.byref(c), None, 0, 0, None, 0, 0, None, 0, None) == hdb.DF11_OK
+    assert L.df11_paged_attention(ctypes.byref(c), None, 0, 8, 0, 0, None, 4, 4, None, None, 1.0, None, None, None, 0,
+                                  None) == hdb.DF11_OK
+
+
+def cache(**change):
+    a = dict(k_pages=P, v_pages=P, n_pages=10, k_page_stride=16384, k_head_stride=2048, k_row_stride=128,
+             v_page_stride=16384, v_head_stride=2048, v_row_stride=128, k_scale=None, v_scale=None, kv_heads=8,
+             head_dim=128, page_size=16, dtype=hdb.DF11_CACHE_BF16)
+    a.update(change)
+    return hdb.step.df11_paged_cache(**a)
+
+
+BAD_CACHES = [
+    (dict(k_pages=None), hdb.DF11_E_INVALID_ARG), (dict(v_pages=P + 2), hdb.DF11_E_INVALID_ARG),
+    (dict(n_pages=0), hdb.DF11_E_INVALID_ARG), (dict(n_pages=1 << 31), hdb.DF11_E_INVALID_ARG),
+    (dict(kv_heads=0), hdb.DF11_E_INVALID_ARG), (dict(k_row_stride=129), hdb.DF11_E_INVALID_ARG),
+    (dict(v_head_stride=1 << 41), hdb.DF11_E_INVALID_ARG), (dict(head_dim=96), hdb.DF11_E_UNSUPPORTED),
+    (dict(head_dim=0), hdb.DF11_E_UNSUPPORTED), (dict(page_size=4), hdb.DF11_E_UNSUPPORTED),
+    (dict(page_size=24), hdb.DF11_E_UNSUPPORTED), (dict(page_size=2048), hdb.DF11_E_UNSUPPORTED),
+    (dict(dtype=2), hdb.DF11_E_UNSUPPORTED), (dict(dtype=hdb.DF11_CACHE_E4M3), hdb.DF11_E_INVALID_ARG),
+    (dict(dtype=hdb.DF11_CACHE_E4M3, k_scale=P, v_scale=P, k_row_stride=136), hdb.DF11_E_INVALID_ARG),
+]
+
+
+@pytest.mark.parametrize("change,status", BAD_CACHES)
+def test_cache_refusals(change, status):
+    L = hdb.lib()
+    c = ctypes.byref(cache(**change))
+    assert L.df11_paged_append(c, P, 1024, 128, P, 1024, 128, P, 1, None) == status
+    assert L.df11_paged_attention(c, P, 1, 8, 1024, 128, P, 4, 4, P, None, 1.0, P, P, None, 0, None) == status
+
+
+@pytest.mark.parametrize("change", [dict(k=None), dict(v=P + 1), dict(slots=None), dict(slots=P + 4), dict(tokens=1 << 31),
+                                    dict(stride=1 << 41)])
+def test_append_refusals(change):
+    a = dict(k=P, v=P, slots=P, tokens=2, stride=1024)
+    a.update(change)
+    c = cache()
+    assert hdb.lib().df11_paged_append(ctypes.byref(c), a["k"], a["stride"], 128, a["v"], a["stride"], 128, a["slots"],
+                                       a["tokens"], None) == hdb.DF11_E_INVALID_ARG
+    assert hdb.lib().df11_paged_append(None, P, 0, 0, P, 0, 0, P, 1, None) == hdb.DF11_E_INVALID_ARG
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), hdb.DF11_E_INVALID_ARG), (dict(out=None), hdb.DF11_E_INVALID_ARG), (dict(table=None), hdb.DF11_E_INVALID_ARG),
+    (dict(lens=None), hdb.DF11_E_INVALID_ARG), (dict(lens=P + 2), hdb.DF11_E_INVALID_ARG), (dict(starts=P + 1), hdb.DF11_E_INVALID_ARG),
+    (dict(lse=P + 2), hdb.DF11_E_INVALID_ARG), (dict(heads=12), hdb.DF11_E_INVALID_ARG), (dict(heads=0), hdb.DF11_E_INVALID_ARG),
+    (dict(width=0), hdb.DF11_E_INVALID_ARG), (dict(ts=3), hdb.DF11_E_INVALID_ARG), (dict(width=1 << 28, ts=1 << 28), hdb.DF11_E_INVALID_ARG),
+    (dict(batch=1 << 25), hdb.DF11_E_INVALID_ARG), (dict(width=4096, ts=4096), hdb.DF11_E_BUFFER_TOO_SMALL),
+    (dict(width=4096, ts=4096, ws=P + 4, size=1 << 40), hdb.DF11_E_INVALID_ARG),
+    (dict(width=4096, ts=4096, ws=None, size=1 << 40), hdb.DF11_E_INVALID_ARG),
+])
+def test_attention_refusals(change, status):
+    a = dict(q=P, batch=2, heads=32, table=P, ts=4, width=4, lens=P, starts=None, out=P, lse=None, ws=None, size=0)
+    a.update(change)
+    c = cache()
+    got = hdb.lib().df11_paged_attention(ctypes.byref(c), a["q"], a["batch"], a["heads"], 4096, 128, a["table"], a["ts"],
+                                         a["width"], a["lens"], a["starts"], 1.0, a["out"], a["lse"], a["ws"], a["size"],
+                                         None)
+    assert got == status
+
+
+def test_workspace_sizes():
+    assert hdb.df11_mx4_matmul_workspace_bytes(1, 4096, 4096) == 0
+    assert hdb.df11_mx4_matmul_workspace_bytes(3, 40, 63) >= 3 * 64 * 2
+    assert hdb.df11_mx4_matmul_workspace_bytes(3, 40, 64, False) >= 3 * 64 * 2
+    assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 16, 4) == 0
+    assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 16, 4096) >= 32 * 130 * 4
+    # calls that the operators refuse need none
+    assert hdb.df11_paged_attention_workspace_bytes(1, 33, 8, 128, 16, 4096) == 0
+    assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 17, 4096) == 0
