@@ -21,7 +21,10 @@ typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr uint64_t kMaxCols = uint64_t{1} << 24;    // columns and strides: a tile's byte offsets fit 32 bits
+constexpr uint64_t kMaxCols = uint64_t{1} << 24;    // columns of a matrix
+constexpr uint64_t kMaxK = uint64_t{1} << 21;       // of a product: 256 rows of codes, or of x, within 31 bits of bytes
+constexpr uint64_t kMaxRows = 0x7FFFFFFFu;
+constexpr uint64_t kMaxStride = uint64_t{1} << 32;
 constexpr uint64_t kMaxValues = uint64_t{1} << 40;  // values of one matrix
 constexpr uint32_t kBlock = 32;                     // values that share a scale
 constexpr uint32_t kNanScale = 255;
@@ -173,7 +176,19 @@ struct MulParams {
     uint16_t *y;
     uint64_t x_stride, y_stride;
     uint32_t m, n, blocks;  // blocks of 32 along k
+    uint32_t y_wide;        // rows of y start at multiples of 16 bytes
+    // tile form
+    uint32_t tiles_m, tiles_n;
+    float *part;  // [splits][m][n_padded] where k is split
+    uint32_t splits, split_stages, n_padded;
 };
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    bf2 v;
+    v.x = static_cast<__bf16>(a);
+    v.y = static_cast<__bf16>(b);
+    return __builtin_bit_cast(uint32_t, v);
+}
 
 // Token form: a workgroup takes 16 rows of w, its waves share k between them
 // and add their sums in LDS.  A lane reads 16 bytes of codes at a time, which
@@ -229,6 +244,175 @@ token_kernel(MulParams p) {
             for (uint32_t k = 0; k < kTokenWaves; ++k) v += s_sum[k][threadIdx.x];
             if (row < p.m && col < p.n)
                 p.y[uint64_t{row} * p.y_stride + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+        }
+    }
+}
+
+// Tile form, for many rows: a workgroup computes a tile of 16 kTilesM kWavesM
+// rows of x by 64 kWavesN rows of w, a wave 16 kTilesM by 64 of it, in stages
+// of 128 along k.  x goes to LDS by loads that write there directly, two
+// stages, the next one loading while one is computed.  The codes go from
+// memory to the registers of the waves that use them and are expanded there:
+// a lane's 16 bytes are one block of 32, k as in the token form.  A row of x
+// in LDS is 16 pieces of 16 bytes; piece c of row i lies at c ^ (i % 16), so
+// that the 16 rows a read touches use all banks once.  Row m of a wave's t-th
+// tile of w is row 16 (m / 4) + 4 t + m % 4 of its 64, which leaves a lane
+// with 16 neighbouring columns of y in the end.
+constexpr uint32_t kStageK = 128;
+constexpr uint32_t kStageBlocks = kStageK / kBlock;
+constexpr uint32_t kRowBytes = kStageK * 2;
+
+typedef __attribute__((address_space(3))) void *LdsPtr;
+
+// Waits for this wave's loads, those into LDS among them: a barrier alone does
+// not (vmcnt 0; the other counters as they are).
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+template <int kWavesM, int kWavesN, int kTilesM, bool kSplit>
+__global__ void __launch_bounds__(64 * kWavesM * kWavesN) tile_kernel(MulParams p) {
+    constexpr int kWaves = kWavesM * kWavesN;
+    constexpr uint32_t kRowsM = 16 * kTilesM * kWavesM, kRowsN = 64 * kWavesN;
+    constexpr int kLoads = kRowsM / 4 / kWaves;  // a wave's loads of a stage, 4 rows each
+    static_assert(kWaves % 4 == 0 && kRowsM / 4 % kWaves == 0, "whole loads, the same piece in all of a lane's");
+    __shared__ __attribute__((aligned(1024))) uint8_t s_x[2 * kRowsM * kRowBytes];
+
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = wave % kWavesM, wn = wave / kWavesM;
+    // workgroups go round the 8 XCDs; each XCD takes a run of neighbouring
+    // tiles, so that its L2 holds what they share
+    const uint32_t tiles = p.tiles_m * p.tiles_n;
+    uint32_t id = blockIdx.x;
+    const uint32_t split = kSplit ? id / tiles : 0;
+    id -= split * tiles;
+    const uint32_t per = tiles / 8, more = tiles % 8, xcd = id % 8;
+    const uint32_t t = xcd * per + min(xcd, more) + id / 8;
+    const uint32_t m0 = (t % p.tiles_m) * kRowsM, n0 = (t / p.tiles_m) * kRowsN;
+
+    const uint32_t stages = (p.blocks + kStageBlocks - 1) / kStageBlocks;
+    const uint32_t first = kSplit ? split * p.split_stages : 0;
+    const uint32_t last = kSplit ? min(first + p.split_stages, stages) : stages;
+
+    // Rows past m and n, and blocks past k, lie past their resource and read as
+    // zero; the scalar offsets stay within it.
+    // x: lane l of a load has row l / 16 of four, of it piece l % 16 in LDS
+    const uint32_t row_bytes = static_cast<uint32_t>(p.x_stride) * 2, k_bytes = p.blocks * kBlock * 2;
+    const Rsrc xr = rsrc(p.x + uint64_t{m0} * p.x_stride, (min(kRowsM, p.m - m0) - 1) * row_bytes + k_bytes);
+    const uint32_t x_piece = (r ^ ((4 * wave + q) & 15u)) * 16;
+    const uint32_t x_off = (4 * wave + q) * row_bytes + x_piece;
+    // w: the lane's row of the wave's first tile
+    const uint32_t rows_n = min(kRowsN, p.n - n0);
+    const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
+    const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
+    const uint32_t w_off = (64 * wn + 16 * (r / 4) + r % 4) * p.blocks + q;
+
+    auto load_x = [&](uint32_t stage, uint8_t *to) {
+        const uint32_t k0 = __builtin_amdgcn_readfirstlane(stage * kRowBytes);
+        const uint32_t off = k0 + x_piece < k_bytes ? x_off : kOff;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(to + (i * kWaves + wave) * 1024), 16,
+                                                     off + 4 * kWaves * i * row_bytes, k0, 0, 0);
+    };
+    struct W {
+        v4u code[4];
+        uint32_t scale[4];
+    };
+    auto load_w = [&](uint32_t stage, W &w) {
+        const uint32_t at = __builtin_amdgcn_readfirstlane(stage * kStageBlocks);
+        const bool in = at + q < p.blocks;
+        const uint32_t code_off = in ? w_off * 16 : kOff, scale_off = in ? w_off : kOff;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w.code[i] = __builtin_amdgcn_raw_buffer_load_b128(wr, code_off + 4 * i * p.blocks * 16, at * 16, 0);
+            w.scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, scale_off + 4 * i * p.blocks, at, 0);
+        }
+    };
+
+    f4 acc[kTilesM][4] = {};
+    auto compute = [&](const uint8_t *x, const W &w) {
+        const uint8_t *row = x + (wm * 16 * kTilesM + r) * kRowBytes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bf8 wf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wf[i] = __builtin_bit_cast(bf8, expand8(w.code[i][j], __builtin_bit_cast(float, (w.scale[i] & 255u) << 23)));
+            const uint32_t piece = ((4 * q + j) ^ r) * 16;
+#pragma unroll
+            for (int m = 0; m < kTilesM; ++m) {
+                const bf8 xf = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + piece);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i], xf, acc[m][i], 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    W w, next;
+    if (first < last) {
+        load_x(first, s_x);
+        load_w(first, w);
+    }
+    uint32_t flip = 0;
+    for (uint32_t s = first; s < last; ++s) {
+        arrived();
+        __syncthreads();  // stage s is there, stage s - 1 is read
+        const uint32_t other = flip ^ (kRowsM * kRowBytes);
+        if (s + 1 < last) {
+            load_x(s + 1, s_x + other);
+            load_w(s + 1, next);
+        }
+        compute(s_x + flip, w);
+        w = next;
+        flip = other;
+    }
+
+    // a lane: columns 16 q .. 16 q + 15 of the wave's 64, row r of each tile
+    const uint32_t col = n0 + 64 * wn + 16 * q;
+#pragma unroll
+    for (int m = 0; m < kTilesM; ++m) {
+        const uint32_t row = m0 + (wm * kTilesM + m) * 16 + r;
+        if (row >= p.m || col >= p.n) continue;
+        if (kSplit) {
+            float *to = p.part + (uint64_t{split} * p.m + row) * p.n_padded + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f4 *>(to + 4 * i) = acc[m][i];
+        } else {
+            uint16_t *to = p.y + uint64_t{row} * p.y_stride + col;
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
+            if (p.y_wide && col + 16 <= p.n) {
+                *reinterpret_cast<v4u *>(to) = v4u{o[0], o[1], o[2], o[3]};
+                *reinterpret_cast<v4u *>(to + 8) = v4u{o[4], o[5], o[6], o[7]};
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i)
+                    if (col + i < p.n) to[i] = static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+// y := the sum of the splits' tiles, in their order.
+__global__ void __launch_bounds__(256) join_kernel(MulParams p) {
+    const uint32_t quads = p.n_padded / 4;
+    const uint64_t total = uint64_t{p.m} * quads;
+    for (uint64_t i = uint64_t{blockIdx.x} * 256 + threadIdx.x; i < total; i += uint64_t{gridDim.x} * 256) {
+        const uint64_t row = i / quads;
+        const uint32_t col = static_cast<uint32_t>(i - row * quads) * 4;
+        if (col >= p.n) continue;
+        f4 v = *reinterpret_cast<const f4 *>(p.part + 4 * i);
+        for (uint32_t s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f4 *>(p.part + s * 4 * total + 4 * i);
+        uint16_t *to = p.y + row * p.y_stride + col;
+        const uint32_t lo = pack2(v[0], v[1]), hi = pack2(v[2], v[3]);
+        if (p.y_wide && col + 4 <= p.n) {
+            *reinterpret_cast<v2u *>(to) = v2u{lo, hi};
+        } else {
+            const uint32_t o[2] = {lo, hi};
+            for (uint32_t j = 0; j < 4 && col + j < p.n; ++j) to[j] = static_cast<uint16_t>(o[j / 2] >> (16 * (j & 1)));
         }
     }
 }
@@ -290,30 +474,75 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
                            static_cast<uint32_t>(cols), blocks, items, out, out_stride));
 }
 
-// Rows of x are read 16 bytes at a time and whole blocks at a time: anything
-// else goes through a packed copy in the workspace.
-bool needs_copy(uint64_t k, bool x_aligned) { return !x_aligned || k % kBlock != 0; }
+// Rows of x are read 16 bytes at a time and whole blocks at a time, with byte
+// offsets of 31 bits in a tile: anything else goes through a packed copy in
+// the workspace.
+constexpr uint64_t kMaxRead = uint64_t{1} << 21;  // stride of x in a tile of 256 rows: 2^30 bytes
 
-uint64_t copy_bytes(uint64_t m, uint64_t k) { return m * ((k + kBlock - 1) / kBlock) * kBlock * 2; }
+uint64_t copy_bytes(uint64_t m, uint64_t k, bool x_readable) {
+    if (x_readable && k % kBlock == 0) return 0;
+    return (m * ((k + kBlock - 1) / kBlock) * kBlock * 2 + 15) / 16 * 16;
+}
 
-uint64_t matmul_workspace(uint64_t m, uint64_t n, uint64_t k, bool x_aligned) {
-    (void)n;
-    return needs_copy(k, x_aligned) ? copy_bytes(m, k) : 0;
+// The form of a product.
+struct Form {
+    bool token;
+    uint32_t variant;  // tile form: rows of x in a tile
+    uint32_t tiles_m, tiles_n, splits, split_stages;
+    uint64_t n_padded, part_bytes;
+};
+
+Form form_of(uint64_t m, uint64_t n, uint64_t k) {
+    Form f = {};
+    f.token = m <= 64;
+    if (f.token) return f;
+    f.variant = m > 128 ? 256 : m > 64 ? 128 : 64;
+    f.tiles_m = static_cast<uint32_t>((m + f.variant - 1) / f.variant);
+    f.tiles_n = static_cast<uint32_t>((n + 255) / 256);
+    const uint64_t tiles = uint64_t{f.tiles_m} * f.tiles_n;
+    const uint32_t stages = static_cast<uint32_t>((k + kStageK - 1) / kStageK);
+    f.splits = 1;
+    f.split_stages = stages;
+    if (tiles < 128 && stages >= 4) {
+        const uint32_t want = static_cast<uint32_t>(std::min<uint64_t>((256 + tiles - 1) / tiles, stages / 2));
+        f.split_stages = (stages + want - 1) / want;
+        f.splits = (stages + f.split_stages - 1) / f.split_stages;
+    }
+    f.n_padded = (n + 15) / 16 * 16;
+    f.part_bytes = f.splits > 1 ? uint64_t{f.splits} * m * f.n_padded * 4 : 0;
+    return f;
+}
+
+uint64_t matmul_workspace(uint64_t m, uint64_t n, uint64_t k, bool x_readable) {
+    return copy_bytes(m, k, x_readable) + form_of(m, n, k).part_bytes;
+}
+
+template <int kWavesM, int kWavesN, int kTilesM>
+hipError_t launch_tiles(const Form &f, hipStream_t st, const MulParams &p) {
+    const uint32_t grid = f.tiles_m * f.tiles_n * f.splits;
+    return f.splits > 1 ? launch(tile_kernel<kWavesM, kWavesN, kTilesM, true>, dim3(grid), 64 * kWavesM * kWavesN, st, p)
+                        : launch(tile_kernel<kWavesM, kWavesN, kTilesM, false>, dim3(grid), 64 * kWavesM * kWavesN, st, p);
 }
 
 df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
                    const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                    uint64_t workspace_bytes, void *hip_stream) {
-    if (m > 0x7FFFFFFFu || n > 0x7FFFFFFFu || k > kMaxCols || x_stride > kMaxCols || x_stride < k || y_stride < n)
+    if (m > kMaxRows || n > kMaxRows || k > kMaxK || x_stride > kMaxStride || x_stride < k || y_stride < n ||
+        y_stride > kMaxStride)
         return DF11_E_INVALID_ARG;
     if (m == 0 || n == 0) return DF11_OK;
     if (!y || (k && (!x || !codes || !scales)) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(x) & 1u) ||
-        (reinterpret_cast<uintptr_t>(y) & 1u) || (workspace && !aligned16(workspace)))
+        (reinterpret_cast<uintptr_t>(y) & 1u) || !aligned16(workspace))
         return DF11_E_INVALID_ARG;
-    const bool al = aligned16(x) && x_stride % 8 == 0;
-    if (workspace_bytes < matmul_workspace(m, n, k, al)) return DF11_E_BUFFER_TOO_SMALL;
+    const bool readable = aligned16(x) && x_stride % 8 == 0 && x_stride <= kMaxRead;
+    const uint64_t copy = copy_bytes(m, k, readable);
+    const Form f = form_of(m, n, k);
+    if (workspace_bytes < copy + f.part_bytes) return DF11_E_BUFFER_TOO_SMALL;
+    if (copy + f.part_bytes && !workspace) return DF11_E_INVALID_ARG;
+    const uint64_t tiles = uint64_t{f.tiles_m} * f.tiles_n * f.splits;
+    if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    MulParams p;
+    MulParams p = {};
     p.x = x;
     p.codes = codes;
     p.scales = scales;
@@ -323,23 +552,36 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.m = static_cast<uint32_t>(m);
     p.n = static_cast<uint32_t>(n);
     p.blocks = static_cast<uint32_t>((k + kBlock - 1) / kBlock);
+    p.y_wide = aligned16(y) && y_stride % 8 == 0;
     hipError_t err = hipSuccess;
-    if (needs_copy(k, al)) {
-        if (!workspace) return DF11_E_INVALID_ARG;
+    if (copy) {
         const uint32_t width = p.blocks * kBlock;
         const uint64_t lanes = m * (width / 8);
-        if (lanes)
-            err = launch(pack_rows_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((lanes + 255) / 256, 8192))), 256,
-                         st, x, x_stride, static_cast<uint32_t>(k), width, m, static_cast<uint16_t *>(workspace));
+        err = launch(pack_rows_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((lanes + 255) / 256, 8192))), 256,
+                     st, x, x_stride, static_cast<uint32_t>(k), width, m, static_cast<uint16_t *>(workspace));
         if (err != hipSuccess) return launched(err);
         p.x = static_cast<const uint16_t *>(workspace);
         p.x_stride = width;
     }
-    const uint32_t gn = static_cast<uint32_t>((n + 15) / 16);
-    if (m <= 16)
-        err = launch(token_kernel<1>, dim3(gn, 1), 64 * kTokenWaves, st, p);
-    else
-        err = launch(token_kernel<4>, dim3(gn, static_cast<uint32_t>((m + 63) / 64)), 64 * kTokenWaves, st, p);
+    if (f.token) {
+        const uint32_t gn = static_cast<uint32_t>((n + 15) / 16);
+        err = m <= 16 ? launch(token_kernel<1>, dim3(gn), 64 * kTokenWaves, st, p)
+                      : launch(token_kernel<4>, dim3(gn), 64 * kTokenWaves, st, p);
+        return launched(err);
+    }
+    p.tiles_m = f.tiles_m;
+    p.tiles_n = f.tiles_n;
+    p.splits = f.splits;
+    p.split_stages = f.split_stages;
+    p.n_padded = static_cast<uint32_t>(f.n_padded);
+    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + copy);
+    err = f.variant == 256   ? launch_tiles<2, 4, 8>(f, st, p)
+          : f.variant == 128 ? launch_tiles<2, 4, 4>(f, st, p)
+                             : launch_tiles<1, 4, 4>(f, st, p);
+    if (err == hipSuccess && f.splits > 1) {
+        const uint64_t quads = m * (f.n_padded / 4);
+        err = launch(join_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((quads + 255) / 256, 8192))), 256, st, p);
+    }
     return launched(err);
 }
 
@@ -356,7 +598,7 @@ extern "C" df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *
 }
 
 extern "C" uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned) {
-    if (m > 0x7FFFFFFFu || n > 0x7FFFFFFFu || k > kMaxCols) return 0;  // refused by the product
+    if (m > kMaxRows || n > kMaxRows || k > kMaxK) return 0;  // refused by the product
     return matmul_workspace(m, n, k, x_aligned != 0);
 }
 

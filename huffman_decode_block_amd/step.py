@@ -139,7 +139,7 @@ def _workspace(torch, given, need, dev):
 
 
 def df11_mx4_matmul_workspace_bytes(m: int, n: int, k: int, x_aligned: bool = True) -> int:
-    """Bytes of workspace df11_mx4_matmul needs (0 for most products)."""
+    """Bytes of workspace df11_mx4_matmul needs."""
     return int(_lib().df11_mx4_matmul_workspace_bytes(int(m), int(n), int(k), 1 if x_aligned else 0))
 
 
@@ -225,7 +225,7 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
                 raise ValueError(f"out must be {(m, n)}, got {tuple(out.shape)}")
         L = _lib()
         xs, xp = _row_stride(x), x.data_ptr()
-        need = L.df11_mx4_matmul_workspace_bytes(m, n, k, 1 if xs % 8 == 0 and xp % 16 == 0 else 0)
+        need = L.df11_mx4_matmul_workspace_bytes(m, n, k, 1 if xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21 else 0)
         ws, size = _workspace(torch, workspace, need, dev)
         st = L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), _row_stride(out),
                                None if ws is None else ws.data_ptr(), size, on.handle)

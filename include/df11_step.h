@@ -63,14 +63,16 @@ df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, uin
  * m = 0 or n = 0 is a no-op; k = 0 gives zeros.  The result does not depend
  * on what runs beside it: every sum has a fixed order.  y must not overlap
  * the inputs.  Errors: DF11_E_INVALID_ARG (null or misaligned pointers,
- * strides below k or n or over 2^24, m or n over 2^31 - 1, k over 2^24),
+ * strides below k or n or over 2^32, m or n over 2^31 - 1, k over 2^21),
  * DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
 df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
                             const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                             uint64_t workspace_bytes, void *hip_stream);
 
-/* Bytes of workspace for a product (0 for most).  x_aligned: whether x is
- * 16-byte aligned with x_stride a multiple of 8. */
+/* Bytes of workspace for a product: a packed copy of x where x cannot be read
+ * 16 bytes at a time or k is no multiple of 32, and partial sums where k is
+ * split over workgroups.  x_aligned: whether x is 16-byte aligned with
+ * x_stride a multiple of 8 and at most 2^21. */
 uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned);
 
 /* ---- Paged key-value cache ----------------------------------------------

@@ -49,7 +49,7 @@ def test_quantise_refusals(change):
     (dict(codes=P + 4), hdb.DF11_E_INVALID_ARG), (dict(scales=None), hdb.DF11_E_INVALID_ARG),
     (dict(xs=63), hdb.DF11_E_INVALID_ARG), (dict(ys=39), hdb.DF11_E_INVALID_ARG),
     (dict(m=1 << 31), hdb.DF11_E_INVALID_ARG), (dict(n=1 << 31, ys=1 << 31), hdb.DF11_E_INVALID_ARG),
-    (dict(k=(1 << 24) + 1, xs=1 << 25), hdb.DF11_E_INVALID_ARG), (dict(xs=1 << 25), hdb.DF11_E_INVALID_ARG),
+    (dict(k=(1 << 21) + 1, xs=1 << 25), hdb.DF11_E_INVALID_ARG), (dict(xs=1 << 33), hdb.DF11_E_INVALID_ARG),
     (dict(k=63), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(x=P + 2), hdb.DF11_E_BUFFER_TOO_SMALL),
     (dict(xs=65), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(k=63, ws=P + 8, size=1 << 20), hdb.DF11_E_INVALID_ARG),
     (dict(k=63, ws=None, size=1 << 20), hdb.DF11_E_INVALID_ARG),
