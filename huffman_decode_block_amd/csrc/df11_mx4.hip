@@ -199,52 +199,62 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // of a lane's codes.
 constexpr uint32_t kTokenWaves = 8;
 
-template <int kTiles>  // tiles of 16 rows of x
+template <int kRows>  // tiles of 16 rows of w
 __global__ void __launch_bounds__(64 * kTokenWaves)
 token_kernel(MulParams p) {
-    __shared__ float s_sum[kTokenWaves][16 * 16];
+    __shared__ float s_sum[kTokenWaves][kRows][16 * 16];
+    constexpr uint32_t kAhead = 4;  // steps whose codes are in flight together
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * kTiles;
-    const uint32_t rows_n = min(16u, p.n - n0);
+    const uint32_t n0 = blockIdx.x * 16 * kRows;
+    const uint32_t rows_n = min(16u * kRows, p.n - n0);
     const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
     const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
-    f4 acc[kTiles] = {};
+    const uint32_t row_bytes = static_cast<uint32_t>(p.x_stride) * 2;
+    const Rsrc xr = rsrc(p.x, (p.m - 1) * row_bytes + p.blocks * kBlock * 2);
+    const uint32_t x_row = r < p.m ? r * row_bytes : kOff;
+    f4 acc[kRows] = {};
     const uint32_t steps = (p.blocks + 3) / 4;
-    for (uint32_t s = wave; s < steps; s += kTokenWaves) {
-        const uint32_t block = 4 * s + q;
-        const bool in = block < p.blocks;
-        const v4u c = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? (r * p.blocks + block) * 16 : kOff, 0, 0);
-        const uint32_t sb = __builtin_amdgcn_raw_buffer_load_b8(sr, in ? r * p.blocks + block : kOff, 0, 0);
-        const float scale = __builtin_bit_cast(float, (sb & 255u) << 23);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-        bf8 w[4];
+    for (uint32_t s0 = wave; s0 < steps; s0 += kTokenWaves * kAhead) {
+        v4u c[kAhead][kRows], x[kAhead][4];
+        uint32_t sb[kAhead][kRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(bf8, expand8(cw[i], scale));
+        for (uint32_t a = 0; a < kAhead; ++a) {
+            const uint32_t block = 4 * (s0 + a * kTokenWaves) + q;
+            const uint32_t at = block < p.blocks ? r * p.blocks + block : kOff / 16;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const uint32_t row = m0 + 16 * t + r;
-            const bool live = in && row < p.m;
-            const v4u *src = reinterpret_cast<const v4u *>(p.x + uint64_t{row} * p.x_stride + block * kBlock);
+            for (uint32_t t = 0; t < kRows; ++t) {
+                c[a][t] = __builtin_amdgcn_raw_buffer_load_b128(wr, (at + 16 * t * p.blocks) * 16, 0, 0);
+                sb[a][t] = __builtin_amdgcn_raw_buffer_load_b8(sr, at + 16 * t * p.blocks, 0, 0);
+            }
+            const uint32_t x_at = block < p.blocks ? x_row + block * kBlock * 2 : kOff;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const v4u xv = live ? src[i] : v4u{0, 0, 0, 0};
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], __builtin_bit_cast(bf8, xv), acc[t], 0, 0, 0);
+            for (int i = 0; i < 4; ++i) x[a][i] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_at + 16 * i, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all loads are on their way before the first is waited for
+#pragma unroll
+        for (uint32_t a = 0; a < kAhead; ++a) {
+#pragma unroll
+            for (uint32_t t = 0; t < kRows; ++t) {
+                const float scale = __builtin_bit_cast(float, (sb[a][t] & 255u) << 23);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, expand8(c[a][t][i], scale)),
+                                                                     __builtin_bit_cast(bf8, x[a][i]), acc[t], 0, 0, 0);
             }
         }
     }
     // acc: column lane % 16 (a row of x), rows 4 (lane / 16) + 0..3 (of w)
-    for (int t = 0; t < kTiles; ++t) {
-        __syncthreads();
-        *reinterpret_cast<f4 *>(&s_sum[wave][r * 16 + 4 * q]) = acc[t];
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            const uint32_t row = m0 + 16 * t + threadIdx.x / 16, col = n0 + threadIdx.x % 16;
-            float v = 0;
-            for (uint32_t k = 0; k < kTokenWaves; ++k) v += s_sum[k][threadIdx.x];
-            if (row < p.m && col < p.n)
-                p.y[uint64_t{row} * p.y_stride + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-        }
+#pragma unroll
+    for (uint32_t t = 0; t < kRows; ++t) *reinterpret_cast<f4 *>(&s_sum[wave][t][r * 16 + 4 * q]) = acc[t];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < kRows * 256; i += 64 * kTokenWaves) {
+        const uint32_t t = i / 256, row = i % 256 / 16, col = n0 + 16 * t + i % 16;
+        float v = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kTokenWaves; ++k) v += s_sum[k][t][i % 256];
+        if (row < p.m && col < p.n)
+            p.y[uint64_t{row} * p.y_stride + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
 }
 
@@ -269,7 +279,8 @@ typedef __attribute__((address_space(3))) void *LdsPtr;
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 template <int kWavesM, int kWavesN, int kTilesM, bool kSplit>
-__global__ void __launch_bounds__(64 * kWavesM * kWavesN) tile_kernel(MulParams p) {
+__global__ void __launch_bounds__(64 * kWavesM * kWavesN) __attribute__((amdgpu_waves_per_eu(2)))
+tile_kernel(MulParams p) {
     constexpr int kWaves = kWavesM * kWavesN;
     constexpr uint32_t kRowsM = 16 * kTilesM * kWavesM, kRowsN = 64 * kWavesN;
     constexpr int kLoads = kRowsM / 4 / kWaves;  // a wave's loads of a stage, 4 rows each
@@ -329,22 +340,43 @@ __global__ void __launch_bounds__(64 * kWavesM * kWavesN) tile_kernel(MulParams 
         }
     };
 
+    // Stage: 4 steps of 32 along k, in each 4 kTilesM matrix instructions.  A
+    // piece of x is read for the next step as soon as this step is done with
+    // the registers it goes to, and the next step's codes are expanded beside;
+    // the order is given to the compiler in groups.
     f4 acc[kTilesM][4] = {};
+    auto expand = [&](const W &w, int j, bf8 (&to)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            to[i] = __builtin_bit_cast(bf8, expand8(w.code[i][j], __builtin_bit_cast(float, (w.scale[i] & 255u) << 23)));
+    };
     auto compute = [&](const uint8_t *x, const W &w) {
         const uint8_t *row = x + (wm * 16 * kTilesM + r) * kRowBytes;
+        bf8 xf[kTilesM], wf[2][4];
+#pragma unroll
+        for (int m = 0; m < kTilesM; ++m)
+            xf[m] = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + ((4 * q) ^ r) * 16);
+        expand(w, 0, wf[0]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            bf8 wf[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                wf[i] = __builtin_bit_cast(bf8, expand8(w.code[i][j], __builtin_bit_cast(float, (w.scale[i] & 255u) << 23)));
-            const uint32_t piece = ((4 * q + j) ^ r) * 16;
+            const uint32_t piece = ((4 * q + j + 1) ^ r) * 16;
+            if (j < 3) expand(w, j + 1, wf[(j + 1) & 1]);
 #pragma unroll
             for (int m = 0; m < kTilesM; ++m) {
-                const bf8 xf = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + piece);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i], xf, acc[m][i], 0, 0, 0);
+                    acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[j & 1][i], xf[m], acc[m][i], 0, 0, 0);
+                if (j < 3) xf[m] = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + piece);
+            }
+            if (j < 3) {
+#pragma unroll
+                for (int m = 0; m < kTilesM; ++m) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                 // matrix instructions
+                    __builtin_amdgcn_sched_group_barrier(0x002, 16 / kTilesM, 0);      // expansion
+                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 // LDS read
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -487,16 +519,19 @@ uint64_t copy_bytes(uint64_t m, uint64_t k, bool x_readable) {
 // The form of a product.
 struct Form {
     bool token;
-    uint32_t variant;  // tile form: rows of x in a tile
+    uint32_t variant;  // token form: tiles of w a wave has; tile form: rows of x in a tile
     uint32_t tiles_m, tiles_n, splits, split_stages;
     uint64_t n_padded, part_bytes;
 };
 
 Form form_of(uint64_t m, uint64_t n, uint64_t k) {
     Form f = {};
-    f.token = m <= 64;
-    if (f.token) return f;
-    f.variant = m > 128 ? 256 : m > 64 ? 128 : 64;
+    f.token = m <= 16;
+    if (f.token) {
+        f.variant = n > 8192 ? 2 : 1;
+        return f;
+    }
+    f.variant = m > 128 ? 256 : m > 64 ? 128 : m > 32 ? 64 : 32;
     f.tiles_m = static_cast<uint32_t>((m + f.variant - 1) / f.variant);
     f.tiles_n = static_cast<uint32_t>((n + 255) / 256);
     const uint64_t tiles = uint64_t{f.tiles_m} * f.tiles_n;
@@ -564,9 +599,11 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         p.x_stride = width;
     }
     if (f.token) {
-        const uint32_t gn = static_cast<uint32_t>((n + 15) / 16);
-        err = m <= 16 ? launch(token_kernel<1>, dim3(gn), 64 * kTokenWaves, st, p)
-                      : launch(token_kernel<4>, dim3(gn), 64 * kTokenWaves, st, p);
+        const dim3 grid(static_cast<uint32_t>((n + 16 * f.variant - 1) / (16 * f.variant)));
+        err = launch(f.variant == 1   ? token_kernel<1>
+                     : f.variant == 2 ? token_kernel<2>
+                                      : token_kernel<4>,
+                     grid, 64 * kTokenWaves, st, p);
         return launched(err);
     }
     p.tiles_m = f.tiles_m;
@@ -576,8 +613,9 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.n_padded = static_cast<uint32_t>(f.n_padded);
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + copy);
     err = f.variant == 256   ? launch_tiles<2, 4, 8>(f, st, p)
-          : f.variant == 128 ? launch_tiles<2, 4, 4>(f, st, p)
-                             : launch_tiles<1, 4, 4>(f, st, p);
+          : f.variant == 128 ? launch_tiles<1, 4, 8>(f, st, p)
+          : f.variant == 64  ? launch_tiles<1, 4, 4>(f, st, p)
+                             : launch_tiles<1, 4, 2>(f, st, p);
     if (err == hipSuccess && f.splits > 1) {
         const uint64_t quads = m * (f.n_padded / 4);
         err = launch(join_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((quads + 255) / 256, 8192))), 256, st, p);
