@@ -49,6 +49,10 @@ _SIGNATURES = {
 }
 
 
+_torch = None  # torch and the library, from the first call on
+_L = None
+
+
 def declare(L) -> None:
     """Sets the argument and result types of the step's entry points."""
     for name, (args, res) in _SIGNATURES.items():
@@ -56,9 +60,14 @@ def declare(L) -> None:
         fn.argtypes, fn.restype = args, res
 
 
-def _lib():
+def _load():
+    global _torch, _L
+    import torch
+
     from . import lib
-    return lib()
+    _L = lib()
+    _torch = torch
+    return torch
 
 
 def _check(status: int, what: str):
@@ -67,44 +76,28 @@ def _check(status: int, what: str):
         check(status, what)
 
 
-class _On:
-    """The device and stream a call runs on: raw handle, and, where the stream
-    is not the current one, a context in which torch allocates for it."""
-
-    __slots__ = ("torch", "device", "handle", "stack")
-
-    def __init__(self, device, stream):
-        import torch
-        self.torch, self.device, self.stack = torch, device, None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            self.handle = stream.cuda_stream
-        else:
-            self.handle = int(stream)
-        if device.index != torch.cuda.current_device() or (
-                stream is not None and self.handle != torch.cuda.current_stream(device).cuda_stream):
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(self.handle, device=device)
-            self.stack = stream
-
-    def __enter__(self):
-        if self.stack is not None:
-            self.stack = self.torch.cuda.stream(self.stack)
-            self.stack.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.__exit__(*exc)
+def _place(dev, stream):
+    """Where a call on `dev` runs: the raw stream handle, and None or a context
+    that makes that device and stream torch's current ones (so that what the
+    call allocates belongs to its stream)."""
+    torch = _torch
+    here = torch.cuda.current_device() == dev.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)  # the public call builds a Stream object, 1 us more
+        return handle, None if here else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        if here and handle == torch._C._cuda_getCurrentRawStream(dev.index):
+            return handle, None
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _tensor(t, name, dtype, ndim, dev=None):
     """Checks a tensor's place, type and rank."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
@@ -113,8 +106,8 @@ def _tensor(t, name, dtype, ndim, dev=None):
 
 
 def _last_dense(t, name):
-    """The last dimension's values lie next to each other and no stride is negative or hidden by expansion."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    """The last dimension's values lie next to each other."""
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
@@ -128,78 +121,105 @@ def _dense(t, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(torch, given, need, dev):
+def _workspace(given, need, dev):
+    """(tensor to keep, address, bytes) of a workspace: the given one or a new one."""
     if given is not None:
-        if not isinstance(given, torch.Tensor) or not given.is_cuda or given.device != dev or not given.is_contiguous():
+        if not isinstance(given, _torch.Tensor) or given.device != dev or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous device tensor on the inputs' GPU")
-        return given, given.numel() * given.element_size()
+        return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=dev), need
+        return None, None, 0
+    t = _torch.empty(need, dtype=_torch.uint8, device=dev)
+    return t, t.data_ptr(), need
 
 
 def df11_mx4_matmul_workspace_bytes(m: int, n: int, k: int, x_aligned: bool = True) -> int:
     """Bytes of workspace df11_mx4_matmul needs."""
-    return int(_lib().df11_mx4_matmul_workspace_bytes(int(m), int(n), int(k), 1 if x_aligned else 0))
+    if _torch is None:
+        _load()
+    return int(_L.df11_mx4_matmul_workspace_bytes(int(m), int(n), int(k), 1 if x_aligned else 0))
+
+
+def _codes(codes, scales, cols, dev):
+    """Checks codes and scale bytes of a matrix with `cols` columns; returns its rows."""
+    u8 = _torch.uint8
+    _tensor(codes, "codes", u8, 2, dev)
+    _tensor(scales, "scales", u8, 2, dev)
+    _dense(codes, "codes")
+    _dense(scales, "scales")
+    blocks = (cols + 31) // 32
+    rows, width = codes.shape
+    if width != 16 * blocks or scales.shape[1] != blocks or scales.shape[0] != rows:
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {cols} columns: "
+                         f"[rows, {16 * blocks}] and [rows, {blocks}] expected")
+    return rows
 
 
 def df11_mx4_quantize(x, codes=None, scales=None, stream=None):
     """4-bit codes and scale bytes of x (BF16 device matrix [rows, cols], rows
     may be strided): uint8 tensors [rows, 16 * ceil(cols / 32)] and [rows,
     ceil(cols / 32)], allocated when None.  Returns (codes, scales)."""
-    import torch
+    torch = _torch or _load()
     _tensor(x, "x", torch.bfloat16, 2)
     _last_dense(x, "x")
-    rows, cols = x.shape
-    if cols == 0:
+    if x.shape[1] == 0:
         raise ValueError("x has no columns")
+    handle, ctx = _place(x.device, stream)
+    if ctx is None:
+        return _quantize(x, codes, scales, handle)
+    with ctx:
+        return _quantize(x, codes, scales, handle)
+
+
+def _quantize(x, codes, scales, handle):
+    rows, cols = x.shape
+    dev = x.device
     blocks = (cols + 31) // 32
-    with _On(x.device, stream) as on:
-        if codes is None:
-            codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty((rows, blocks), dtype=torch.uint8, device=x.device)
-        _codes(codes, scales, cols, x.device)
-        if codes.shape[0] != rows:
-            raise ValueError(f"codes has {codes.shape[0]} rows, x {rows}")
-        st = _lib().df11_mx4_quantize(x.data_ptr(), rows, cols, _row_stride(x), codes.data_ptr(), scales.data_ptr(),
-                                      on.handle)
-    _check(st, "df11_mx4_quantize")
+    if codes is None:
+        codes = _torch.empty((rows, 16 * blocks), dtype=_torch.uint8, device=dev)
+    if scales is None:
+        scales = _torch.empty((rows, blocks), dtype=_torch.uint8, device=dev)
+    if _codes(codes, scales, cols, dev) != rows:
+        raise ValueError(f"codes has {codes.shape[0]} rows, x {rows}")
+    _check(_L.df11_mx4_quantize(x.data_ptr(), rows, cols, _row_stride(x), codes.data_ptr(), scales.data_ptr(), handle),
+           "df11_mx4_quantize")
     return codes, scales
-
-
-def _codes(codes, scales, cols, dev):
-    import torch
-    _tensor(codes, "codes", torch.uint8, 2, dev)
-    _tensor(scales, "scales", torch.uint8, 2, dev)
-    _dense(codes, "codes")
-    _dense(scales, "scales")
-    blocks = (cols + 31) // 32
-    if codes.shape[1] != 16 * blocks or scales.shape[1] != blocks or codes.shape[0] != scales.shape[0]:
-        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {cols} columns: "
-                         f"[rows, {16 * blocks}] and [rows, {blocks}] expected")
 
 
 def df11_mx4_dequantize(codes, scales, cols: int, out=None, stream=None):
     """The values of 4-bit codes as a BF16 matrix [rows, cols] (exact).  Returns out."""
-    import torch
+    if _torch is None:
+        _load()
     cols = int(cols)
     if cols <= 0:
         raise ValueError("cols must be positive")
     _codes(codes, scales, cols, None)
-    rows, dev = codes.shape[0], codes.device
+    dev = codes.device
     if scales.device != dev:
         raise ValueError(f"scales is on {scales.device}, not {dev}")
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        _tensor(out, "out", torch.bfloat16, 2, dev)
-        _last_dense(out, "out")
-        if tuple(out.shape) != (rows, cols):
-            raise ValueError(f"out must be {(rows, cols)}, got {tuple(out.shape)}")
-        st = _lib().df11_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                        _row_stride(out), on.handle)
-    _check(st, "df11_mx4_dequantize")
+    handle, ctx = _place(dev, stream)
+    if ctx is None:
+        return _dequantize(codes, scales, cols, out, handle)
+    with ctx:
+        return _dequantize(codes, scales, cols, out, handle)
+
+
+def _out(out, shape, dtype, dev, name="out"):
+    """A new output, or the given one checked."""
+    if out is None:
+        return _torch.empty(shape, dtype=dtype, device=dev)
+    _tensor(out, name, dtype, len(shape), dev)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(out.shape)}")
+    _last_dense(out, name)
+    return out
+
+
+def _dequantize(codes, scales, cols, out, handle):
+    rows = codes.shape[0]
+    out = _out(out, (rows, cols), _torch.bfloat16, codes.device)
+    _check(_L.df11_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), _row_stride(out),
+                                  handle), "df11_mx4_dequantize")
     return out
 
 
@@ -208,48 +228,47 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
     of the 4-bit matrix [n, k] in codes and scales; sums in 32 bits, one
     rounding.  workspace: df11_mx4_matmul_workspace_bytes bytes, allocated
     when None and needed.  Returns out."""
-    import torch
+    torch = _torch or _load()
     _tensor(x, "x", torch.bfloat16, 2)
     _last_dense(x, "x")
+    dev = x.device
+    n = _codes(codes, scales, x.shape[1], dev)
+    handle, ctx = _place(dev, stream)
+    if ctx is None:
+        return _matmul(x, codes, scales, n, out, workspace, handle)
+    with ctx:
+        return _matmul(x, codes, scales, n, out, workspace, handle)
+
+
+def _matmul(x, codes, scales, n, out, workspace, handle):
     m, k = x.shape
     dev = x.device
-    _codes(codes, scales, k, dev)
-    n = codes.shape[0]
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        else:
-            _tensor(out, "out", torch.bfloat16, 2, dev)
-            _last_dense(out, "out")
-            if tuple(out.shape) != (m, n):
-                raise ValueError(f"out must be {(m, n)}, got {tuple(out.shape)}")
-        L = _lib()
-        xs, xp = _row_stride(x), x.data_ptr()
-        need = L.df11_mx4_matmul_workspace_bytes(m, n, k, 1 if xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21 else 0)
-        ws, size = _workspace(torch, workspace, need, dev)
-        st = L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), _row_stride(out),
-                               None if ws is None else ws.data_ptr(), size, on.handle)
-    _check(st, "df11_mx4_matmul")
+    out = _out(out, (m, n), _torch.bfloat16, dev)
+    xs, xp = _row_stride(x), x.data_ptr()
+    need = _L.df11_mx4_matmul_workspace_bytes(m, n, k, xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21)
+    keep, ws, size = _workspace(workspace, need, dev)
+    _check(_L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), _row_stride(out), ws,
+                              size, handle), "df11_mx4_matmul")
     return out
 
 
 def _cache(k_pages, v_pages, k_scale, v_scale, dev):
     """The df11_paged_cache of page tensors [n_pages, kv_heads, page_size, head_dim]."""
-    import torch
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a device tensor")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [n_pages, kv_heads, page_size, head_dim], got {tuple(t.shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not {dev}")
-        _last_dense(t, name)
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
-        raise ValueError("k_pages and v_pages differ in shape or type")
+    torch = _torch
+    dtype = k_pages.dtype if isinstance(k_pages, torch.Tensor) else None
+    e4m3 = dtype is torch.float8_e4m3fn
+    if not e4m3 and dtype is not torch.bfloat16:
+        raise TypeError(f"pages must be device tensors of bfloat16 or float8_e4m3fn, got {dtype}")
+    _tensor(k_pages, "k_pages", dtype, 4, dev)
+    _tensor(v_pages, "v_pages", dtype, 4, dev)
     n, h, page, d = k_pages.shape
-    e4m3 = k_pages.dtype == torch.float8_e4m3fn
-    if not e4m3 and k_pages.dtype != torch.bfloat16:
-        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages differ in shape")
+    k0, k1, k2, k3 = k_pages.stride()
+    v0, v1, v2, v3 = v_pages.stride()
+    if k3 != 1 or v3 != 1:
+        raise ValueError("the last dimension of the pages must be contiguous")
+    ks = vs = None
     if e4m3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None:
@@ -258,11 +277,10 @@ def _cache(k_pages, v_pages, k_scale, v_scale, dev):
             _dense(t, name)
             if t.shape[0] != h:
                 raise ValueError(f"{name} must hold {h} values, one for each head")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to E4M3 pages")
-    ks, vs = k_pages.stride(), v_pages.stride()
-    return df11_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), n, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                            k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None, h, d, page,
+    return df11_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), n, k0, k1, k2, v0, v1, v2, ks, vs, h, d, page,
                             DF11_CACHE_E4M3 if e4m3 else DF11_CACHE_BF16)
 
 
@@ -273,10 +291,11 @@ def df11_paged_append(k, v, slots, k_pages, v_pages, k_scale=None, v_scale=None,
     slots: int64 [tokens], page * page_size + position; negative or past the
     cache: the token is skipped.  E4M3 pages take k_scale and v_scale, float32
     [kv_heads]: what is stored is the value over its head's scale."""
-    import torch
-    _tensor(k, "k", torch.bfloat16, 3)
+    torch = _torch or _load()
+    bf16 = torch.bfloat16
+    _tensor(k, "k", bf16, 3)
     dev = k.device
-    _tensor(v, "v", torch.bfloat16, 3, dev)
+    _tensor(v, "v", bf16, 3, dev)
     _tensor(slots, "slots", torch.int64, 1, dev)
     _dense(slots, "slots")
     _last_dense(k, "k")
@@ -284,19 +303,27 @@ def df11_paged_append(k, v, slots, k_pages, v_pages, k_scale=None, v_scale=None,
     c = _cache(k_pages, v_pages, k_scale, v_scale, dev)
     t = slots.shape[0]
     want = (t, c.kv_heads, c.head_dim)
-    if tuple(k.shape) != want or tuple(v.shape) != want:
+    if k.shape != want or v.shape != want:
         raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    with _On(dev, stream) as on:
-        st = _lib().df11_paged_append(ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                                      v.stride(0), v.stride(1), slots.data_ptr(), t, on.handle)
+    handle, ctx = _place(dev, stream)
+    k0, k1, _ = k.stride()
+    v0, v1, _ = v.stride()
+    args = (ctypes.byref(c), k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, slots.data_ptr(), t, handle)
+    if ctx is None:
+        st = _L.df11_paged_append(*args)
+    else:
+        with ctx:
+            st = _L.df11_paged_append(*args)
     _check(st, "df11_paged_append")
 
 
 def df11_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
                                          table_width: int) -> int:
     """Bytes of workspace df11_paged_attention needs."""
-    return int(_lib().df11_paged_attention_workspace_bytes(int(batch), int(q_heads), int(kv_heads), int(head_dim),
-                                                           int(page_size), int(table_width)))
+    if _torch is None:
+        _load()
+    return int(_L.df11_paged_attention_workspace_bytes(int(batch), int(q_heads), int(kv_heads), int(head_dim),
+                                                       int(page_size), int(table_width)))
 
 
 def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, scale=None, k_scale=None, v_scale=None,
@@ -312,48 +339,50 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
     Returns (out, lse): BF16 [batch, q_heads, head_dim] and float32 [batch,
     q_heads], the natural logarithm of the sum of exponentials; a sequence
     with no position gets zeros and -inf."""
-    import torch
+    torch = _torch or _load()
+    i32 = torch.int32
     _tensor(q, "q", torch.bfloat16, 3)
     dev = q.device
     _last_dense(q, "q")
     c = _cache(k_pages, v_pages, k_scale, v_scale, dev)
-    _tensor(page_table, "page_table", torch.int32, 2, dev)
+    _tensor(page_table, "page_table", i32, 2, dev)
     _last_dense(page_table, "page_table")
-    _tensor(lens, "lens", torch.int32, 1, dev)
+    _tensor(lens, "lens", i32, 1, dev)
     _dense(lens, "lens")
     batch, heads, dim = q.shape
-    if dim != c.head_dim or heads % max(1, c.kv_heads) != 0:
+    if dim != c.head_dim or c.kv_heads == 0 or heads % c.kv_heads:
         raise ValueError(f"q {tuple(q.shape)} does not fit pages of {c.kv_heads} heads of {c.head_dim}")
     if page_table.shape[0] != batch or lens.shape[0] != batch:
         raise ValueError(f"page_table and lens must hold {batch} sequences")
     if starts is not None:
-        _tensor(starts, "starts", torch.int32, 1, dev)
+        _tensor(starts, "starts", i32, 1, dev)
         _dense(starts, "starts")
         if starts.shape[0] != batch:
             raise ValueError(f"starts must hold {batch} sequences")
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((batch, heads, dim), dtype=torch.bfloat16, device=dev)
-        else:
-            _tensor(out, "out", torch.bfloat16, 3, dev)
-            _dense(out, "out")
-            if tuple(out.shape) != (batch, heads, dim):
-                raise ValueError(f"out must be {(batch, heads, dim)}, got {tuple(out.shape)}")
-        if lse is None:
-            lse = torch.empty((batch, heads), dtype=torch.float32, device=dev)
-        else:
-            _tensor(lse, "lse", torch.float32, 2, dev)
-            _dense(lse, "lse")
-            if tuple(lse.shape) != (batch, heads):
-                raise ValueError(f"lse must be {(batch, heads)}, got {tuple(lse.shape)}")
-        L = _lib()
-        width = page_table.shape[1]
-        need = L.df11_paged_attention_workspace_bytes(batch, heads, c.kv_heads, dim, c.page_size, width)
-        ws, size = _workspace(torch, workspace, need, dev)
-        st = L.df11_paged_attention(
-            ctypes.byref(c), q.data_ptr(), batch, heads, q.stride(0), q.stride(1), page_table.data_ptr(),
-            page_table.stride(0) if batch > 1 else width, width, lens.data_ptr(),
-            None if starts is None else starts.data_ptr(), dim ** -0.5 if scale is None else float(scale),
-            out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), size, on.handle)
-    _check(st, "df11_paged_attention")
+    scale = dim ** -0.5 if scale is None else float(scale)
+    handle, ctx = _place(dev, stream)
+    if ctx is None:
+        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle)
+    with ctx:
+        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle)
+
+
+def _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle):
+    batch, heads, dim = q.shape
+    dev = q.device
+    given = out is not None, lse is not None
+    out = _out(out, (batch, heads, dim), _torch.bfloat16, dev)
+    lse = _out(lse, (batch, heads), _torch.float32, dev, "lse")
+    if given[0]:
+        _dense(out, "out")
+    if given[1]:
+        _dense(lse, "lse")
+    width = page_table.shape[1]
+    need = _L.df11_paged_attention_workspace_bytes(batch, heads, c.kv_heads, dim, c.page_size, width)
+    keep, ws, size = _workspace(workspace, need, dev)
+    q0, q1, _ = q.stride()
+    _check(_L.df11_paged_attention(ctypes.byref(c), q.data_ptr(), batch, heads, q0, q1, page_table.data_ptr(),
+                                   page_table.stride(0) if batch > 1 else width, width, lens.data_ptr(),
+                                   None if starts is None else starts.data_ptr(), scale, out.data_ptr(),
+                                   lse.data_ptr(), ws, size, handle), "df11_paged_attention")
     return out, lse
