@@ -137,7 +137,8 @@ struct AttnParams {
     float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
     uint64_t q_batch, q_head, table_stride, n_pages;
     uint32_t batch, q_heads, kv_heads, group, tiles, splits, chunk, page_shift, positions;  // positions: table_width * page_size
-    float scale;  // times log2 e
+    uint32_t q_wide;  // rows of q start at multiples of 16 bytes
+    float scale;      // times log2 e
 };
 
 struct Range {
@@ -213,10 +214,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
 #pragma unroll
     for (int i = 0; i < kKChunks; ++i) {
         const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = qp[d + 2 * j] | (uint32_t{qp[d + 2 * j + 1]} << 16);
-        qf[i] = __builtin_bit_cast(bf8, have ? v4u{w[0], w[1], w[2], w[3]} : v4u{0, 0, 0, 0});
+        qf[i] = __builtin_bit_cast(bf8, have ? load8(qp + d, p.q_wide) : v4u{0, 0, 0, 0});
     }
     const float scale = kE4M3 ? p.scale * p.k.scale[h] : p.scale;
     const uint8_t *kb = p.k.base + h * p.k.head, *vb = p.v.base + h * p.v.head;
@@ -378,27 +376,66 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
     }
 }
 
-// One workgroup joins the chunks of one query head.
+// One workgroup joins the chunks of one query head: the waves' lanes read the
+// chunks' maxima and sums side by side, then kDim / 4 lanes take four values
+// each of every (256 / (kDim / 4))-th chunk, and LDS adds what they have.
+constexpr uint32_t kJoinThreads = 256;
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int i = 32; i; i >>= 1) v = fmaxf(v, __shfl_xor(v, i));
+    return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int i = 32; i; i >>= 1) v += __shfl_xor(v, i);
+    return v;
+}
+
 template <int kDim>
-__global__ void __launch_bounds__(kDim) join_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p) {
+    constexpr uint32_t kQuads = kDim / 4, kGroups = kJoinThreads / kQuads;
+    __shared__ f4 s_part[kGroups][kQuads];
     const uint64_t row = blockIdx.x;
     const uint32_t b = static_cast<uint32_t>(row / p.q_heads);
     const Range range = range_of(p, b);
-    const uint32_t n = (range.len - range.base + p.chunk - 1) / p.chunk;
+    const uint32_t n = range.len > range.start ? (range.len - range.base + p.chunk - 1) / p.chunk : 0;
     const float *stats = p.stats + 2 * row * p.splits;
-    const float *part = p.part + row * p.splits * kDim + threadIdx.x;
-    const uint32_t used = range.len > range.start ? n : 0;
+    const uint32_t lane = threadIdx.x & 63u;
     float top = -INFINITY;
-    for (uint32_t i = 0; i < used; ++i) top = fmaxf(top, stats[2 * i]);
+    for (uint32_t i = lane; i < n; i += 64) top = fmaxf(top, stats[2 * i]);
+    top = wave_max(top);
     const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0, o = 0;
-    for (uint32_t i = 0; i < used; ++i) {
+    float sum = 0;
+    for (uint32_t i = lane; i < n; i += 64) sum += stats[2 * i + 1] * exp2_(stats[2 * i] - ref);
+    sum = wave_sum(sum);
+    const uint32_t d = threadIdx.x % kQuads, group = threadIdx.x / kQuads;
+    const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
+    f4 o = {};
+#pragma unroll 4
+    for (uint32_t i = group; i < n; i += kGroups) {
         const float f = exp2_(stats[2 * i] - ref);
-        sum += stats[2 * i + 1] * f;
-        o += part[uint64_t{i} * kDim] * f;
+        const f4 v = part[uint64_t{i} * kQuads];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += v[j] * f;
     }
-    p.out[row * kDim + threadIdx.x] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum == 0 ? 0.0f : o / sum));
-    if (threadIdx.x == 0 && p.lse) p.lse[row] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    s_part[group][d] = o;
+    __syncthreads();
+    if (threadIdx.x < kQuads) {
+#pragma unroll
+        for (uint32_t g = 1; g < kGroups; ++g) {
+            const f4 v = s_part[g][d];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += v[j];
+        }
+        const float inv = sum == 0 ? 0.0f : 1.0f / sum;
+        v2u out;
+        out.x = pack2(o[0] * inv, o[1] * inv);
+        out.y = pack2(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<v2u *>(p.out + row * kDim + 4 * d) = out;
+        if (threadIdx.x == 0 && p.lse) p.lse[row] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
 }
 
 // ---- Host ------------------------------------------------------------------
@@ -521,7 +558,7 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
         table_stride > kMaxStride || q_batch > kMaxStride || q_head > kMaxStride)
         return DF11_E_INVALID_ARG;
     if (batch == 0) return DF11_OK;
-    if (!q || !table || !lens || !out || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 1u) ||
+    if (!q || !table || !lens || !out || (reinterpret_cast<uintptr_t>(q) & 1u) || !aligned16(out) ||
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(starts) |
           reinterpret_cast<uintptr_t>(lse)) & 3u) ||
         !aligned16(workspace))
@@ -535,6 +572,7 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     p.starts = starts;
     p.out = out;
     p.lse = lse;
+    p.q_wide = aligned16(q) && (q_batch | q_head) % 8 == 0;
     p.q_batch = q_batch;
     p.q_head = q_head;
     p.table_stride = table_stride;
@@ -570,7 +608,7 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
         err = launch(c->head_dim == 64    ? join_kernel<64>
                      : c->head_dim == 128 ? join_kernel<128>
                                           : join_kernel<256>,
-                     static_cast<uint32_t>(rows), c->head_dim, st, p);
+                     static_cast<uint32_t>(rows), kJoinThreads, st, p);
     return launched(err);
 }
 

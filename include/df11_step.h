@@ -115,7 +115,8 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  * page_size]); position j lies in page page_table[b * table_stride + j /
  * page_size].  A table entry outside [0, n_pages) masks its positions.  With
  * s_j = scale * q . k_j:
- *   out[b, g, :] = sum_j exp(s_j) v_j / sum_j exp(s_j)   (BF16, contiguous)
+ *   out[b, g, :] = sum_j exp(s_j) v_j / sum_j exp(s_j)   (BF16, contiguous,
+ *                  16-byte aligned)
  *   lse[b, g]    = log sum_j exp(s_j)                    (32 bits; NULL = not wanted)
  * and where no position is left, zeros and -infinity.  What masked positions
  * hold, NaN included, does not matter.  Scores, maxima, sums and the weighted
