@@ -45,7 +45,12 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     return v > b ? v : b;
 }
 
-template <bool kAligned>
+// 16 bytes of a row that may start at any even address: the hardware loads and
+// stores them as they lie, without the compiler having to take them apart.
+struct __attribute__((packed, aligned(2))) Piece {
+    uint32_t w[4];
+};
+
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_kernel(const uint16_t *x, uint64_t row_stride, uint32_t cols, uint32_t blocks, uint64_t items,
                 uint8_t *codes, uint8_t *scales) {
@@ -60,9 +65,9 @@ quantize_kernel(const uint16_t *x, uint64_t row_stride, uint32_t cols, uint32_t 
         const uint32_t col = block * kBlock + part * 8;
         const uint16_t *src = x + row * row_stride + col;
         uint32_t w[4];  // two values each
-        if (kAligned && col + 8 <= cols) {
-            const v4u t = *reinterpret_cast<const v4u *>(src);
-            w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+        if (col + 8 <= cols) {
+            const Piece t = *reinterpret_cast<const Piece *>(src);
+            w[0] = t.w[0], w[1] = t.w[1], w[2] = t.w[2], w[3] = t.w[3];
         } else {
 #pragma unroll
             for (uint32_t i = 0; i < 4; ++i) {
@@ -119,7 +124,6 @@ __device__ __forceinline__ v4u expand8(uint32_t codes, float scale) {
     return v4u{expand2<0>(codes, scale), expand2<1>(codes, scale), expand2<2>(codes, scale), expand2<3>(codes, scale)};
 }
 
-template <bool kAligned>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_kernel(const uint8_t *codes, const uint8_t *scales, uint32_t cols, uint32_t blocks, uint64_t items,
                   uint16_t *out, uint64_t out_stride) {
@@ -137,8 +141,8 @@ dequantize_kernel(const uint8_t *codes, const uint8_t *scales, uint32_t cols, ui
         v4u o = expand8(code, __builtin_bit_cast(float, s << 23));
         if (s == kNanScale) o = v4u{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
         uint16_t *dst = out + row * out_stride + col;
-        if (kAligned && col + 8 <= cols) {
-            *reinterpret_cast<v4u *>(dst) = o;
+        if (col + 8 <= cols) {
+            *reinterpret_cast<Piece *>(dst) = Piece{o.x, o.y, o.z, o.w};
         } else {
             const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
@@ -486,8 +490,7 @@ df11_status quantize(const uint16_t *x, uint64_t rows, uint64_t cols, uint64_t r
     if (!x || !codes || !scales || !aligned16(codes) || (reinterpret_cast<uintptr_t>(x) & 1u)) return DF11_E_INVALID_ARG;
     const uint32_t blocks = static_cast<uint32_t>((cols + kBlock - 1) / kBlock);
     const uint64_t items = rows * blocks;
-    const bool al = aligned16(x) && row_stride % 8 == 0;
-    return launched(launch(al ? quantize_kernel<true> : quantize_kernel<false>, dim3(quant_grid(items)), kQuantThreads,
+    return launched(launch(quantize_kernel, dim3(quant_grid(items)), kQuantThreads,
                            static_cast<hipStream_t>(hip_stream), x, row_stride, static_cast<uint32_t>(cols), blocks,
                            items, codes, scales));
 }
@@ -500,8 +503,7 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
         return DF11_E_INVALID_ARG;
     const uint32_t blocks = static_cast<uint32_t>((cols + kBlock - 1) / kBlock);
     const uint64_t items = rows * blocks;
-    const bool al = aligned16(out) && out_stride % 8 == 0;
-    return launched(launch(al ? dequantize_kernel<true> : dequantize_kernel<false>, dim3(quant_grid(items)),
+    return launched(launch(dequantize_kernel, dim3(quant_grid(items)),
                            kQuantThreads, static_cast<hipStream_t>(hip_stream), codes, scales,
                            static_cast<uint32_t>(cols), blocks, items, out, out_stride));
 }

@@ -36,9 +36,9 @@ struct AppendParams {
     const uint16_t *ks, *vs;
     uint64_t k_token, k_head, v_token, v_head;  // source strides, elements
     const int64_t *slots;
-    uint64_t lanes;  // tokens * kv_heads * head_dim / 8
+    uint64_t lanes;  // tokens * per_token
     uint64_t n_slots;
-    uint32_t kv_heads, dim_shift, page_shift;  // head_dim / 8 = 1 << dim_shift
+    uint32_t per_token, dim_shift, page_shift;  // kv_heads * head_dim / 8; head_dim / 8 = 1 << dim_shift
 };
 
 __device__ __forceinline__ v4u load8(const uint16_t *p, bool aligned) {
@@ -49,23 +49,45 @@ __device__ __forceinline__ v4u load8(const uint16_t *p, bool aligned) {
     return v4u{w[0], w[1], w[2], w[3]};
 }
 
-// E4M3 of x / scale, saturating: the conversion itself turns magnitudes over
-// 448 into NaN, so they are held to 448 before it, and NaN is let through.
-__device__ __forceinline__ float to_e4m3_range(uint32_t bits, float scale) {
-    const float v = __builtin_bit_cast(float, bits) / scale;
+// x / scale for the eight values of a lane, rounded as a division: with r the
+// rounded reciprocal and q = x r, q + (x - q scale) r is the rounded quotient
+// (Markstein) as long as nothing over- or underflows; quotients of 1024 and
+// more are past E4M3 and keep q, and a scale without a normal reciprocal takes
+// the division itself.  E4M3's conversion turns magnitudes over 448 into NaN,
+// so they are held to 448 before it; NaN is let through.
+struct Scale {
+    float s, r;
+    bool plain;
+};
+
+__device__ __forceinline__ Scale scale_of(float s) {
+    const float r = 1.0f / s, a = fabsf(r);
+    return Scale{s, r, !(a >= 0x1p-100f && a <= 0x1p100f)};
+}
+
+__device__ __forceinline__ float to_e4m3_range(uint32_t bits, const Scale &s) {
+    const float x = __builtin_bit_cast(float, bits);
+    float v;
+    if (s.plain) {
+        v = x / s.s;
+    } else {
+        const float q = x * s.r;
+        v = fabsf(q) < 1024.0f ? fmaf(fmaf(-q, s.s, x), s.r, q) : q;
+    }
     return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
 }
 
 __device__ __forceinline__ v2u e4m3x8(v4u x, float scale) {
+    const Scale s = scale_of(scale);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         int r = 0;
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i] << 16, scale),
-                                            to_e4m3_range(w[2 * i] & 0xFFFF0000u, scale), r, false);
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i + 1] << 16, scale),
-                                            to_e4m3_range(w[2 * i + 1] & 0xFFFF0000u, scale), r, true);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i] << 16, s), to_e4m3_range(w[2 * i] & 0xFFFF0000u, s), r,
+                                            false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(w[2 * i + 1] << 16, s),
+                                            to_e4m3_range(w[2 * i + 1] & 0xFFFF0000u, s), r, true);
         o[i] = static_cast<uint32_t>(r);
     }
     return v2u{o[0], o[1]};
@@ -74,11 +96,13 @@ __device__ __forceinline__ v2u e4m3x8(v4u x, float scale) {
 template <bool kE4M3, bool kAligned>
 __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
     const uint32_t per_head = 1u << p.dim_shift;
-    for (uint64_t i = uint64_t{blockIdx.x} * 256 + threadIdx.x; i < p.lanes; i += uint64_t{gridDim.x} * 256) {
-        const uint32_t d = static_cast<uint32_t>(i) & (per_head - 1);
-        const uint64_t th = i >> p.dim_shift;
-        const uint64_t t = th / p.kv_heads;
-        const uint32_t h = static_cast<uint32_t>(th - t * p.kv_heads);
+    for (uint64_t base = uint64_t{blockIdx.x} * 256; base < p.lanes; base += uint64_t{gridDim.x} * 256) {
+        if (base + threadIdx.x >= p.lanes) break;
+        const uint64_t t0 = base / p.per_token;  // uniform
+        const uint32_t local = static_cast<uint32_t>(base - t0 * p.per_token) + threadIdx.x;
+        const uint32_t down = local / p.per_token, in = local - down * p.per_token;
+        const uint64_t t = t0 + down;
+        const uint32_t d = in & (per_head - 1), h = in >> p.dim_shift;
         const int64_t slot = p.slots[t];
         if (slot < 0 || static_cast<uint64_t>(slot) >= p.n_slots) continue;
         const v4u kv = load8(p.ks + t * p.k_token + h * p.k_head + 8 * d, kAligned);
@@ -126,6 +150,7 @@ constexpr uint32_t kStep = 32;
 constexpr uint32_t kMaxChunk = 1024;
 constexpr uint32_t kMinPage = 8, kMaxPage = 1024;
 constexpr uint32_t kHeadTile = 16;
+constexpr uint32_t kPad = 4;  // floats between a head's values in LDS: the heads start in different banks
 
 struct AttnParams {
     Pages k, v;
@@ -181,7 +206,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
     constexpr int kVWords = kPiece * (kE4M3 ? 1 : 2) / 4;  // dwords of a V piece
     __shared__ int32_t s_page[kMaxChunk / kMinPage + 1];
     __shared__ float s_stat[kWaves][2][kHeadTile];
-    __shared__ float s_out[kWaves][kHeadTile][kDim + 4];
+    extern __shared__ float s_out[];  // [kWaves][heads of a tile][kDim + kPad]
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -194,6 +219,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
     const uint32_t c0 = range.base + split * p.chunk;
     const uint32_t heads = min(kHeadTile, p.group - tile * kHeadTile);
     const uint32_t head0 = h * p.group + tile * kHeadTile;
+    const uint32_t out_heads = min(kHeadTile, p.group);  // as the host sizes s_out
     const bool single = p.splits == 1;
     if (c0 >= range.len && !(single && split == 0)) return;
     const uint32_t c1 = min(c0 + p.chunk, range.len);
@@ -341,10 +367,14 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
         s_stat[wave][1][r] = l;
     }
     // acc[j][c]: d = (4 q + c) * kPiece + j
+    if (have) {
+        float *to = s_out + (wave * out_heads + r) * (kDim + kPad) + 4 * q * kPiece;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) s_out[wave][r][(4 * q + c) * kPiece + j] = acc[j][c];
+            for (int j = 0; j < kPiece; j += 4)
+                *reinterpret_cast<f4 *>(to + c * kPiece + j) = f4{acc[j][c], acc[j + 1][c], acc[j + 2][c], acc[j + 3][c]};
+    }
     __syncthreads();
     const float v_scale = kE4M3 ? p.v.scale[h] : 1.0f;
     for (uint32_t i = threadIdx.x; i < heads * kDim; i += 64 * kWaves) {
@@ -358,7 +388,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
         for (uint32_t k = 0; k < kWaves; ++k) {
             const float f = exp2_(s_stat[k][0][g] - ref);
             sum += s_stat[k][1][g] * f;
-            o += s_out[k][g][d] * f;
+            o += s_out[(k * out_heads + g) * (kDim + kPad) + d] * f;
         }
         o *= v_scale;
         const uint64_t row = uint64_t{b} * p.q_heads + head0 + g;
@@ -446,9 +476,10 @@ struct Plain {
 };
 
 template <class... A>
-hipError_t launch(void (*fn)(A...), uint32_t grid, uint32_t threads, hipStream_t st, typename Plain<A>::type... a) {
+hipError_t launch(void (*fn)(A...), uint32_t grid, uint32_t threads, uint32_t lds, hipStream_t st,
+                  typename Plain<A>::type... a) {
     void *args[] = {&a...};
-    return hipLaunchKernel(reinterpret_cast<const void *>(fn), dim3(grid), dim3(threads), args, 0, st);
+    return hipLaunchKernel(reinterpret_cast<const void *>(fn), dim3(grid), dim3(threads), args, lds, st);
 }
 
 df11_status launched(hipError_t err) {
@@ -510,17 +541,17 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
     p.v_token = v_token;
     p.v_head = v_head;
     p.slots = slots;
-    p.kv_heads = c->kv_heads;
+    p.per_token = c->kv_heads * (c->head_dim / 8);
     p.dim_shift = log2_of(c->head_dim / 8);
     p.page_shift = log2_of(c->page_size);
     p.n_slots = c->n_pages * c->page_size;
-    p.lanes = (tokens * c->kv_heads) << p.dim_shift;
+    p.lanes = tokens * p.per_token;
     const bool al = aligned16(k) && aligned16(v) && (k_token | k_head | v_token | v_head) % 8 == 0;
     const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
     auto fn = e4m3 ? (al ? append_kernel<true, true> : append_kernel<true, false>)
                    : (al ? append_kernel<false, true> : append_kernel<false, false>);
     const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((p.lanes + 255) / 256, 1u << 20));
-    return launched(launch(fn, grid, 256, static_cast<hipStream_t>(hip_stream), p));
+    return launched(launch(fn, grid, 256, 0, static_cast<hipStream_t>(hip_stream), p));
 }
 
 struct Split {
@@ -603,12 +634,13 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
         case 128: fn = e4m3 ? attend_kernel<128, true> : attend_kernel<128, false>; break;
         default: fn = e4m3 ? attend_kernel<256, true> : attend_kernel<256, false>; break;
     }
-    hipError_t err = launch(fn, static_cast<uint32_t>(groups), 64 * kWaves, st, p);
+    hipError_t err = launch(fn, static_cast<uint32_t>(groups), 64 * kWaves,
+                            kWaves * std::min(kHeadTile, p.group) * (c->head_dim + kPad) * sizeof(float), st, p);
     if (err == hipSuccess && p.splits > 1)
         err = launch(c->head_dim == 64    ? join_kernel<64>
                      : c->head_dim == 128 ? join_kernel<128>
                                           : join_kernel<256>,
-                     static_cast<uint32_t>(rows), kJoinThreads, st, p);
+                     static_cast<uint32_t>(rows), kJoinThreads, 0, st, p);
     return launched(err);
 }
 
