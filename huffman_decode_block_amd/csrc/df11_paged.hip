@@ -16,6 +16,7 @@ using df11w::v4u;
 
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 }
 
 // ---- Attention of one token ------------------------------------------------
-// A sequence's positions are cut into chunks of `chunk`; a workgroup takes one
+// A sequence's positions are cut into up to `splits` chunks of the same size, a
+// multiple of 128, by the lengths as the device finds them; a workgroup takes one
 // chunk of one cache head for up to 16 of its query heads, its four waves the
 // chunk's steps of 32 positions in turn.  Each wave keeps the running maximum,
 // sum and weighted values of what it has seen, the waves join in LDS, and a
@@ -147,7 +149,8 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;
-constexpr uint32_t kMaxChunk = 1024;
+constexpr uint32_t kMinChunk = kWaves * kStep;
+constexpr uint32_t kMaxChunk = 4096;
 constexpr uint32_t kMinPage = 8, kMaxPage = 1024;
 constexpr uint32_t kHeadTile = 16;
 constexpr uint32_t kPad = 4;  // floats between a head's values in LDS: the heads start in different banks
@@ -161,13 +164,14 @@ struct AttnParams {
     float *part;   // [batch * q_heads][splits][head_dim], weighted values over their sum
     float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
     uint64_t q_batch, q_head, table_stride, n_pages;
-    uint32_t batch, q_heads, kv_heads, group, tiles, splits, chunk, page_shift, positions;  // positions: table_width * page_size
+    uint32_t batch, q_heads, kv_heads, group, tiles, splits, page_shift, positions;  // positions: table_width * page_size
     uint32_t q_wide;  // rows of q start at multiples of 16 bytes
     float scale;      // times log2 e
 };
 
 struct Range {
     uint32_t start, len, base;  // base: start down to a multiple of the step
+    uint32_t chunk, chunks;     // positions of a chunk, chunks that hold any
 };
 
 __device__ __forceinline__ Range range_of(const AttnParams &p, uint32_t b) {
@@ -176,6 +180,9 @@ __device__ __forceinline__ Range range_of(const AttnParams &p, uint32_t b) {
     r.len = min(static_cast<uint32_t>(max(len, 0)), p.positions);
     r.start = min(static_cast<uint32_t>(max(start, 0)), r.len);
     r.base = r.start & ~(kStep - 1);
+    const uint32_t span = r.len > r.start ? r.len - r.base : 0;
+    r.chunk = ((span + p.splits - 1) / p.splits + kMinChunk - 1) / kMinChunk * kMinChunk;
+    r.chunks = span ? (span + r.chunk - 1) / r.chunk : 0;
     return r;
 }
 
@@ -198,31 +205,48 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Waves of a SIMD that the registers are held to (without it the compiler takes
+// more and leaves one or two): 8 x 32,768 positions in E4M3 101 -> 99 us, 32 x
+// 2,048 BF16 positions of 8 heads of 64 29.2 -> 28.1 us.
+constexpr int waves_for(int dim, bool e4m3) { return dim == 64 ? 4 : dim == 128 ? (e4m3 ? 4 : 3) : 1; }
+
 template <int kDim, bool kE4M3>
-__global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim, kE4M3))))
+attend_kernel(AttnParams p) {
     constexpr int kPiece = kDim / 16;              // values of a V row in a lane; tiles of out^T
     constexpr int kKChunks = kDim / 32;            // matrix instructions over d
     constexpr int kKLoads = kE4M3 ? kDim / 64 : kKChunks;  // 16-byte loads of a K row in a lane
     constexpr int kVWords = kPiece * (kE4M3 ? 1 : 2) / 4;  // dwords of a V piece
     __shared__ int32_t s_page[kMaxChunk / kMinPage + 1];
     __shared__ float s_stat[kWaves][2][kHeadTile];
-    extern __shared__ float s_out[];  // [kWaves][heads of a tile][kDim + kPad]
+    extern __shared__ __attribute__((aligned(16))) float s_out[];  // [kWaves][heads of a tile][kDim + kPad]
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t split = blockIdx.x % p.splits;
-    uint32_t rest = blockIdx.x / p.splits;
+    // chunks of all heads of all sequences before the next chunks: workgroups
+    // go round the 8 XCDs, and the first chunks, which every sequence has,
+    // spread over all of them
+    const uint32_t units = p.batch * p.kv_heads * p.tiles;
+    const uint32_t split = blockIdx.x / units;
+    uint32_t rest = blockIdx.x - split * units;
     const uint32_t tile = rest % p.tiles;
     rest /= p.tiles;
     const uint32_t h = rest % p.kv_heads, b = rest / p.kv_heads;
     const Range range = range_of(p, b);
-    const uint32_t c0 = range.base + split * p.chunk;
+    const uint32_t c0 = range.base + split * range.chunk;
     const uint32_t heads = min(kHeadTile, p.group - tile * kHeadTile);
     const uint32_t head0 = h * p.group + tile * kHeadTile;
     const uint32_t out_heads = min(kHeadTile, p.group);  // as the host sizes s_out
     const bool single = p.splits == 1;
-    if (c0 >= range.len && !(single && split == 0)) return;
-    const uint32_t c1 = min(c0 + p.chunk, range.len);
+    if (split >= range.chunks && !single) {  // nothing here: the join gives it no weight
+        for (uint32_t g = threadIdx.x; g < heads; g += 64 * kWaves) {
+            float *to = p.stats + 2 * ((uint64_t{b} * p.q_heads + head0 + g) * p.splits + split);
+            to[0] = -INFINITY;
+            to[1] = 0;
+        }
+        return;
+    }
+    const uint32_t c1 = split < range.chunks ? min(c0 + range.chunk, range.len) : c0;  // a single chunk may be empty
 
     // the chunk's pages; -1 masks
     const uint32_t first = c0 >> p.page_shift;
@@ -247,11 +271,9 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
     const uint32_t in_page = (1u << p.page_shift) - 1;
     __syncthreads();
 
-    float m = -INFINITY, l = 0;  // m over all lanes of a head, l over this lane's positions
-    f4 acc[kPiece] = {};
-    for (uint32_t p0 = c0 + wave * kStep; p0 < c1; p0 += kWaves * kStep) {
-        // K rows: lane r has position r of each half
-        v4u kr[2][kKLoads];
+    // K rows of a step: lane r has position r of each half
+    v4u kr[2][kKLoads];
+    auto load_k = [&](uint32_t p0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint32_t pos = min(p0 + 16 * t + r, c1 - 1);
@@ -260,31 +282,39 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
 #pragma unroll
             for (int i = 0; i < kKLoads; ++i) kr[t][i] = *reinterpret_cast<const v4u *>(row + 64 * i);
         }
-        // V rows: positions 4 q + 0..3 of each half
-        uint32_t vr[8][kVWords];
-        bool live[8];
+    };
+    // V rows of a step: positions 4 q + 0..3 of each half (of one page: pages
+    // hold multiples of 8); live: those that count
+    typedef uint32_t VRow __attribute__((ext_vector_type(kVWords)));
+    typedef VRow VRowInMemory __attribute__((aligned(4)));
+    VRow vr[8];
+    bool live[8];
+    auto load_v = [&](uint32_t p0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t pos = p0 + 16 * (i / 4) + 4 * q + (i & 3);
-            const uint32_t at = min(pos, c1 - 1);
-            const int32_t page = s_page[(at >> p.page_shift) - first];
-            live[i] = pos >= range.start && pos < c1 && page >= 0;
-            const uint8_t *row = vb + static_cast<uint64_t>(max(page, 0)) * p.v.page + uint64_t{at & in_page} * p.v.row +
-                                 r * (kVWords * 4);
-            if constexpr (kVWords == 1) {
-                vr[i][0] = *reinterpret_cast<const uint32_t *>(row);
-            } else if constexpr (kVWords == 2) {
-                const v2u t = *reinterpret_cast<const v2u *>(row);
-                vr[i][0] = t.x, vr[i][1] = t.y;
-            } else {
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t pos0 = p0 + 16 * t + 4 * q, at0 = min(pos0, c1 - 1);
+            const int32_t page = s_page[(at0 >> p.page_shift) - first];
+            const uint8_t *rows = vb + static_cast<uint64_t>(max(page, 0)) * p.v.page + r * (kVWords * 4);
 #pragma unroll
-                for (int j = 0; j < kVWords / 4; ++j) {
-                    const v4u t = *reinterpret_cast<const v4u *>(row + 16 * j);
-                    vr[i][4 * j] = t.x, vr[i][4 * j + 1] = t.y, vr[i][4 * j + 2] = t.z, vr[i][4 * j + 3] = t.w;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t pos = pos0 + i, at = min(pos, c1 - 1);
+                live[4 * t + i] = pos >= range.start && pos < c1 && page >= 0;
+                const uint8_t *row = rows + uint64_t{at & in_page} * p.v.row;
+                vr[4 * t + i] = *reinterpret_cast<const VRowInMemory *>(row);
             }
         }
-        // scores
+    };
+
+    float m = -INFINITY, l = 0;  // m over all lanes of a head, l over this lane's positions
+    f4 acc[kPiece] = {};
+    uint32_t p0 = c0 + wave * kStep;
+    if (p0 < c1) {
+        load_k(p0);
+        load_v(p0);
+    }
+    while (p0 < c1) {
+        // the registers of K and V are loaded again as soon as they are used up
+        const uint32_t next = p0 + kWaves * kStep;
         f4 s[2] = {};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -297,6 +327,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
                     kw = kr[t][kE4M3 ? 0 : i];
                 s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[i], s[t], 0, 0, 0);
             }
+        if (next < c1) load_k(next);
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -329,9 +360,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
         const bool all = live[0] && live[1] && live[2] && live[3] && live[4] && live[5] && live[6] && live[7];
         if (!__all(all)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int j = 0; j < kVWords; ++j) vr[i][j] = live[i] ? vr[i][j] : 0u;
+            for (int i = 0; i < 8; ++i) vr[i] = live[i] ? vr[i] : VRow(0);
         }
 #pragma unroll
         for (int j = 0; j < kPiece; j += 2) {
@@ -357,6 +386,8 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
                 acc[j + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w_lo, o, 0, 0, 0);
             }
         }
+        if (next < c1) load_v(next);
+        p0 = next;
     }
 
     // join the waves
@@ -406,9 +437,12 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttnParams p) {
     }
 }
 
-// One workgroup joins the chunks of one query head: the waves' lanes read the
-// chunks' maxima and sums side by side, then kDim / 4 lanes take four values
-// each of every (256 / (kDim / 4))-th chunk, and LDS adds what they have.
+// One workgroup joins the chunks of one query head: every wave's lanes read the
+// chunks' maxima and sums side by side, kDim / 4 lanes take four values each of
+// every kGroups-th chunk, and LDS adds what they have.  Bound by latency: the
+// maxima, the sums and the first chunks' values are loaded without waiting for
+// one another (a chunk without positions has left its values unwritten; they
+// are read and given no weight).
 constexpr uint32_t kJoinThreads = 256;
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -428,27 +462,42 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p) {
     constexpr uint32_t kQuads = kDim / 4, kGroups = kJoinThreads / kQuads;
     __shared__ f4 s_part[kGroups][kQuads];
     const uint64_t row = blockIdx.x;
-    const uint32_t b = static_cast<uint32_t>(row / p.q_heads);
-    const Range range = range_of(p, b);
-    const uint32_t n = range.len > range.start ? (range.len - range.base + p.chunk - 1) / p.chunk : 0;
-    const float *stats = p.stats + 2 * row * p.splits;
-    const uint32_t lane = threadIdx.x & 63u;
-    float top = -INFINITY;
-    for (uint32_t i = lane; i < n; i += 64) top = fmaxf(top, stats[2 * i]);
+    const uint32_t lane = threadIdx.x & 63u, d = threadIdx.x % kQuads, group = threadIdx.x / kQuads;
+    const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row * p.splits;
+    const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
+    constexpr int kAhead = 4;
+    v2f first = {-INFINITY, 0};
+    if (lane < p.splits) first = stats[lane];
+    f4 v[kAhead] = {};
+    float m[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+        const uint32_t i = group + a * kGroups;
+        m[a] = -INFINITY;
+        if (i < p.splits) {
+            m[a] = stats[i].x;
+            v[a] = part[uint64_t{i} * kQuads];
+        }
+    }
+    float top = first.x;
+    for (uint32_t i = lane + 64; i < p.splits; i += 64) top = fmaxf(top, stats[i].x);
     top = wave_max(top);
     const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0;
-    for (uint32_t i = lane; i < n; i += 64) sum += stats[2 * i + 1] * exp2_(stats[2 * i] - ref);
+    float sum = first.y * exp2_(first.x - ref);
+    for (uint32_t i = lane + 64; i < p.splits; i += 64) sum += stats[i].y * exp2_(stats[i].x - ref);
     sum = wave_sum(sum);
-    const uint32_t d = threadIdx.x % kQuads, group = threadIdx.x / kQuads;
-    const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
     f4 o = {};
-#pragma unroll 4
-    for (uint32_t i = group; i < n; i += kGroups) {
-        const float f = exp2_(stats[2 * i] - ref);
-        const f4 v = part[uint64_t{i} * kQuads];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += v[j] * f;
+    for (int a = 0; a < kAhead; ++a) {
+        const float f = exp2_(m[a] - ref);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += m[a] == -INFINITY ? 0.0f : v[a][j] * f;
+    }
+    for (uint32_t i = group + kAhead * kGroups; i < p.splits; i += kGroups) {
+        const float mi = stats[i].x, f = exp2_(mi - ref);
+        const f4 w = part[uint64_t{i} * kQuads];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += mi == -INFINITY ? 0.0f : w[j] * f;
     }
     s_part[group][d] = o;
     __syncthreads();
@@ -554,20 +603,20 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
     return launched(launch(fn, grid, 256, 0, static_cast<hipStream_t>(hip_stream), p));
 }
 
-struct Split {
-    uint32_t chunk, splits;
-};
+// Chunks of a sequence.  The device cuts what a sequence really holds, so the
+// page table's width only bounds them: as many as give each of 256 compute
+// units a workgroup, no more than chunks of kMinChunk, and enough that none
+// exceeds kMaxChunk.  Measured with 256, 512 and 1,024 workgroups wanted: 8 x
+// 32,768 BF16 positions of 8 heads (1.07 GB) 188, 188 and 190 us; one sequence of
+// 65,536 52.1, 53.2 and 55.9; 16 windows of 1,024 over 4 heads of 256 17.3, 20.2
+// and 22.7.
+constexpr uint64_t kWantGroups = 256;
 
-// Chunks that give every compute unit several workgroups, where there are
-// positions enough.  The page table's width bounds the lengths, which only
-// the device knows.
-Split split_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions) {
-    Split s;
-    s.chunk = 256;
-    while (s.chunk < kMaxChunk && batch * kv_heads * tiles * ((positions + s.chunk - 1) / s.chunk) > 4096) s.chunk *= 2;
-    s.splits = static_cast<uint32_t>((positions + s.chunk - 1) / s.chunk);
-    s.splits = std::max(s.splits, 1u);
-    return s;
+uint32_t splits_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions) {
+    const uint64_t units = std::max<uint64_t>(batch * kv_heads * tiles, 1);
+    const uint64_t want = (kWantGroups + units - 1) / units;
+    const uint64_t most = (positions + kMinChunk - 1) / kMinChunk, least = (positions + kMaxChunk - 1) / kMaxChunk;
+    return static_cast<uint32_t>(std::max(std::min(want, most), std::max<uint64_t>(least, 1)));
 }
 
 uint64_t attention_workspace(uint64_t rows, uint32_t head_dim, uint32_t splits) {
@@ -616,9 +665,7 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     p.page_shift = log2_of(c->page_size);
     p.positions = static_cast<uint32_t>(width * c->page_size);
     p.scale = scale * kLog2e;
-    const Split s = split_of(batch, p.kv_heads, p.tiles, p.positions);
-    p.chunk = s.chunk;
-    p.splits = s.splits;
+    p.splits = splits_of(batch, p.kv_heads, p.tiles, p.positions);
     const uint64_t rows = batch * q_heads;
     if (workspace_bytes < attention_workspace(rows, c->head_dim, p.splits)) return DF11_E_BUFFER_TOO_SMALL;
     if (p.splits > 1 && !workspace) return DF11_E_INVALID_ARG;
@@ -659,8 +706,8 @@ extern "C" uint64_t df11_paged_attention_workspace_bytes(uint64_t batch, uint64_
                                                          uint32_t head_dim, uint32_t page_size, uint64_t table_width) {
     if (!page_ok(page_size) || !attention_sizes_ok(batch, q_heads, kv_heads, page_size, table_width)) return 0;
     const uint32_t group = static_cast<uint32_t>(q_heads / kv_heads);
-    const Split s = split_of(batch, kv_heads, (group + kHeadTile - 1) / kHeadTile, table_width * page_size);
-    return attention_workspace(batch * q_heads, head_dim, s.splits);
+    const uint32_t tiles = (group + kHeadTile - 1) / kHeadTile;
+    return attention_workspace(batch * q_heads, head_dim, splits_of(batch, kv_heads, tiles, table_width * page_size));
 }
 
 extern "C" df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch,
