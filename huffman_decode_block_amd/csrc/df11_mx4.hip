@@ -194,71 +194,122 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// Token form: a workgroup takes 16 rows of w, its waves share k between them
-// and add their sums in LDS.  A lane reads 16 bytes of codes at a time, which
-// is one block of one row: lane l has row l % 16 and block 4 s + l / 16 of
-// step s.  The matrix instruction's k index is ours to choose, as long as both
-// operands agree: its i-th instruction of a step takes codes 8 i .. 8 i + 7 of
-// every lane's block, so nothing moves between lanes and one scale serves all
-// of a lane's codes.
-constexpr uint32_t kTokenWaves = 8;
+typedef __attribute__((address_space(3))) void *LdsPtr;
 
-template <int kRows>  // tiles of 16 rows of w
-__global__ void __launch_bounds__(64 * kTokenWaves)
+// Waits for this wave's loads, those into LDS among them: a barrier alone does
+// not (vmcnt 0; the other counters as they are).
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// Token form, for few rows: a workgroup takes 16 kRows rows of w by kX of x, its
+// waves share k between them and add their sums in LDS.  A lane reads 16 bytes
+// of codes at a time, which is one block of one row: lane l has row l % 16 and
+// block 4 s + l / 16 of step s.  The matrix instruction's k index is ours to
+// choose, as long as both operands agree: its i-th instruction of a step takes
+// codes 8 i .. 8 i + 7 of every lane's block, so nothing moves between lanes and
+// one scale serves all of a lane's codes.
+// Bound by the path of vector loads as soon as those are not few and wide: x
+// comes in rows of 256 bytes a step by loads into the wave's own part of LDS
+// (one instruction for 4 rows; read into registers in the order of the matrix
+// instruction it took four for 16 rows, and 16 x 4096 x 14336 21 us, 7 without
+// them), and the scales of four steps in one load of 16 bytes (a byte for each
+// step: 1 x 128256 x 4096 90 us against 71).  Piece c of row i of x lies at
+// c ^ (i % 16), as in the tile form.
+template <int kX, int kRows, int kWaves, int kAhead, bool kWide>
+__global__ void __launch_bounds__(64 * kWaves)
 token_kernel(MulParams p) {
-    __shared__ float s_sum[kTokenWaves][kRows][16 * 16];
-    constexpr uint32_t kAhead = 4;  // steps whose codes are in flight together
+    constexpr int kM = kX < 16 ? 1 : kX / 16;  // tiles of x
+    constexpr uint32_t kGroup = 4;             // steps whose scales are loaded together
+    constexpr uint32_t kStepBytes = kX * 256, kWaveBytes = kAhead * kStepBytes;
+    constexpr uint32_t kSumBytes = kM * kRows * 1024;  // of a wave
+    __shared__ __attribute__((aligned(1024))) uint8_t s_x[kWaves * (kWaveBytes > kSumBytes ? kWaveBytes : kSumBytes)];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t n0 = blockIdx.x * 16 * kRows;
-    const uint32_t rows_n = min(16u * kRows, p.n - n0);
+    const uint32_t n0 = blockIdx.x * 16 * kRows, m0 = blockIdx.y * kX;
+    const uint32_t rows_n = min(16u * kRows, p.n - n0), rows_m = min(uint32_t{kX}, p.m - m0);
     const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
     const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
-    const uint32_t row_bytes = static_cast<uint32_t>(p.x_stride) * 2;
-    const Rsrc xr = rsrc(p.x, (p.m - 1) * row_bytes + p.blocks * kBlock * 2);
-    const uint32_t x_row = r < p.m ? r * row_bytes : kOff;
-    f4 acc[kRows] = {};
-    const uint32_t steps = (p.blocks + 3) / 4;
-    for (uint32_t s0 = wave; s0 < steps; s0 += kTokenWaves * kAhead) {
-        v4u c[kAhead][kRows], x[kAhead][4];
-        uint32_t sb[kAhead][kRows];
-#pragma unroll
-        for (uint32_t a = 0; a < kAhead; ++a) {
-            const uint32_t block = 4 * (s0 + a * kTokenWaves) + q;
-            const uint32_t at = block < p.blocks ? r * p.blocks + block : kOff / 16;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.x_stride) * 2, k_bytes = p.blocks * kBlock * 2;
+    const Rsrc xr = rsrc(p.x + uint64_t{m0} * p.x_stride, (rows_m - 1) * row_bytes + k_bytes);
+    uint8_t *mine = s_x + wave * kWaveBytes;
+    f4 acc[kM][kRows] = {};
+    for (uint32_t g0 = wave * kGroup * 4; g0 < p.blocks; g0 += kWaves * kGroup * 4) {
+        uint32_t sc[kRows][kGroup];  // byte i of word a: the scale of block i of the group's step a in row r
+        if (kWide) {
 #pragma unroll
             for (uint32_t t = 0; t < kRows; ++t) {
-                c[a][t] = __builtin_amdgcn_raw_buffer_load_b128(wr, (at + 16 * t * p.blocks) * 16, 0, 0);
-                sb[a][t] = __builtin_amdgcn_raw_buffer_load_b8(sr, at + 16 * t * p.blocks, 0, 0);
+                const v4u v = __builtin_amdgcn_raw_buffer_load_b128(sr, (r + 16 * t) * p.blocks + g0, 0, 0);
+                sc[t][0] = v.x, sc[t][1] = v.y, sc[t][2] = v.z, sc[t][3] = v.w;
             }
-            const uint32_t x_at = block < p.blocks ? x_row + block * kBlock * 2 : kOff;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[a][i] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_at + 16 * i, 0, 0);
         }
-        __builtin_amdgcn_sched_barrier(0);  // all loads are on their way before the first is waited for
 #pragma unroll
-        for (uint32_t a = 0; a < kAhead; ++a) {
+        for (uint32_t b0 = 0; b0 < kGroup; b0 += kAhead) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // what was read from LDS before has arrived (lgkmcnt 0)
+            v4u c[kAhead][kRows];
 #pragma unroll
-            for (uint32_t t = 0; t < kRows; ++t) {
-                const float scale = __builtin_bit_cast(float, (sb[a][t] & 255u) << 23);
+            for (uint32_t a = 0; a < kAhead; ++a) {
+                const uint32_t block0 = g0 + 4 * (b0 + a);  // past the end at most in the last group
+                const uint32_t k0 = min(block0, p.blocks) * kBlock * 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, expand8(c[a][t][i], scale)),
-                                                                     __builtin_bit_cast(bf8, x[a][i]), acc[t], 0, 0, 0);
+                for (uint32_t j = 0; j < kX / 4; ++j) {
+                    const uint32_t row = 4 * j + q, piece = (r ^ (row & 15u)) * 16;
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(mine + a * kStepBytes + j * 1024), 16,
+                                                             k0 + piece < k_bytes ? row * row_bytes + piece : kOff,
+                                                             __builtin_amdgcn_readfirstlane(k0), 0, 0);
+                }
+                const uint32_t at = block0 + q < p.blocks ? r * p.blocks + block0 + q : kOff / 16;
+#pragma unroll
+                for (uint32_t t = 0; t < kRows; ++t) {
+                    c[a][t] = __builtin_amdgcn_raw_buffer_load_b128(wr, (at + 16 * t * p.blocks) * 16, 0, 0);
+                    if (!kWide)
+                        sc[t][b0 + a] = (__builtin_amdgcn_raw_buffer_load_b8(sr, at + 16 * t * p.blocks, 0, 0) & 255u)
+                                        << (8 * q);
+                }
+            }
+            arrived();
+#pragma unroll
+            for (uint32_t a = 0; a < kAhead; ++a) {
+                float scale[kRows];
+#pragma unroll
+                for (uint32_t t = 0; t < kRows; ++t)
+                    scale[t] = __builtin_bit_cast(float, (sc[t][b0 + a] >> (8 * q) & 255u) << 23);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    bf8 xf[kM];
+#pragma unroll
+                    for (uint32_t u = 0; u < kM; ++u) {
+                        const uint32_t row = kX < 16 ? r % kX : 16 * u + r;  // rows past kX repeat: columns not stored
+                        xf[u] = *reinterpret_cast<const bf8 *>(mine + a * kStepBytes + row * 256 +
+                                                               ((4 * q + i) ^ (row & 15u)) * 16);
+                    }
+#pragma unroll
+                    for (uint32_t t = 0; t < kRows; ++t) {
+                        const bf8 wf = __builtin_bit_cast(bf8, expand8(c[a][t][i], scale[t]));
+#pragma unroll
+                        for (uint32_t u = 0; u < kM; ++u)
+                            acc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[u], acc[u][t], 0, 0, 0);
+                    }
+                }
             }
         }
     }
     // acc: column lane % 16 (a row of x), rows 4 (lane / 16) + 0..3 (of w)
+    __syncthreads();  // the sums go where x was
+    float *sum = reinterpret_cast<float *>(s_x);
 #pragma unroll
-    for (uint32_t t = 0; t < kRows; ++t) *reinterpret_cast<f4 *>(&s_sum[wave][t][r * 16 + 4 * q]) = acc[t];
+    for (uint32_t u = 0; u < kM; ++u)
+#pragma unroll
+        for (uint32_t t = 0; t < kRows; ++t)
+            *reinterpret_cast<f4 *>(sum + ((wave * kM + u) * kRows + t) * 256 + r * 16 + 4 * q) = acc[u][t];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < kRows * 256; i += 64 * kTokenWaves) {
-        const uint32_t t = i / 256, row = i % 256 / 16, col = n0 + 16 * t + i % 16;
+    for (uint32_t i = threadIdx.x; i < kM * kRows * 256; i += 64 * kWaves) {
+        // neighbouring threads take neighbouring columns of a row
+        const uint32_t col = i % (16 * kRows), row = i / (16 * kRows);
+        const uint32_t at = ((row / 16) * kRows + col / 16) * 256 + row % 16 * 16 + col % 16;
         float v = 0;
 #pragma unroll
-        for (uint32_t k = 0; k < kTokenWaves; ++k) v += s_sum[k][t][i % 256];
-        if (row < p.m && col < p.n)
-            p.y[uint64_t{row} * p.y_stride + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+        for (uint32_t k = 0; k < kWaves; ++k) v += sum[k * kM * kRows * 256 + at];
+        if (row < rows_m && col < rows_n)
+            p.y[uint64_t{m0 + row} * p.y_stride + n0 + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
 }
 
@@ -275,12 +326,6 @@ token_kernel(MulParams p) {
 constexpr uint32_t kStageK = 128;
 constexpr uint32_t kStageBlocks = kStageK / kBlock;
 constexpr uint32_t kRowBytes = kStageK * 2;
-
-typedef __attribute__((address_space(3))) void *LdsPtr;
-
-// Waits for this wave's loads, those into LDS among them: a barrier alone does
-// not (vmcnt 0; the other counters as they are).
-__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 template <int kWavesM, int kWavesN, int kTilesM, bool kSplit>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN) __attribute__((amdgpu_waves_per_eu(2)))
@@ -530,7 +575,7 @@ Form form_of(uint64_t m, uint64_t n, uint64_t k) {
     Form f = {};
     f.token = m <= 16;
     if (f.token) {
-        f.variant = n > 8192 ? 2 : 1;
+        f.variant = m <= 4 ? 0x11 : 0x21;
         return f;
     }
     f.variant = m > 128 ? 256 : m > 64 ? 128 : m > 32 ? 64 : 32;
@@ -601,11 +646,15 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         p.x_stride = width;
     }
     if (f.token) {
-        const dim3 grid(static_cast<uint32_t>((n + 16 * f.variant - 1) / (16 * f.variant)));
-        err = launch(f.variant == 1   ? token_kernel<1>
-                     : f.variant == 2 ? token_kernel<2>
-                                      : token_kernel<4>,
-                     grid, 64 * kTokenWaves, st, p);
+        const bool wide = p.blocks % 16 == 0 && aligned16(scales);
+        switch (f.variant) {
+#define C(v, x, b, w, a) case v: { const dim3 grid(static_cast<uint32_t>((n + 16 * b - 1) / (16 * b)), static_cast<uint32_t>((m + x - 1) / (x))); \
+   err = wide ? launch(token_kernel<x, b, w, a, true>, grid, 64 * w, st, p) : launch(token_kernel<x, b, w, a, false>, grid, 64 * w, st, p); break; }
+            C(0x11, 4, 1, 8, 4) C(0x12, 4, 2, 8, 4) C(0x14, 4, 4, 8, 4) C(0x15, 4, 1, 4, 4) C(0x16, 4, 2, 4, 4) C(0x17, 4, 4, 4, 4) C(0x18, 4, 1, 8, 2)
+            C(0x21, 16, 1, 8, 4) C(0x22, 16, 2, 8, 4) C(0x24, 16, 4, 8, 4) C(0x25, 16, 1, 8, 2) C(0x26, 16, 2, 8, 2) C(0x27, 16, 4, 8, 2) C(0x28, 16, 4, 4, 4) C(0x29, 16, 2, 4, 4) C(0x2a, 16, 1, 4, 4)
+            C(0x41, 32, 1, 8, 2) C(0x42, 32, 2, 8, 2) C(0x44, 32, 4, 8, 2) C(0x45, 32, 1, 4, 4) C(0x46, 32, 2, 4, 4) C(0x47, 32, 4, 4, 2)
+            C(0x81, 64, 1, 8, 1) C(0x82, 64, 2, 8, 1) C(0x84, 64, 4, 8, 1) C(0x87, 64, 4, 4, 2)
+        }
         return launched(err);
     }
     p.tiles_m = f.tiles_m;
