@@ -183,8 +183,6 @@ struct MulParams {
     uint32_t y_wide;        // rows of y start at multiples of 16 bytes
     // tile form
     uint32_t tiles_m, tiles_n;
-    float *part;  // [splits][m][n_padded] where k is split
-    uint32_t splits, split_stages, n_padded;
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -313,9 +311,9 @@ token_kernel(MulParams p) {
     }
 }
 
-// Tile form, for many rows: a workgroup computes a tile of 16 kTilesM kWavesM
-// rows of x by 64 kWavesN rows of w, a wave 16 kTilesM by 64 of it, in stages
-// of 128 along k.  x goes to LDS by loads that write there directly, two
+// Tile form, for many rows: a workgroup computes a tile of 16 kTiles rows of x
+// by 256 rows of w, each of its four waves 16 kTiles by 64 of it, in stages of
+// 128 along k.  x goes to LDS by loads that write there directly, two
 // stages, the next one loading while one is computed.  The codes go from
 // memory to the registers of the waves that use them and are expanded there:
 // a lane's 16 bytes are one block of 32, k as in the token form.  A row of x
@@ -327,31 +325,26 @@ constexpr uint32_t kStageK = 128;
 constexpr uint32_t kStageBlocks = kStageK / kBlock;
 constexpr uint32_t kRowBytes = kStageK * 2;
 
-template <int kWavesM, int kWavesN, int kTilesM, bool kSplit>
-__global__ void __launch_bounds__(64 * kWavesM * kWavesN) __attribute__((amdgpu_waves_per_eu(2)))
+constexpr uint32_t kTileWaves = 4;
+
+template <int kTiles>
+__global__ void __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2)))
 tile_kernel(MulParams p) {
-    constexpr int kWaves = kWavesM * kWavesN;
-    constexpr uint32_t kRowsM = 16 * kTilesM * kWavesM, kRowsN = 64 * kWavesN;
-    constexpr int kLoads = kRowsM / 4 / kWaves;  // a wave's loads of a stage, 4 rows each
-    static_assert(kWaves % 4 == 0 && kRowsM / 4 % kWaves == 0, "whole loads, the same piece in all of a lane's");
+    constexpr uint32_t kRowsM = 16 * kTiles, kRowsN = 64 * kTileWaves;
+    constexpr int kLoads = kRowsM / 4 / kTileWaves;  // a wave's loads of a stage: 4 rows each, 16 rows from one another
     __shared__ __attribute__((aligned(1024))) uint8_t s_x[2 * kRowsM * kRowBytes];
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t wm = wave % kWavesM, wn = wave / kWavesM;
     // workgroups go round the 8 XCDs; each XCD takes a run of neighbouring
     // tiles, so that its L2 holds what they share
     const uint32_t tiles = p.tiles_m * p.tiles_n;
-    uint32_t id = blockIdx.x;
-    const uint32_t split = kSplit ? id / tiles : 0;
-    id -= split * tiles;
+    const uint32_t id = blockIdx.x;
     const uint32_t per = tiles / 8, more = tiles % 8, xcd = id % 8;
     const uint32_t t = xcd * per + min(xcd, more) + id / 8;
     const uint32_t m0 = (t % p.tiles_m) * kRowsM, n0 = (t / p.tiles_m) * kRowsN;
 
     const uint32_t stages = (p.blocks + kStageBlocks - 1) / kStageBlocks;
-    const uint32_t first = kSplit ? split * p.split_stages : 0;
-    const uint32_t last = kSplit ? min(first + p.split_stages, stages) : stages;
 
     // Rows past m and n, and blocks past k, lie past their resource and read as
     // zero; the scalar offsets stay within it.
@@ -364,15 +357,15 @@ tile_kernel(MulParams p) {
     const uint32_t rows_n = min(kRowsN, p.n - n0);
     const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
     const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
-    const uint32_t w_off = (64 * wn + 16 * (r / 4) + r % 4) * p.blocks + q;
+    const uint32_t w_off = (64 * wave + 16 * (r / 4) + r % 4) * p.blocks + q;
 
     auto load_x = [&](uint32_t stage, uint8_t *to) {
         const uint32_t k0 = __builtin_amdgcn_readfirstlane(stage * kRowBytes);
         const uint32_t off = k0 + x_piece < k_bytes ? x_off : kOff;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(to + (i * kWaves + wave) * 1024), 16,
-                                                     off + 4 * kWaves * i * row_bytes, k0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(to + (i * kTileWaves + wave) * 1024), 16,
+                                                     off + 4 * kTileWaves * i * row_bytes, k0, 0, 0);
     };
     struct W {
         v4u code[4];
@@ -389,21 +382,21 @@ tile_kernel(MulParams p) {
         }
     };
 
-    // Stage: 4 steps of 32 along k, in each 4 kTilesM matrix instructions.  A
+    // Stage: 4 steps of 32 along k, in each 4 kTiles matrix instructions.  A
     // piece of x is read for the next step as soon as this step is done with
     // the registers it goes to, and the next step's codes are expanded beside;
     // the order is given to the compiler in groups.
-    f4 acc[kTilesM][4] = {};
+    f4 acc[kTiles][4] = {};
     auto expand = [&](const W &w, int j, bf8 (&to)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             to[i] = __builtin_bit_cast(bf8, expand8(w.code[i][j], __builtin_bit_cast(float, (w.scale[i] & 255u) << 23)));
     };
     auto compute = [&](const uint8_t *x, const W &w) {
-        const uint8_t *row = x + (wm * 16 * kTilesM + r) * kRowBytes;
-        bf8 xf[kTilesM], wf[2][4];
+        const uint8_t *row = x + r * kRowBytes;
+        bf8 xf[kTiles], wf[2][4];
 #pragma unroll
-        for (int m = 0; m < kTilesM; ++m)
+        for (int m = 0; m < kTiles; ++m)
             xf[m] = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + ((4 * q) ^ r) * 16);
         expand(w, 0, wf[0]);
         __builtin_amdgcn_sched_barrier(0);
@@ -412,7 +405,7 @@ tile_kernel(MulParams p) {
             const uint32_t piece = ((4 * q + j + 1) ^ r) * 16;
             if (j < 3) expand(w, j + 1, wf[(j + 1) & 1]);
 #pragma unroll
-            for (int m = 0; m < kTilesM; ++m) {
+            for (int m = 0; m < kTiles; ++m) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[j & 1][i], xf[m], acc[m][i], 0, 0, 0);
@@ -420,9 +413,9 @@ tile_kernel(MulParams p) {
             }
             if (j < 3) {
 #pragma unroll
-                for (int m = 0; m < kTilesM; ++m) {
+                for (int m = 0; m < kTiles; ++m) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                 // matrix instructions
-                    __builtin_amdgcn_sched_group_barrier(0x002, 16 / kTilesM, 0);      // expansion
+                    __builtin_amdgcn_sched_group_barrier(0x002, 16 / kTiles, 0);      // expansion
                     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
                     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 // LDS read
                 }
@@ -432,16 +425,16 @@ tile_kernel(MulParams p) {
     };
 
     W w, next;
-    if (first < last) {
-        load_x(first, s_x);
-        load_w(first, w);
+    if (stages) {
+        load_x(0, s_x);
+        load_w(0, w);
     }
     uint32_t flip = 0;
-    for (uint32_t s = first; s < last; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
         arrived();
         __syncthreads();  // stage s is there, stage s - 1 is read
         const uint32_t other = flip ^ (kRowsM * kRowBytes);
-        if (s + 1 < last) {
+        if (s + 1 < stages) {
             load_x(s + 1, s_x + other);
             load_w(s + 1, next);
         }
@@ -451,49 +444,22 @@ tile_kernel(MulParams p) {
     }
 
     // a lane: columns 16 q .. 16 q + 15 of the wave's 64, row r of each tile
-    const uint32_t col = n0 + 64 * wn + 16 * q;
+    const uint32_t col = n0 + 64 * wave + 16 * q;
 #pragma unroll
-    for (int m = 0; m < kTilesM; ++m) {
-        const uint32_t row = m0 + (wm * kTilesM + m) * 16 + r;
+    for (int m = 0; m < kTiles; ++m) {
+        const uint32_t row = m0 + 16 * m + r;
         if (row >= p.m || col >= p.n) continue;
-        if (kSplit) {
-            float *to = p.part + (uint64_t{split} * p.m + row) * p.n_padded + col;
+        uint16_t *to = p.y + uint64_t{row} * p.y_stride + col;
+        uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<f4 *>(to + 4 * i) = acc[m][i];
+        for (int i = 0; i < 8; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
+        if (p.y_wide && col + 16 <= p.n) {
+            *reinterpret_cast<v4u *>(to) = v4u{o[0], o[1], o[2], o[3]};
+            *reinterpret_cast<v4u *>(to + 8) = v4u{o[4], o[5], o[6], o[7]};
         } else {
-            uint16_t *to = p.y + uint64_t{row} * p.y_stride + col;
-            uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
-            if (p.y_wide && col + 16 <= p.n) {
-                *reinterpret_cast<v4u *>(to) = v4u{o[0], o[1], o[2], o[3]};
-                *reinterpret_cast<v4u *>(to + 8) = v4u{o[4], o[5], o[6], o[7]};
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < 16; ++i)
-                    if (col + i < p.n) to[i] = static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1)));
-            }
-        }
-    }
-}
-
-// y := the sum of the splits' tiles, in their order.
-__global__ void __launch_bounds__(256) join_kernel(MulParams p) {
-    const uint32_t quads = p.n_padded / 4;
-    const uint64_t total = uint64_t{p.m} * quads;
-    for (uint64_t i = uint64_t{blockIdx.x} * 256 + threadIdx.x; i < total; i += uint64_t{gridDim.x} * 256) {
-        const uint64_t row = i / quads;
-        const uint32_t col = static_cast<uint32_t>(i - row * quads) * 4;
-        if (col >= p.n) continue;
-        f4 v = *reinterpret_cast<const f4 *>(p.part + 4 * i);
-        for (uint32_t s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f4 *>(p.part + s * 4 * total + 4 * i);
-        uint16_t *to = p.y + row * p.y_stride + col;
-        const uint32_t lo = pack2(v[0], v[1]), hi = pack2(v[2], v[3]);
-        if (p.y_wide && col + 4 <= p.n) {
-            *reinterpret_cast<v2u *>(to) = v2u{lo, hi};
-        } else {
-            const uint32_t o[2] = {lo, hi};
-            for (uint32_t j = 0; j < 4 && col + j < p.n; ++j) to[j] = static_cast<uint16_t>(o[j / 2] >> (16 * (j & 1)));
+            for (uint32_t i = 0; i < 16; ++i)
+                if (col + i < p.n) to[i] = static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1)));
         }
     }
 }
@@ -563,47 +529,49 @@ uint64_t copy_bytes(uint64_t m, uint64_t k, bool x_readable) {
     return (m * ((k + kBlock - 1) / kBlock) * kBlock * 2 + 15) / 16 * 16;
 }
 
-// The form of a product.
+// The form of a product: workgroups of the token form take 16 rows of w and up
+// to 64 of x to 64 by 64, of the tile form 64, 128 or 256 rows of x by 256 of w.
+//  - Up to 32 rows, and as long as 64 x 64 pieces make no more than two for
+//    each of 256 compute units, the token form, whose waves share k, is the
+//    faster one: 512 x 4096 x 4096 32.2 us against 36.6 for the best of the tile
+//    form (k split over workgroups and joined), 256 x 14336 x 4096 (896 pieces) 64.0
+//    against 46.8.
+//  - In the token form the largest piece that leaves 160 workgroups (256 of
+//    16 rows): 64 x 4096 x 4096 8.2 us by 32 x 32 (256 workgroups), 10.8 by 64 x 32 (128)
+//    and 15.8 by 64 x 64 (64); 16 x 14336 x 4096 9.5 by 16 x 32 (448), 10.1 by 16 x 64 (224),
+//    11.7 by 16 x 16.
+//  - In the tile form 128 rows where those give 160 tiles, else 64: 1536 x 4096
+//    x 4096 (192 tiles of 128) 60 us against 75, 1024 x 4096 x 4096 (128) 57
+//    against 47.  256 rows by eight waves were no faster: 2048 x 14336 x 4096 204
+//    us against 197, 4096 x 4096 x 4096 105 against 109.
 struct Form {
     bool token;
-    uint32_t variant;  // token form: tiles of w a wave has; tile form: rows of x in a tile
-    uint32_t tiles_m, tiles_n, splits, split_stages;
-    uint64_t n_padded, part_bytes;
+    uint32_t x, rows;  // rows of x in a piece or tile; token form: tiles of 16 rows of w
 };
 
-Form form_of(uint64_t m, uint64_t n, uint64_t k) {
-    Form f = {};
-    f.token = m <= 16;
-    if (f.token) {
-        f.variant = m <= 4 ? 0x11 : 0x21;
-        return f;
-    }
-    f.variant = m > 128 ? 256 : m > 64 ? 128 : m > 32 ? 64 : 32;
-    f.tiles_m = static_cast<uint32_t>((m + f.variant - 1) / f.variant);
-    f.tiles_n = static_cast<uint32_t>((n + 255) / 256);
-    const uint64_t tiles = uint64_t{f.tiles_m} * f.tiles_n;
-    const uint32_t stages = static_cast<uint32_t>((k + kStageK - 1) / kStageK);
-    f.splits = 1;
-    f.split_stages = stages;
-    if (tiles < 128 && stages >= 4) {
-        const uint32_t want = static_cast<uint32_t>(std::min<uint64_t>((256 + tiles - 1) / tiles, stages / 2));
-        f.split_stages = (stages + want - 1) / want;
-        f.splits = (stages + f.split_stages - 1) / f.split_stages;
-    }
-    f.n_padded = (n + 15) / 16 * 16;
-    f.part_bytes = f.splits > 1 ? uint64_t{f.splits} * m * f.n_padded * 4 : 0;
-    return f;
+uint64_t pieces(uint64_t m, uint64_t x, uint64_t n, uint64_t w) { return ((m + x - 1) / x) * ((n + w - 1) / w); }
+
+Form form_of(uint64_t m, uint64_t n) {
+    if (m <= 4) return {true, 4, 1};
+    if (m > 32 && pieces(m, 64, n, 64) > 512)
+        return {false, pieces(m, 128, n, 256) >= 160 ? 128u : 64u, 0};
+    if (m > 32)
+        for (uint32_t rows : {4u, 2u})
+            if (pieces(m, 64, n, 16 * rows) >= 160) return {true, 64, rows};
+    if (m > 16)
+        for (uint32_t rows : {4u, 2u})
+            if (pieces(m, 32, n, 16 * rows) >= 160) return {true, 32, rows};
+    for (uint32_t rows : {4u, 2u})
+        if (pieces(m, 16, n, 16 * rows) >= 256) return {true, 16, rows};
+    return {true, 16, 1};
 }
 
-uint64_t matmul_workspace(uint64_t m, uint64_t n, uint64_t k, bool x_readable) {
-    return copy_bytes(m, k, x_readable) + form_of(m, n, k).part_bytes;
-}
-
-template <int kWavesM, int kWavesN, int kTilesM>
-hipError_t launch_tiles(const Form &f, hipStream_t st, const MulParams &p) {
-    const uint32_t grid = f.tiles_m * f.tiles_n * f.splits;
-    return f.splits > 1 ? launch(tile_kernel<kWavesM, kWavesN, kTilesM, true>, dim3(grid), 64 * kWavesM * kWavesN, st, p)
-                        : launch(tile_kernel<kWavesM, kWavesN, kTilesM, false>, dim3(grid), 64 * kWavesM * kWavesN, st, p);
+template <int kX, int kRows, int kAhead>
+hipError_t launch_token(bool wide, hipStream_t st, const MulParams &p) {
+    constexpr int kWaves = 8;
+    const dim3 grid((p.n + 16 * kRows - 1) / (16 * kRows), (p.m + kX - 1) / kX);
+    return wide ? launch(token_kernel<kX, kRows, kWaves, kAhead, true>, grid, 64 * kWaves, st, p)
+                : launch(token_kernel<kX, kRows, kWaves, kAhead, false>, grid, 64 * kWaves, st, p);
 }
 
 df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
@@ -618,10 +586,10 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         return DF11_E_INVALID_ARG;
     const bool readable = aligned16(x) && x_stride % 8 == 0 && x_stride <= kMaxRead;
     const uint64_t copy = copy_bytes(m, k, readable);
-    const Form f = form_of(m, n, k);
-    if (workspace_bytes < copy + f.part_bytes) return DF11_E_BUFFER_TOO_SMALL;
-    if (copy + f.part_bytes && !workspace) return DF11_E_INVALID_ARG;
-    const uint64_t tiles = uint64_t{f.tiles_m} * f.tiles_n * f.splits;
+    if (workspace_bytes < copy) return DF11_E_BUFFER_TOO_SMALL;
+    if (copy && !workspace) return DF11_E_INVALID_ARG;
+    const Form f = form_of(m, n);
+    const uint64_t tiles = f.token ? 0 : pieces(m, f.x, n, 256);
     if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     MulParams p = {};
@@ -647,31 +615,22 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     }
     if (f.token) {
         const bool wide = p.blocks % 16 == 0 && aligned16(scales);
-        switch (f.variant) {
-#define C(v, x, b, w, a) case v: { const dim3 grid(static_cast<uint32_t>((n + 16 * b - 1) / (16 * b)), static_cast<uint32_t>((m + x - 1) / (x))); \
-   err = wide ? launch(token_kernel<x, b, w, a, true>, grid, 64 * w, st, p) : launch(token_kernel<x, b, w, a, false>, grid, 64 * w, st, p); break; }
-            C(0x11, 4, 1, 8, 4) C(0x12, 4, 2, 8, 4) C(0x14, 4, 4, 8, 4) C(0x15, 4, 1, 4, 4) C(0x16, 4, 2, 4, 4) C(0x17, 4, 4, 4, 4) C(0x18, 4, 1, 8, 2)
-            C(0x21, 16, 1, 8, 4) C(0x22, 16, 2, 8, 4) C(0x24, 16, 4, 8, 4) C(0x25, 16, 1, 8, 2) C(0x26, 16, 2, 8, 2) C(0x27, 16, 4, 8, 2) C(0x28, 16, 4, 4, 4) C(0x29, 16, 2, 4, 4) C(0x2a, 16, 1, 4, 4)
-            C(0x41, 32, 1, 8, 2) C(0x42, 32, 2, 8, 2) C(0x44, 32, 4, 8, 2) C(0x45, 32, 1, 4, 4) C(0x46, 32, 2, 4, 4) C(0x47, 32, 4, 4, 2)
-            C(0x81, 64, 1, 8, 1) C(0x82, 64, 2, 8, 1) C(0x84, 64, 4, 8, 1) C(0x87, 64, 4, 4, 2)
+        switch (f.x + f.rows) {
+            case 4 + 1: return launched(launch_token<4, 1, 4>(wide, st, p));
+            case 16 + 1: return launched(launch_token<16, 1, 2>(wide, st, p));
+            case 16 + 2: return launched(launch_token<16, 2, 2>(wide, st, p));
+            case 16 + 4: return launched(launch_token<16, 4, 2>(wide, st, p));
+            case 32 + 2: return launched(launch_token<32, 2, 2>(wide, st, p));
+            case 32 + 4: return launched(launch_token<32, 4, 2>(wide, st, p));
+            case 64 + 2: return launched(launch_token<64, 2, 1>(wide, st, p));
+            default: return launched(launch_token<64, 4, 1>(wide, st, p));
         }
-        return launched(err);
     }
-    p.tiles_m = f.tiles_m;
-    p.tiles_n = f.tiles_n;
-    p.splits = f.splits;
-    p.split_stages = f.split_stages;
-    p.n_padded = static_cast<uint32_t>(f.n_padded);
-    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + copy);
-    err = f.variant == 256   ? launch_tiles<2, 4, 8>(f, st, p)
-          : f.variant == 128 ? launch_tiles<1, 4, 8>(f, st, p)
-          : f.variant == 64  ? launch_tiles<1, 4, 4>(f, st, p)
-                             : launch_tiles<1, 4, 2>(f, st, p);
-    if (err == hipSuccess && f.splits > 1) {
-        const uint64_t quads = m * (f.n_padded / 4);
-        err = launch(join_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((quads + 255) / 256, 8192))), 256, st, p);
-    }
-    return launched(err);
+    p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
+    p.tiles_n = static_cast<uint32_t>((n + 255) / 256);
+    const dim3 grid(static_cast<uint32_t>(tiles));
+    return launched(f.x == 128 ? launch(tile_kernel<8>, grid, 64 * kTileWaves, st, p)
+                               : launch(tile_kernel<4>, grid, 64 * kTileWaves, st, p));
 }
 
 }  // namespace
@@ -687,8 +646,8 @@ extern "C" df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *
 }
 
 extern "C" uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned) {
-    if (m > kMaxRows || n > kMaxRows || k > kMaxK) return 0;  // refused by the product
-    return matmul_workspace(m, n, k, x_aligned != 0);
+    if (m > kMaxRows || n > kMaxRows || k > kMaxK || n == 0) return 0;  // refused by the product, or nothing to do
+    return copy_bytes(m, k, x_aligned != 0);
 }
 
 extern "C" df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
