@@ -179,7 +179,7 @@ struct MulParams {
     const uint8_t *codes, *scales;
     uint16_t *y;
     uint64_t x_stride, y_stride;
-    uint32_t m, n, blocks;  // blocks of 32 along k
+    uint32_t m, n, k, blocks;  // blocks of 32 along k
     uint32_t y_wide;        // rows of y start at multiples of 16 bytes
     // tile form
     uint32_t tiles_m, tiles_n;
@@ -212,9 +212,28 @@ __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); 
 // them), and the scales of four steps in one load of 16 bytes (a byte for each
 // step: 1 x 128256 x 4096 90 us against 71).  Piece c of row i of x lies at
 // c ^ (i % 16), as in the tile form.
-template <int kX, int kRows, int kWaves, int kAhead, bool kWide>
+// How the token form reads: kReadWide as above, for k in multiples of 512; kReadNarrow
+// with a byte of scales for each block; kReadAny also takes rows of x that start
+// anywhere and end inside a block, through registers.
+__device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint32_t k) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (col + 8 <= k) {
+        const Piece t = *reinterpret_cast<const Piece *>(row + col);
+        w[0] = t.w[0], w[1] = t.w[1], w[2] = t.w[2], w[3] = t.w[3];
+    } else if (col < k) {
+#pragma unroll
+        for (uint32_t i = 0; i < 7; ++i)
+            if (col + i < k) w[i / 2] |= uint32_t{row[col + i]} << (16 * (i & 1));
+    }
+    return v4u{w[0], w[1], w[2], w[3]};
+}
+
+enum TokenReads : int { kReadWide, kReadNarrow, kReadAny };
+
+template <int kX, int kRows, int kWaves, int kAhead, int kReads>
 __global__ void __launch_bounds__(64 * kWaves)
 token_kernel(MulParams p) {
+    constexpr bool kWide = kReads == kReadWide;
     constexpr int kM = kX < 16 ? 1 : kX / 16;  // tiles of x
     constexpr uint32_t kGroup = 4;             // steps whose scales are loaded together
     constexpr uint32_t kStepBytes = kX * 256, kWaveBytes = kAhead * kStepBytes;
@@ -227,7 +246,8 @@ token_kernel(MulParams p) {
     const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
     const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
     const uint32_t row_bytes = static_cast<uint32_t>(p.x_stride) * 2, k_bytes = p.blocks * kBlock * 2;
-    const Rsrc xr = rsrc(p.x + uint64_t{m0} * p.x_stride, (rows_m - 1) * row_bytes + k_bytes);
+    const uint16_t *x0 = p.x + uint64_t{m0} * p.x_stride;
+    const Rsrc xr = rsrc(x0, (rows_m - 1) * row_bytes + k_bytes);
     uint8_t *mine = s_x + wave * kWaveBytes;
     f4 acc[kM][kRows] = {};
     for (uint32_t g0 = wave * kGroup * 4; g0 < p.blocks; g0 += kWaves * kGroup * 4) {
@@ -242,7 +262,7 @@ token_kernel(MulParams p) {
 #pragma unroll
         for (uint32_t b0 = 0; b0 < kGroup; b0 += kAhead) {
             __builtin_amdgcn_s_waitcnt(0xC07F);  // what was read from LDS before has arrived (lgkmcnt 0)
-            v4u c[kAhead][kRows];
+            v4u c[kAhead][kRows], xs[kAhead][kX / 4];
 #pragma unroll
             for (uint32_t a = 0; a < kAhead; ++a) {
                 const uint32_t block0 = g0 + 4 * (b0 + a);  // past the end at most in the last group
@@ -250,9 +270,12 @@ token_kernel(MulParams p) {
 #pragma unroll
                 for (uint32_t j = 0; j < kX / 4; ++j) {
                     const uint32_t row = 4 * j + q, piece = (r ^ (row & 15u)) * 16;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(mine + a * kStepBytes + j * 1024), 16,
-                                                             k0 + piece < k_bytes ? row * row_bytes + piece : kOff,
-                                                             __builtin_amdgcn_readfirstlane(k0), 0, 0);
+                    if (kReads == kReadAny)
+                        xs[a][j] = row < rows_m ? piece_of(x0 + row * p.x_stride, (k0 + piece) / 2, p.k) : v4u{0, 0, 0, 0};
+                    else
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(mine + a * kStepBytes + j * 1024), 16,
+                                                                 k0 + piece < k_bytes ? row * row_bytes + piece : kOff,
+                                                                 __builtin_amdgcn_readfirstlane(k0), 0, 0);
                 }
                 const uint32_t at = block0 + q < p.blocks ? r * p.blocks + block0 + q : kOff / 16;
 #pragma unroll
@@ -263,7 +286,15 @@ token_kernel(MulParams p) {
                                         << (8 * q);
                 }
             }
-            arrived();
+            if (kReads == kReadAny) {
+#pragma unroll
+                for (uint32_t a = 0; a < kAhead; ++a)
+#pragma unroll
+                    for (uint32_t j = 0; j < kX / 4; ++j)
+                        *reinterpret_cast<v4u *>(mine + a * kStepBytes + j * 1024 + lane * 16) = xs[a][j];
+            } else {
+                arrived();
+            }
 #pragma unroll
             for (uint32_t a = 0; a < kAhead; ++a) {
                 float scale[kRows];
@@ -519,16 +550,6 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
                            static_cast<uint32_t>(cols), blocks, items, out, out_stride));
 }
 
-// Rows of x are read 16 bytes at a time and whole blocks at a time, with byte
-// offsets of 31 bits in a tile: anything else goes through a packed copy in
-// the workspace.
-constexpr uint64_t kMaxRead = uint64_t{1} << 21;  // stride of x in a tile of 256 rows: 2^30 bytes
-
-uint64_t copy_bytes(uint64_t m, uint64_t k, bool x_readable) {
-    if (x_readable && k % kBlock == 0) return 0;
-    return (m * ((k + kBlock - 1) / kBlock) * kBlock * 2 + 15) / 16 * 16;
-}
-
 // The form of a product: workgroups of the token form take 16 rows of w and up
 // to 64 of x to 64 by 64, of the tile form 64, 128 or 256 rows of x by 256 of w.
 //  - Up to 32 rows, and as long as 64 x 64 pieces make no more than two for
@@ -567,11 +588,23 @@ Form form_of(uint64_t m, uint64_t n) {
 }
 
 template <int kX, int kRows, int kAhead>
-hipError_t launch_token(bool wide, hipStream_t st, const MulParams &p) {
+hipError_t launch_token(int reads, hipStream_t st, const MulParams &p) {
     constexpr int kWaves = 8;
     const dim3 grid((p.n + 16 * kRows - 1) / (16 * kRows), (p.m + kX - 1) / kX);
-    return wide ? launch(token_kernel<kX, kRows, kWaves, kAhead, true>, grid, 64 * kWaves, st, p)
-                : launch(token_kernel<kX, kRows, kWaves, kAhead, false>, grid, 64 * kWaves, st, p);
+    return launch(reads == kReadWide     ? token_kernel<kX, kRows, kWaves, kAhead, kReadWide>
+                  : reads == kReadNarrow ? token_kernel<kX, kRows, kWaves, kAhead, kReadNarrow>
+                                         : token_kernel<kX, kRows, kWaves, kAhead, kReadAny>,
+                  grid, 64 * kWaves, st, p);
+}
+
+// Rows of x are read 16 bytes and whole blocks at a time, with byte offsets of
+// 31 bits in a tile.  The token form has another way for those that cannot be
+// (kReadAny); for the tile form they are copied into the workspace first.
+constexpr uint64_t kMaxRead = uint64_t{1} << 21;  // stride of x for 256 rows in 2^30 bytes
+
+uint64_t copy_bytes(uint64_t m, uint64_t n, uint64_t k, bool x_readable) {
+    if ((x_readable && k % kBlock == 0) || m == 0 || n == 0 || form_of(m, n).token) return 0;
+    return (m * ((k + kBlock - 1) / kBlock) * kBlock * 2 + 15) / 16 * 16;
 }
 
 df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
@@ -585,7 +618,7 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         (reinterpret_cast<uintptr_t>(y) & 1u) || !aligned16(workspace))
         return DF11_E_INVALID_ARG;
     const bool readable = aligned16(x) && x_stride % 8 == 0 && x_stride <= kMaxRead;
-    const uint64_t copy = copy_bytes(m, k, readable);
+    const uint64_t copy = copy_bytes(m, n, k, readable);
     if (workspace_bytes < copy) return DF11_E_BUFFER_TOO_SMALL;
     if (copy && !workspace) return DF11_E_INVALID_ARG;
     const Form f = form_of(m, n);
@@ -601,6 +634,7 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.y_stride = y_stride;
     p.m = static_cast<uint32_t>(m);
     p.n = static_cast<uint32_t>(n);
+    p.k = static_cast<uint32_t>(k);
     p.blocks = static_cast<uint32_t>((k + kBlock - 1) / kBlock);
     p.y_wide = aligned16(y) && y_stride % 8 == 0;
     hipError_t err = hipSuccess;
@@ -614,16 +648,18 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         p.x_stride = width;
     }
     if (f.token) {
-        const bool wide = p.blocks % 16 == 0 && aligned16(scales);
+        const int reads = !readable || k % kBlock != 0                    ? kReadAny
+                          : p.blocks % 16 == 0 && aligned16(scales) ? kReadWide
+                                                                    : kReadNarrow;
         switch (f.x + f.rows) {
-            case 4 + 1: return launched(launch_token<4, 1, 4>(wide, st, p));
-            case 16 + 1: return launched(launch_token<16, 1, 2>(wide, st, p));
-            case 16 + 2: return launched(launch_token<16, 2, 2>(wide, st, p));
-            case 16 + 4: return launched(launch_token<16, 4, 2>(wide, st, p));
-            case 32 + 2: return launched(launch_token<32, 2, 2>(wide, st, p));
-            case 32 + 4: return launched(launch_token<32, 4, 2>(wide, st, p));
-            case 64 + 2: return launched(launch_token<64, 2, 1>(wide, st, p));
-            default: return launched(launch_token<64, 4, 1>(wide, st, p));
+            case 4 + 1: return launched(launch_token<4, 1, 4>(reads, st, p));
+            case 16 + 1: return launched(launch_token<16, 1, 2>(reads, st, p));
+            case 16 + 2: return launched(launch_token<16, 2, 2>(reads, st, p));
+            case 16 + 4: return launched(launch_token<16, 4, 2>(reads, st, p));
+            case 32 + 2: return launched(launch_token<32, 2, 2>(reads, st, p));
+            case 32 + 4: return launched(launch_token<32, 4, 2>(reads, st, p));
+            case 64 + 2: return launched(launch_token<64, 2, 1>(reads, st, p));
+            default: return launched(launch_token<64, 4, 1>(reads, st, p));
         }
     }
     p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
@@ -646,8 +682,8 @@ extern "C" df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *
 }
 
 extern "C" uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned) {
-    if (m > kMaxRows || n > kMaxRows || k > kMaxK || n == 0) return 0;  // refused by the product, or nothing to do
-    return copy_bytes(m, k, x_aligned != 0);
+    if (m > kMaxRows || n > kMaxRows || k > kMaxK) return 0;  // refused by the product
+    return copy_bytes(m, n, k, x_aligned != 0);
 }
 
 extern "C" df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,

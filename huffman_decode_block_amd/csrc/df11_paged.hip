@@ -606,13 +606,15 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
 // Chunks of a sequence.  The device cuts what a sequence really holds, so the
 // page table's width only bounds them: as many as give each of 256 compute
 // units a workgroup, no more than chunks of kMinChunk, and enough that none
-// exceeds kMaxChunk.  Measured with 256, 512 and 1,024 workgroups wanted: 8 x
+// exceeds kMaxChunk; none where the table holds at most 256 positions (a second
+// kernel takes longer than the second step of a wave).  Measured with 256, 512 and 1,024 workgroups wanted: 8 x
 // 32,768 BF16 positions of 8 heads (1.07 GB) 188, 188 and 190 us; one sequence of
 // 65,536 52.1, 53.2 and 55.9; 16 windows of 1,024 over 4 heads of 256 17.3, 20.2
 // and 22.7.
 constexpr uint64_t kWantGroups = 256;
 
 uint32_t splits_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions) {
+    if (positions <= 2 * kMinChunk) return 1;
     const uint64_t units = std::max<uint64_t>(batch * kv_heads * tiles, 1);
     const uint64_t want = (kWantGroups + units - 1) / units;
     const uint64_t most = (positions + kMinChunk - 1) / kMinChunk, least = (positions + kMaxChunk - 1) / kMaxChunk;

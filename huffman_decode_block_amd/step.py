@@ -77,32 +77,37 @@ def _check(status: int, what: str):
 
 
 def _place(dev, stream):
-    """Where a call on `dev` runs: the raw stream handle, and None or a context
-    that makes that device and stream torch's current ones (so that what the
-    call allocates belongs to its stream)."""
+    """Where a call on GPU number `dev` runs: the raw stream handle, and None or
+    a context that makes that device and stream torch's current ones (so that
+    what the call allocates belongs to its stream)."""
     torch = _torch
-    here = torch.cuda.current_device() == dev.index
+    # torch's own calls below the public ones, which build a Stream object and
+    # check for initialisation: 2 us less of a call's 9
+    here = torch._C._cuda_getDevice() == dev
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)  # the public call builds a Stream object, 1 us more
-        return handle, None if here else torch.cuda.device(dev)
+        return torch._C._cuda_getCurrentRawStream(dev), None if here else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         handle = int(stream)
-        if here and handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        if here and handle == torch._C._cuda_getCurrentRawStream(dev):
             return handle, None
         stream = torch.cuda.ExternalStream(handle, device=dev)
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _tensor(t, name, dtype, ndim, dev=None):
-    """Checks a tensor's place, type and rank."""
-    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+def _tensor(t, name, dtype, ndim, dev):
+    """Checks a tensor's type, rank and place (a GPU's number; -1 for any GPU)."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a device tensor")
+    at = t.get_device()
+    if at < 0:
         raise TypeError(f"{name} must be a device tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    if at != dev and dev >= 0:
+        raise ValueError(f"{name} is on GPU {at}, not {dev}")
+    return at
 
 
 def _last_dense(t, name):
@@ -121,15 +126,15 @@ def _dense(t, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(given, need, dev):
+def _workspace(given, need, like, dev):
     """(tensor to keep, address, bytes) of a workspace: the given one or a new one."""
     if given is not None:
-        if not isinstance(given, _torch.Tensor) or given.device != dev or not given.is_contiguous():
+        if not isinstance(given, _torch.Tensor) or given.get_device() != dev or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous device tensor on the inputs' GPU")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    t = _torch.empty(need, dtype=_torch.uint8, device=dev)
+    t = like.new_empty((need,), dtype=_torch.uint8)
     return t, t.data_ptr(), need
 
 
@@ -141,18 +146,18 @@ def df11_mx4_matmul_workspace_bytes(m: int, n: int, k: int, x_aligned: bool = Tr
 
 
 def _codes(codes, scales, cols, dev):
-    """Checks codes and scale bytes of a matrix with `cols` columns; returns its rows."""
+    """Checks codes and scale bytes of a matrix with `cols` columns; returns its rows and GPU."""
     u8 = _torch.uint8
-    _tensor(codes, "codes", u8, 2, dev)
+    dev = _tensor(codes, "codes", u8, 2, dev)
     _tensor(scales, "scales", u8, 2, dev)
     _dense(codes, "codes")
     _dense(scales, "scales")
     blocks = (cols + 31) // 32
     rows, width = codes.shape
-    if width != 16 * blocks or scales.shape[1] != blocks or scales.shape[0] != rows:
+    if width != 16 * blocks or scales.shape != (rows, blocks):
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {cols} columns: "
                          f"[rows, {16 * blocks}] and [rows, {blocks}] expected")
-    return rows
+    return rows, dev
 
 
 def df11_mx4_quantize(x, codes=None, scales=None, stream=None):
@@ -160,26 +165,26 @@ def df11_mx4_quantize(x, codes=None, scales=None, stream=None):
     may be strided): uint8 tensors [rows, 16 * ceil(cols / 32)] and [rows,
     ceil(cols / 32)], allocated when None.  Returns (codes, scales)."""
     torch = _torch or _load()
-    _tensor(x, "x", torch.bfloat16, 2)
+    dev = _tensor(x, "x", torch.bfloat16, 2, -1)
     _last_dense(x, "x")
     if x.shape[1] == 0:
         raise ValueError("x has no columns")
-    handle, ctx = _place(x.device, stream)
+    handle, ctx = _place(dev, stream)
     if ctx is None:
-        return _quantize(x, codes, scales, handle)
+        return _quantize(x, codes, scales, dev, handle)
     with ctx:
-        return _quantize(x, codes, scales, handle)
+        return _quantize(x, codes, scales, dev, handle)
 
 
-def _quantize(x, codes, scales, handle):
+def _quantize(x, codes, scales, dev, handle):
     rows, cols = x.shape
-    dev = x.device
     blocks = (cols + 31) // 32
+    given = codes is not None or scales is not None
     if codes is None:
-        codes = _torch.empty((rows, 16 * blocks), dtype=_torch.uint8, device=dev)
+        codes = x.new_empty((rows, 16 * blocks), dtype=_torch.uint8)
     if scales is None:
-        scales = _torch.empty((rows, blocks), dtype=_torch.uint8, device=dev)
-    if _codes(codes, scales, cols, dev) != rows:
+        scales = x.new_empty((rows, blocks), dtype=_torch.uint8)
+    if given and _codes(codes, scales, cols, dev)[0] != rows:
         raise ValueError(f"codes has {codes.shape[0]} rows, x {rows}")
     _check(_L.df11_mx4_quantize(x.data_ptr(), rows, cols, _row_stride(x), codes.data_ptr(), scales.data_ptr(), handle),
            "df11_mx4_quantize")
@@ -193,31 +198,28 @@ def df11_mx4_dequantize(codes, scales, cols: int, out=None, stream=None):
     cols = int(cols)
     if cols <= 0:
         raise ValueError("cols must be positive")
-    _codes(codes, scales, cols, None)
-    dev = codes.device
-    if scales.device != dev:
-        raise ValueError(f"scales is on {scales.device}, not {dev}")
+    _, dev = _codes(codes, scales, cols, -1)
     handle, ctx = _place(dev, stream)
     if ctx is None:
-        return _dequantize(codes, scales, cols, out, handle)
+        return _dequantize(codes, scales, cols, out, dev, handle)
     with ctx:
-        return _dequantize(codes, scales, cols, out, handle)
+        return _dequantize(codes, scales, cols, out, dev, handle)
 
 
-def _out(out, shape, dtype, dev, name="out"):
-    """A new output, or the given one checked."""
+def _out(out, like, shape, dtype, dev, name="out"):
+    """A new output on the device of `like`, or the given one checked."""
     if out is None:
-        return _torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     _tensor(out, name, dtype, len(shape), dev)
-    if tuple(out.shape) != shape:
+    if out.shape != shape:
         raise ValueError(f"{name} must be {shape}, got {tuple(out.shape)}")
     _last_dense(out, name)
     return out
 
 
-def _dequantize(codes, scales, cols, out, handle):
+def _dequantize(codes, scales, cols, out, dev, handle):
     rows = codes.shape[0]
-    out = _out(out, (rows, cols), _torch.bfloat16, codes.device)
+    out = _out(out, codes, (rows, cols), _torch.bfloat16, dev)
     _check(_L.df11_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), _row_stride(out),
                                   handle), "df11_mx4_dequantize")
     return out
@@ -229,24 +231,22 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
     rounding.  workspace: df11_mx4_matmul_workspace_bytes bytes, allocated
     when None and needed.  Returns out."""
     torch = _torch or _load()
-    _tensor(x, "x", torch.bfloat16, 2)
+    dev = _tensor(x, "x", torch.bfloat16, 2, -1)
     _last_dense(x, "x")
-    dev = x.device
-    n = _codes(codes, scales, x.shape[1], dev)
+    n, _ = _codes(codes, scales, x.shape[1], dev)
     handle, ctx = _place(dev, stream)
     if ctx is None:
-        return _matmul(x, codes, scales, n, out, workspace, handle)
+        return _matmul(x, codes, scales, n, out, workspace, dev, handle)
     with ctx:
-        return _matmul(x, codes, scales, n, out, workspace, handle)
+        return _matmul(x, codes, scales, n, out, workspace, dev, handle)
 
 
-def _matmul(x, codes, scales, n, out, workspace, handle):
+def _matmul(x, codes, scales, n, out, workspace, dev, handle):
     m, k = x.shape
-    dev = x.device
-    out = _out(out, (m, n), _torch.bfloat16, dev)
+    out = _out(out, x, (m, n), _torch.bfloat16, dev)
     xs, xp = _row_stride(x), x.data_ptr()
     need = _L.df11_mx4_matmul_workspace_bytes(m, n, k, xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21)
-    keep, ws, size = _workspace(workspace, need, dev)
+    keep, ws, size = _workspace(workspace, need, x, dev)
     _check(_L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), _row_stride(out), ws,
                               size, handle), "df11_mx4_matmul")
     return out
@@ -293,8 +293,7 @@ def df11_paged_append(k, v, slots, k_pages, v_pages, k_scale=None, v_scale=None,
     [kv_heads]: what is stored is the value over its head's scale."""
     torch = _torch or _load()
     bf16 = torch.bfloat16
-    _tensor(k, "k", bf16, 3)
-    dev = k.device
+    dev = _tensor(k, "k", bf16, 3, -1)
     _tensor(v, "v", bf16, 3, dev)
     _tensor(slots, "slots", torch.int64, 1, dev)
     _dense(slots, "slots")
@@ -341,8 +340,7 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
     with no position gets zeros and -inf."""
     torch = _torch or _load()
     i32 = torch.int32
-    _tensor(q, "q", torch.bfloat16, 3)
-    dev = q.device
+    dev = _tensor(q, "q", torch.bfloat16, 3, -1)
     _last_dense(q, "q")
     c = _cache(k_pages, v_pages, k_scale, v_scale, dev)
     _tensor(page_table, "page_table", i32, 2, dev)
@@ -362,24 +360,23 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
     scale = dim ** -0.5 if scale is None else float(scale)
     handle, ctx = _place(dev, stream)
     if ctx is None:
-        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle)
+        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, handle)
     with ctx:
-        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle)
+        return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, handle)
 
 
-def _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, handle):
+def _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, handle):
     batch, heads, dim = q.shape
-    dev = q.device
     given = out is not None, lse is not None
-    out = _out(out, (batch, heads, dim), _torch.bfloat16, dev)
-    lse = _out(lse, (batch, heads), _torch.float32, dev, "lse")
+    out = _out(out, q, (batch, heads, dim), _torch.bfloat16, dev)
+    lse = _out(lse, q, (batch, heads), _torch.float32, dev, "lse")
     if given[0]:
         _dense(out, "out")
     if given[1]:
         _dense(lse, "lse")
     width = page_table.shape[1]
     need = _L.df11_paged_attention_workspace_bytes(batch, heads, c.kv_heads, dim, c.page_size, width)
-    keep, ws, size = _workspace(workspace, need, dev)
+    keep, ws, size = _workspace(workspace, need, q, dev)
     q0, q1, _ = q.stride()
     _check(_L.df11_paged_attention(ctypes.byref(c), q.data_ptr(), batch, heads, q0, q1, page_table.data_ptr(),
                                    page_table.stride(0) if batch > 1 else width, width, lens.data_ptr(),

@@ -69,10 +69,10 @@ df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t 
                             const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                             uint64_t workspace_bytes, void *hip_stream);
 
-/* Bytes of workspace for a product: those of a packed copy of x where x cannot
- * be read 16 bytes at a time or k is no multiple of 32, else 0.  x_aligned:
- * whether x is 16-byte aligned with x_stride a multiple of 8 and at most
- * 2^21. */
+/* Bytes of workspace for a product: 0, but for many rows of x that cannot be
+ * read 16 bytes at a time or with k no multiple of 32 (a packed copy of x).
+ * x_aligned: whether x is 16-byte aligned with x_stride a multiple of 8 and at
+ * most 2^21. */
 uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned);
 
 /* ---- Paged key-value cache ----------------------------------------------

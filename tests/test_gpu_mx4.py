@@ -170,6 +170,7 @@ SHAPES = [
     (31, 33, 1000), (33, 257, 512), (64, 64, 64), (65, 1000, 160), (77, 257, 199), (128, 128, 128), (129, 130, 320),
     (200, 72, 2048), (256, 256, 256), (257, 511, 65), (300, 1024, 1024), (513, 260, 288), (1, 300, 14336),
     (1024, 512, 544), (2, 128300, 64), (5, 8, 8192), (48, 2048, 4096), (700, 640, 32),
+    (1500, 1500, 512), (1400, 1600, 200), (2100, 2111, 96), (16, 8200, 512), (32, 5200, 1024), (40, 10300, 160), (129, 8193, 64),
 ]
 
 
@@ -185,6 +186,7 @@ def test_product_against_64_bits(torch, m, n, k):
 
 @pytest.mark.parametrize("m,n,k,pad,offset", [
     (1, 96, 128, 0, 1), (4, 96, 128, 8, 8), (19, 50, 256, 3, 2), (90, 200, 96, 5, 0), (150, 129, 100, 0, 4), (260, 140, 64, 8, 3),
+    (1500, 1500, 70, 1, 0), (1600, 1411, 64, 0, 1), (70, 3000, 515, 0, 0),
 ])
 def test_product_of_strided_rows(torch, m, n, k, pad, offset):
     """What lies between the rows of x is NaN; the rows of y are strided too."""
@@ -274,7 +276,7 @@ def test_refusals(torch):
         hdb.df11_mx4_quantize(x[:, :0])
     with pytest.raises(ValueError):
         hdb.df11_mx4_dequantize(c, s, 65)
+    wide = torch.zeros(2048, 65, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(hdb.DF11Error) as e:
-        hdb.df11_mx4_matmul(x[:, 1:], *hdb.df11_mx4_quantize(x[:, 1:]),
-                            workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        hdb.df11_mx4_matmul(wide, *hdb.df11_mx4_quantize(wide), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == hdb.DF11_E_BUFFER_TOO_SMALL

@@ -43,6 +43,9 @@ def test_quantise_refusals(change):
         hdb.DF11_E_INVALID_ARG
 
 
+MANY = dict(m=4096, n=4096, ys=4096)  # rows and columns enough for the form that needs x readable or copied
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(x=None), hdb.DF11_E_INVALID_ARG), (dict(x=P + 1), hdb.DF11_E_INVALID_ARG),
     (dict(y=None), hdb.DF11_E_INVALID_ARG), (dict(y=P + 1), hdb.DF11_E_INVALID_ARG),
@@ -50,9 +53,9 @@ def test_quantise_refusals(change):
     (dict(xs=63), hdb.DF11_E_INVALID_ARG), (dict(ys=39), hdb.DF11_E_INVALID_ARG),
     (dict(m=1 << 31), hdb.DF11_E_INVALID_ARG), (dict(n=1 << 31, ys=1 << 31), hdb.DF11_E_INVALID_ARG),
     (dict(k=(1 << 21) + 1, xs=1 << 25), hdb.DF11_E_INVALID_ARG), (dict(xs=1 << 33), hdb.DF11_E_INVALID_ARG),
-    (dict(k=63), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(x=P + 2), hdb.DF11_E_BUFFER_TOO_SMALL),
-    (dict(xs=65), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(k=63, ws=P + 8, size=1 << 20), hdb.DF11_E_INVALID_ARG),
-    (dict(k=63, ws=None, size=1 << 20), hdb.DF11_E_INVALID_ARG),
+    (dict(MANY, k=63), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(MANY, x=P + 2), hdb.DF11_E_BUFFER_TOO_SMALL),
+    (dict(MANY, xs=65), hdb.DF11_E_BUFFER_TOO_SMALL), (dict(MANY, k=63, ws=P + 8, size=1 << 30), hdb.DF11_E_INVALID_ARG),
+    (dict(MANY, k=63, ws=None, size=1 << 30), hdb.DF11_E_INVALID_ARG),
 ])
 def test_product_refusals(change, status):
     a = dict(x=P, m=3, k=64, xs=64, codes=P, scales=P, n=40, y=P, ys=40, ws=None, size=0)
@@ -134,8 +137,10 @@ def test_attention_refusals(change, status):
 
 def test_workspace_sizes():
     assert hdb.df11_mx4_matmul_workspace_bytes(1, 4096, 4096) == 0
-    assert hdb.df11_mx4_matmul_workspace_bytes(3, 40, 63) >= 3 * 64 * 2
-    assert hdb.df11_mx4_matmul_workspace_bytes(3, 40, 64, False) >= 3 * 64 * 2
+    assert hdb.df11_mx4_matmul_workspace_bytes(3, 40, 63, False) == 0
+    assert hdb.df11_mx4_matmul_workspace_bytes(4096, 4096, 64) == 0
+    assert hdb.df11_mx4_matmul_workspace_bytes(4096, 4096, 63) >= 4096 * 64 * 2
+    assert hdb.df11_mx4_matmul_workspace_bytes(4096, 4096, 64, False) >= 4096 * 64 * 2
     assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 16, 4) == 0
     assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 16, 4096) >= 32 * 130 * 4
     # calls that the operators refuse need none
