@@ -118,7 +118,8 @@ def _last_dense(t, name):
 
 def _row_stride(t):
     """A matrix's row stride; of a single row (torch leaves it open) its length."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else cols or 1
 
 
 def _dense(t, name):
@@ -150,8 +151,8 @@ def _codes(codes, scales, cols, dev):
     u8 = _torch.uint8
     dev = _tensor(codes, "codes", u8, 2, dev)
     _tensor(scales, "scales", u8, 2, dev)
-    _dense(codes, "codes")
-    _dense(scales, "scales")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
     blocks = (cols + 31) // 32
     rows, width = codes.shape
     if width != 16 * blocks or scales.shape != (rows, blocks):
@@ -243,12 +244,17 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
 
 def _matmul(x, codes, scales, n, out, workspace, dev, handle):
     m, k = x.shape
-    out = _out(out, x, (m, n), _torch.bfloat16, dev)
+    if out is None:
+        out, ys = x.new_empty((m, n)), n if n else 1
+    else:
+        ys = _row_stride(_out(out, x, (m, n), _torch.bfloat16, dev))
     xs, xp = _row_stride(x), x.data_ptr()
-    need = _L.df11_mx4_matmul_workspace_bytes(m, n, k, xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21)
-    keep, ws, size = _workspace(workspace, need, x, dev)
-    _check(_L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), _row_stride(out), ws,
-                              size, handle), "df11_mx4_matmul")
+    keep, ws, size = workspace, None, 0
+    if workspace is not None or k % 32 or xs % 8 or xp % 16 or xs > 1 << 21:
+        need = _L.df11_mx4_matmul_workspace_bytes(m, n, k, xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21)
+        keep, ws, size = _workspace(workspace, need, x, dev)
+    _check(_L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), ys, ws, size, handle),
+           "df11_mx4_matmul")
     return out
 
 
@@ -367,13 +373,14 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
 
 def _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, handle):
     batch, heads, dim = q.shape
-    given = out is not None, lse is not None
-    out = _out(out, q, (batch, heads, dim), _torch.bfloat16, dev)
-    lse = _out(lse, q, (batch, heads), _torch.float32, dev, "lse")
-    if given[0]:
-        _dense(out, "out")
-    if given[1]:
-        _dense(lse, "lse")
+    if out is None:
+        out = q.new_empty((batch, heads, dim))
+    else:
+        _dense(_out(out, q, (batch, heads, dim), _torch.bfloat16, dev), "out")
+    if lse is None:
+        lse = q.new_empty((batch, heads), dtype=_torch.float32)
+    else:
+        _dense(_out(lse, q, (batch, heads), _torch.float32, dev, "lse"), "lse")
     width = page_table.shape[1]
     need = _L.df11_paged_attention_workspace_bytes(batch, heads, c.kv_heads, dim, c.page_size, width)
     keep, ws, size = _workspace(workspace, need, q, dev)
