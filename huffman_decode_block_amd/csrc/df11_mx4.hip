@@ -357,6 +357,7 @@ constexpr uint32_t kStageBlocks = kStageK / kBlock;
 constexpr uint32_t kRowBytes = kStageK * 2;
 
 constexpr uint32_t kTileWaves = 4;
+constexpr uint32_t kBand = 8;
 
 template <int kTiles>
 __global__ void __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2)))
@@ -368,12 +369,13 @@ tile_kernel(MulParams p) {
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // workgroups go round the 8 XCDs; each XCD takes a run of neighbouring
-    // tiles, so that its L2 holds what they share
-    const uint32_t tiles = p.tiles_m * p.tiles_n;
-    const uint32_t id = blockIdx.x;
-    const uint32_t per = tiles / 8, more = tiles % 8, xcd = id % 8;
-    const uint32_t t = xcd * per + min(xcd, more) + id / 8;
-    const uint32_t m0 = (t % p.tiles_m) * kRowsM, n0 = (t / p.tiles_m) * kRowsN;
+    // tiles, in bands of 8 tiles along m, so that its L2 holds what the tiles of
+    // the moment share
+    const uint32_t tiles = p.tiles_m * p.tiles_n, per = tiles / 8, more = tiles % 8, xcd = blockIdx.x % 8;
+    const uint32_t t = xcd * per + min(xcd, more) + blockIdx.x / 8;
+    const uint32_t band = t / (kBand * p.tiles_n), in_band = t - band * kBand * p.tiles_n;
+    const uint32_t width = min(kBand, p.tiles_m - band * kBand);
+    const uint32_t m0 = (band * kBand + in_band % width) * kRowsM, n0 = in_band / width * kRowsN;
 
     const uint32_t stages = (p.blocks + kStageBlocks - 1) / kStageBlocks;
 
