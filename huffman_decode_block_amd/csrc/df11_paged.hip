@@ -42,12 +42,15 @@ struct AppendParams {
     uint32_t per_token, dim_shift, page_shift;  // kv_heads * head_dim / 8; head_dim / 8 = 1 << dim_shift
 };
 
-__device__ __forceinline__ v4u load8(const uint16_t *p, bool aligned) {
-    if (aligned) return *reinterpret_cast<const v4u *>(p);
+// Eight values that may start at any even address: the hardware loads them as
+// they lie, without the compiler having to take them apart.
+struct __attribute__((packed, aligned(2))) Eight {
     uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | (uint32_t{p[2 * i + 1]} << 16);
-    return v4u{w[0], w[1], w[2], w[3]};
+};
+
+__device__ __forceinline__ v4u load8(const uint16_t *p) {
+    const Eight t = *reinterpret_cast<const Eight *>(p);
+    return v4u{t.w[0], t.w[1], t.w[2], t.w[3]};
 }
 
 // x / scale for the eight values of a lane, rounded as a division: with r the
@@ -94,7 +97,7 @@ __device__ __forceinline__ v2u e4m3x8(v4u x, float scale) {
     return v2u{o[0], o[1]};
 }
 
-template <bool kE4M3, bool kAligned>
+template <bool kE4M3>
 __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
     const uint32_t per_head = 1u << p.dim_shift;
     for (uint64_t base = uint64_t{blockIdx.x} * 256; base < p.lanes; base += uint64_t{gridDim.x} * 256) {
@@ -106,8 +109,8 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
         const uint32_t d = in & (per_head - 1), h = in >> p.dim_shift;
         const int64_t slot = p.slots[t];
         if (slot < 0 || static_cast<uint64_t>(slot) >= p.n_slots) continue;
-        const v4u kv = load8(p.ks + t * p.k_token + h * p.k_head + 8 * d, kAligned);
-        const v4u vv = load8(p.vs + t * p.v_token + h * p.v_head + 8 * d, kAligned);
+        const v4u kv = load8(p.ks + t * p.k_token + h * p.k_head + 8 * d);
+        const v4u vv = load8(p.vs + t * p.v_token + h * p.v_head + 8 * d);
         const uint64_t page = static_cast<uint64_t>(slot) >> p.page_shift;
         const uint64_t row = static_cast<uint64_t>(slot) & ((uint64_t{1} << p.page_shift) - 1);
         uint8_t *ko = p.k.base + page * p.k.page + h * p.k.head + row * p.k.row;
@@ -165,8 +168,7 @@ struct AttnParams {
     float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
     uint64_t q_batch, q_head, table_stride, n_pages;
     uint32_t batch, q_heads, kv_heads, group, tiles, splits, page_shift, positions;  // positions: table_width * page_size
-    uint32_t q_wide;  // rows of q start at multiples of 16 bytes
-    float scale;      // times log2 e
+    float scale;  // times log2 e
 };
 
 struct Range {
@@ -207,8 +209,9 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 
 // Waves of a SIMD that the registers are held to (without it the compiler takes
 // more and leaves one or two): 8 x 32,768 positions in E4M3 101 -> 99 us, 32 x
-// 2,048 BF16 positions of 8 heads of 64 29.2 -> 28.1 us.
-constexpr int waves_for(int dim, bool e4m3) { return dim == 64 ? 4 : dim == 128 ? (e4m3 ? 4 : 3) : 1; }
+// 2,048 BF16 positions of 8 heads of 64 29.2 -> 28.1 us; BF16 heads of 256 are
+// left one wave, as two spill: 8 x 8,192 of 8 heads 94 us against 118.
+constexpr int waves_for(int dim, bool e4m3) { return dim == 64 ? 4 : dim == 128 ? (e4m3 ? 4 : 3) : e4m3 ? 2 : 1; }
 
 template <int kDim, bool kE4M3>
 __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim, kE4M3))))
@@ -264,7 +267,7 @@ attend_kernel(AttnParams p) {
 #pragma unroll
     for (int i = 0; i < kKChunks; ++i) {
         const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
-        qf[i] = __builtin_bit_cast(bf8, have ? load8(qp + d, p.q_wide) : v4u{0, 0, 0, 0});
+        qf[i] = __builtin_bit_cast(bf8, have ? load8(qp + d) : v4u{0, 0, 0, 0});
     }
     const float scale = kE4M3 ? p.scale * p.k.scale[h] : p.scale;
     const uint8_t *kb = p.k.base + h * p.k.head, *vb = p.v.base + h * p.v.head;
@@ -595,10 +598,7 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
     p.page_shift = log2_of(c->page_size);
     p.n_slots = c->n_pages * c->page_size;
     p.lanes = tokens * p.per_token;
-    const bool al = aligned16(k) && aligned16(v) && (k_token | k_head | v_token | v_head) % 8 == 0;
-    const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
-    auto fn = e4m3 ? (al ? append_kernel<true, true> : append_kernel<true, false>)
-                   : (al ? append_kernel<false, true> : append_kernel<false, false>);
+    auto fn = c->dtype == DF11_CACHE_E4M3 ? append_kernel<true> : append_kernel<false>;
     const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((p.lanes + 255) / 256, 1u << 20));
     return launched(launch(fn, grid, 256, 0, static_cast<hipStream_t>(hip_stream), p));
 }
@@ -654,7 +654,6 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     p.starts = starts;
     p.out = out;
     p.lse = lse;
-    p.q_wide = aligned16(q) && (q_batch | q_head) % 8 == 0;
     p.q_batch = q_batch;
     p.q_head = q_head;
     p.table_stride = table_stride;
