@@ -31,9 +31,12 @@ constexpr uint32_t kNanScale = 255;
 
 // ---- Quantisation ----------------------------------------------------------
 // Four lanes take one block of 32 values, 8 values (16 bytes) each; the
-// block's maximum goes round the four by two DPP exchanges.  Bound by HBM: 2
-// bytes read and 17/32 written for a value.  An item is a block; items are
-// numbered row by row, so that rows of any width fill the lanes.
+// block's maximum goes round the four by two DPP exchanges.  An item is a
+// block; items are numbered row by row, so that rows of any width fill the
+// lanes.  Bound by HBM: 2 bytes read and 17/32 written for a value, and the
+// other way round in the expansion: 4096 x 4096 in 9.8 and 9.3 us, 4.3 and 4.6
+// TB/s (a large copy reaches 4.7); 9001 x 1387, rows that start at any even
+// address, 9.0 and 8.1 us, where loads of one value at a time took 15.6 and 19.8.
 
 constexpr uint32_t kQuantThreads = 256;
 constexpr uint32_t kQuantItems = kQuantThreads / 4;  // blocks per workgroup and step
@@ -205,16 +208,16 @@ __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); 
 // choose, as long as both operands agree: its i-th instruction of a step takes
 // codes 8 i .. 8 i + 7 of every lane's block, so nothing moves between lanes and
 // one scale serves all of a lane's codes.
-// Bound by the path of vector loads as soon as those are not few and wide: x
-// comes in rows of 256 bytes a step by loads into the wave's own part of LDS
-// (one instruction for 4 rows; read into registers in the order of the matrix
-// instruction it took four for 16 rows, and 16 x 4096 x 14336 21 us, 7 without
-// them), and the scales of four steps in one load of 16 bytes (a byte for each
-// step: 1 x 128256 x 4096 90 us against 71).  Piece c of row i of x lies at
-// c ^ (i % 16), as in the tile form.
-// How the token form reads: kReadWide as above, for k in multiples of 512; kReadNarrow
-// with a byte of scales for each block; kReadAny also takes rows of x that start
-// anywhere and end inside a block, through registers.
+// Bound by HBM for the largest (1 x 128256 x 4096: 279 MB in 48 us, 5.8 TB/s), by
+// a kernel's own start and end for the smallest (1 x 4096 x 4096: 4 us), and by
+// the path of vector loads as soon as those are not few and wide.  So x comes
+// in rows of 256 bytes a step by loads into the wave's own part of LDS, one
+// instruction for 4 rows (piece c of row i lies at c ^ (i % 16), as in the tile
+// form), and the scales of four steps in one load of 16 bytes.  With x read
+// from memory in the order of the matrix instruction, four loads a step, and a
+// byte of scales for each block, 1 x 128256 x 4096 took 88 us and 16 x 4096 x
+// 14336 21 where it is 10.6 now.
+// Eight values of a row of k values, from column col on, zeros past its end.
 __device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint32_t k) {
     uint32_t w[4] = {0, 0, 0, 0};
     if (col + 8 <= k) {
@@ -228,17 +231,22 @@ __device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint3
     return v4u{w[0], w[1], w[2], w[3]};
 }
 
+// How the token form reads: kReadWide as above, for k in multiples of 512;
+// kReadNarrow with a byte of scales for each block; kReadAny also takes rows of
+// x that start anywhere and end inside a block, through registers.
 enum TokenReads : int { kReadWide, kReadNarrow, kReadAny };
 
-template <int kX, int kRows, int kWaves, int kAhead, int kReads>
-__global__ void __launch_bounds__(64 * kWaves)
+constexpr int kTokenWaves = 8;
+
+template <int kX, int kRows, int kAhead, int kReads>
+__global__ void __launch_bounds__(64 * kTokenWaves)
 token_kernel(MulParams p) {
     constexpr bool kWide = kReads == kReadWide;
     constexpr int kM = kX < 16 ? 1 : kX / 16;  // tiles of x
     constexpr uint32_t kGroup = 4;             // steps whose scales are loaded together
     constexpr uint32_t kStepBytes = kX * 256, kWaveBytes = kAhead * kStepBytes;
     constexpr uint32_t kSumBytes = kM * kRows * 1024;  // of a wave
-    __shared__ __attribute__((aligned(1024))) uint8_t s_x[kWaves * (kWaveBytes > kSumBytes ? kWaveBytes : kSumBytes)];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_x[kTokenWaves * (kWaveBytes > kSumBytes ? kWaveBytes : kSumBytes)];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n0 = blockIdx.x * 16 * kRows, m0 = blockIdx.y * kX;
@@ -250,7 +258,7 @@ token_kernel(MulParams p) {
     const Rsrc xr = rsrc(x0, (rows_m - 1) * row_bytes + k_bytes);
     uint8_t *mine = s_x + wave * kWaveBytes;
     f4 acc[kM][kRows] = {};
-    for (uint32_t g0 = wave * kGroup * 4; g0 < p.blocks; g0 += kWaves * kGroup * 4) {
+    for (uint32_t g0 = wave * kGroup * 4; g0 < p.blocks; g0 += kTokenWaves * kGroup * 4) {
         uint32_t sc[kRows][kGroup];  // byte i of word a: the scale of block i of the group's step a in row r
         if (kWide) {
 #pragma unroll
@@ -330,13 +338,13 @@ token_kernel(MulParams p) {
         for (uint32_t t = 0; t < kRows; ++t)
             *reinterpret_cast<f4 *>(sum + ((wave * kM + u) * kRows + t) * 256 + r * 16 + 4 * q) = acc[u][t];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < kM * kRows * 256; i += 64 * kWaves) {
+    for (uint32_t i = threadIdx.x; i < kM * kRows * 256; i += 64 * kTokenWaves) {
         // neighbouring threads take neighbouring columns of a row
         const uint32_t col = i % (16 * kRows), row = i / (16 * kRows);
         const uint32_t at = ((row / 16) * kRows + col / 16) * 256 + row % 16 * 16 + col % 16;
         float v = 0;
 #pragma unroll
-        for (uint32_t k = 0; k < kWaves; ++k) v += sum[k * kM * kRows * 256 + at];
+        for (uint32_t k = 0; k < kTokenWaves; ++k) v += sum[k * kM * kRows * 256 + at];
         if (row < rows_m && col < rows_n)
             p.y[uint64_t{m0 + row} * p.y_stride + n0 + col] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
@@ -352,6 +360,12 @@ token_kernel(MulParams p) {
 // that the 16 rows a read touches use all banks once.  Row m of a wave's t-th
 // tile of w is row 16 (m / 4) + 4 t + m % 4 of its 64, which leaves a lane
 // with 16 neighbouring columns of y in the end.
+// Bound by the matrix unit, held back by the loads of a stage: 8192 x 8192 x 8192
+// in 805 us, 1.37 PFLOP/s (a large BF16 product of the vendor's library reaches 1.39 on
+// the same card), 2048 x 14336 x 4096 197 us, 1.22; without the loads of the
+// next stage the latter takes 167, without expanding the codes no less than
+// with.  Two workgroups of four waves on a compute unit hide one another's
+// barriers: one of eight waves and 256 rows took 204.
 constexpr uint32_t kStageK = 128;
 constexpr uint32_t kStageBlocks = kStageK / kBlock;
 constexpr uint32_t kRowBytes = kStageK * 2;
@@ -370,7 +384,7 @@ tile_kernel(MulParams p) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // workgroups go round the 8 XCDs; each XCD takes a run of neighbouring
     // tiles, in bands of 8 tiles along m, so that its L2 holds what the tiles of
-    // the moment share
+    // the moment share (8192 x 8192 x 8192: 805 us, 854 with all of m in a band)
     const uint32_t tiles = p.tiles_m * p.tiles_n, per = tiles / 8, more = tiles % 8, xcd = blockIdx.x % 8;
     const uint32_t t = xcd * per + min(xcd, more) + blockIdx.x / 8;
     const uint32_t band = t / (kBand * p.tiles_n), in_band = t - band * kBand * p.tiles_n;
@@ -418,7 +432,8 @@ tile_kernel(MulParams p) {
     // Stage: 4 steps of 32 along k, in each 4 kTiles matrix instructions.  A
     // piece of x is read for the next step as soon as this step is done with
     // the registers it goes to, and the next step's codes are expanded beside;
-    // the order is given to the compiler in groups.
+    // the order is given to the compiler in groups (left to itself it read just
+    // before use: 2048 x 14336 x 4096 239 us against 212, in tiles of 256 rows).
     f4 acc[kTiles][4] = {};
     auto expand = [&](const W &w, int j, bf8 (&to)[4]) {
 #pragma unroll
@@ -552,12 +567,13 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
                            static_cast<uint32_t>(cols), blocks, items, out, out_stride));
 }
 
-// The form of a product: workgroups of the token form take 16 rows of w and up
-// to 64 of x to 64 by 64, of the tile form 64, 128 or 256 rows of x by 256 of w.
+// The form of a product.  A workgroup of the token form takes a piece of 4, 16,
+// 32 or 64 rows of x by 16, 32 or 64 of w, one of the tile form 64 or 128 rows of x
+// by 256 of w.
 //  - Up to 32 rows, and as long as 64 x 64 pieces make no more than two for
 //    each of 256 compute units, the token form, whose waves share k, is the
 //    faster one: 512 x 4096 x 4096 32.2 us against 36.6 for the best of the tile
-//    form (k split over workgroups and joined), 256 x 14336 x 4096 (896 pieces) 64.0
+//    form (then with k split over workgroups and joined), 256 x 14336 x 4096 (896 pieces) 64.0
 //    against 46.8.
 //  - In the token form the largest piece that leaves 160 workgroups (256 of
 //    16 rows): 64 x 4096 x 4096 8.2 us by 32 x 32 (256 workgroups), 10.8 by 64 x 32 (128)
@@ -591,12 +607,11 @@ Form form_of(uint64_t m, uint64_t n) {
 
 template <int kX, int kRows, int kAhead>
 hipError_t launch_token(int reads, hipStream_t st, const MulParams &p) {
-    constexpr int kWaves = 8;
     const dim3 grid((p.n + 16 * kRows - 1) / (16 * kRows), (p.m + kX - 1) / kX);
-    return launch(reads == kReadWide     ? token_kernel<kX, kRows, kWaves, kAhead, kReadWide>
-                  : reads == kReadNarrow ? token_kernel<kX, kRows, kWaves, kAhead, kReadNarrow>
-                                         : token_kernel<kX, kRows, kWaves, kAhead, kReadAny>,
-                  grid, 64 * kWaves, st, p);
+    return launch(reads == kReadWide     ? token_kernel<kX, kRows, kAhead, kReadWide>
+                  : reads == kReadNarrow ? token_kernel<kX, kRows, kAhead, kReadNarrow>
+                                         : token_kernel<kX, kRows, kAhead, kReadAny>,
+                  grid, 64 * kTokenWaves, st, p);
 }
 
 // Rows of x are read 16 bytes and whole blocks at a time, with byte offsets of

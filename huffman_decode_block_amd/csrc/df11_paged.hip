@@ -29,8 +29,10 @@ struct Pages {
 };
 
 // ---- Append ----------------------------------------------------------------
-// A lane moves 8 values of K and the same 8 of V.  Bound by latency for the
-// tokens of a step, by HBM for a prompt.
+// A lane moves 8 values of K and the same 8 of V.  Bound by the launch for the
+// tokens of a step (32 tokens of 8 heads of 128: 2.6 us, the shortest a kernel
+// takes here), by HBM for a prompt (8,192 tokens into E4M3 pages: 50 MB in 11.3
+// us, 4.5 TB/s, where a large copy reaches 4.7).
 
 struct AppendParams {
     Pages k, v;
@@ -78,6 +80,7 @@ __device__ __forceinline__ float to_e4m3_range(uint32_t bits, const Scale &s) {
         const float q = x * s.r;
         v = fabsf(q) < 1024.0f ? fmaf(fmaf(-q, s.s, x), s.r, q) : q;
     }
+    v = copysignf(v, x * s.r);  // the correction turns -0 into 0
     return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
 }
 
@@ -148,7 +151,11 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 // The weights exp(s - m) lie in [0, 1]; one BF16 number would add an error as
 // large as the output's own rounding, so they are given as two, high part and
 // remainder.  The matrix unit has time for it: the kernel is bound by reading
-// K and V.
+// K and V, each once.  At 8 sequences of 32,768 positions, 8 cache heads of 128
+// and 64 query heads: BF16 1.07 GB in 187 us, 5.7 TB/s; E4M3 537 MB in 99 us, 5.4
+// TB/s.  Where there is less to read the start and the end count: one sequence
+// of 8,192 takes 9.7 us and its join 3.9 (33.5 MB would take 5.9 at the former
+// rate), 64 ragged ones up to 1,024 positions 33 us for 124 MB.
 
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;
@@ -164,7 +171,7 @@ struct AttnParams {
     const int32_t *table, *lens, *starts;
     uint16_t *out;
     float *lse;
-    float *part;   // [batch * q_heads][splits][head_dim], weighted values over their sum
+    float *part;   // [batch * q_heads][splits][head_dim]: sums of weighted values
     float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
     uint64_t q_batch, q_head, table_stride, n_pages;
     uint32_t batch, q_heads, kv_heads, group, tiles, splits, page_shift, positions;  // positions: table_width * page_size
