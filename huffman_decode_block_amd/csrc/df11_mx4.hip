@@ -225,8 +225,10 @@ __device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint3
         w[0] = t.w[0], w[1] = t.w[1], w[2] = t.w[2], w[3] = t.w[3];
     } else if (col < k) {
 #pragma unroll
-        for (uint32_t i = 0; i < 7; ++i)
-            if (col + i < k) w[i / 2] |= uint32_t{row[col + i]} << (16 * (i & 1));
+        for (uint32_t i = 0; i < 7; ++i) {
+            const uint32_t v = row[min(col + i, k - 1)];  // no branch for each value
+            w[i / 2] |= (col + i < k ? v : 0u) << (16 * (i & 1));
+        }
     }
     return v4u{w[0], w[1], w[2], w[3]};
 }
@@ -242,8 +244,8 @@ template <int kX, int kRows, int kAhead, int kReads>
 __global__ void __launch_bounds__(64 * kTokenWaves)
 token_kernel(MulParams p) {
     constexpr bool kWide = kReads == kReadWide;
-    constexpr int kM = kX < 16 ? 1 : kX / 16;  // tiles of x
-    constexpr uint32_t kGroup = 4;             // steps whose scales are loaded together
+    constexpr int kM = kX < 16 ? 1 : kX / 16;        // tiles of x
+    constexpr uint32_t kGroup = kWide ? 4 : kAhead;  // steps that a wave takes together: those whose scales are one load
     constexpr uint32_t kStepBytes = kX * 256, kWaveBytes = kAhead * kStepBytes;
     constexpr uint32_t kSumBytes = kM * kRows * 1024;  // of a wave
     __shared__ __attribute__((aligned(1024))) uint8_t s_x[kTokenWaves * (kWaveBytes > kSumBytes ? kWaveBytes : kSumBytes)];
@@ -665,9 +667,11 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         p.x_stride = width;
     }
     if (f.token) {
-        const int reads = !readable || k % kBlock != 0                    ? kReadAny
-                          : p.blocks % 16 == 0 && aligned16(scales) ? kReadWide
-                                                                    : kReadNarrow;
+        // kReadWide gives a wave 512 of k at a time: below 2,048 that leaves more
+        // than half of the waves idle (512 x 4096 x 1024 18.7 us against 16.5; at
+        // 2,048 16 x 14336 takes 6.1 against 7.5)
+        const bool wide = p.blocks % 16 == 0 && p.blocks >= 64 && aligned16(scales);
+        const int reads = !readable || k % kBlock != 0 ? kReadAny : wide ? kReadWide : kReadNarrow;
         switch (f.x + f.rows) {
             case 4 + 1: return launched(launch_token<4, 1, 4>(reads, st, p));
             case 16 + 1: return launched(launch_token<16, 1, 2>(reads, st, p));
