@@ -353,8 +353,8 @@ token_kernel(MulParams p) {
 }
 
 // Tile form, for many rows: a workgroup computes a tile of 16 kTiles rows of x
-// by 256 rows of w, each of its four waves 16 kTiles by 64 of it, in stages of
-// 128 along k.  x goes to LDS by loads that write there directly, two
+// by 256 rows of w, each wave of a group of four 16 kTiles by 64 of it, in stages
+// of 128 along k; two groups take the stages in turn and add their sums.  x goes to LDS by loads that write there directly, two
 // stages, the next one loading while one is computed.  The codes go from
 // memory to the registers of the waves that use them and are expanded there:
 // a lane's 16 bytes are one block of 32, k as in the token form.  A row of x
@@ -362,12 +362,15 @@ token_kernel(MulParams p) {
 // that the 16 rows a read touches use all banks once.  Row m of a wave's t-th
 // tile of w is row 16 (m / 4) + 4 t + m % 4 of its 64, which leaves a lane
 // with 16 neighbouring columns of y in the end.
+// Scales come with kWide, for k in multiples of 512, for four stages at a time
+// and through LDS like x; else by a byte for each block (8192 x 8192 x 8192: 744
+// us against 805, 1024 x 4096 x 4096 39 against 46).
 // Bound by the matrix unit, held back by the loads of a stage: 8192 x 8192 x 8192
-// in 805 us, 1.37 PFLOP/s (a large BF16 product of the vendor's library reaches 1.39 on
-// the same card), 2048 x 14336 x 4096 197 us, 1.22; without the loads of the
-// next stage the latter takes 167, without expanding the codes no less than
-// with.  Two workgroups of four waves on a compute unit hide one another's
-// barriers: one of eight waves and 256 rows took 204.
+// in 744 us, 1.48 PFLOP/s (a large BF16 product of the vendor's library reaches
+// 1.39 on the same card), 2048 x 14336 x 4096 in 186, 1.30; expanding the codes
+// costs nothing beside the matrix instructions.  Two workgroups of four waves
+// on a compute unit hide one another's barriers: one of eight waves and 256
+// rows was no faster (204 us against 197 for 2048 x 14336 x 4096 at the time).
 constexpr uint32_t kStageK = 128;
 constexpr uint32_t kStageBlocks = kStageK / kBlock;
 constexpr uint32_t kRowBytes = kStageK * 2;
@@ -375,18 +378,23 @@ constexpr uint32_t kRowBytes = kStageK * 2;
 constexpr uint32_t kTileWaves = 4;
 constexpr uint32_t kBand = 8;
 
-template <int kTiles>
-__global__ void __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2)))
+template <int kTiles, int kGroups, bool kWide>
+__global__ void __launch_bounds__(64 * kTileWaves * kGroups) __attribute__((amdgpu_waves_per_eu(2)))
 tile_kernel(MulParams p) {
     constexpr uint32_t kRowsM = 16 * kTiles, kRowsN = 64 * kTileWaves;
     constexpr int kLoads = kRowsM / 4 / kTileWaves;  // a wave's loads of a stage: 4 rows each, 16 rows from one another
-    __shared__ __attribute__((aligned(1024))) uint8_t s_x[2 * kRowsM * kRowBytes];
+    constexpr uint32_t kGroupBytes = 2 * kRowsM * kRowBytes;  // two stages; as many bytes as a group's sums
+    __shared__ __attribute__((aligned(1024))) uint8_t s_all[kGroups * kGroupBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_scale[kWide ? kGroups * kTileWaves * 2 * 1024 : 16];
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kTileWaves;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kTileWaves;
+    uint8_t *s_x = s_all + group * kGroupBytes;
     // workgroups go round the 8 XCDs; each XCD takes a run of neighbouring
     // tiles, in bands of 8 tiles along m, so that its L2 holds what the tiles of
-    // the moment share (8192 x 8192 x 8192: 805 us, 854 with all of m in a band)
+    // the moment share (8192 x 8192 x 8192: 854 us with all of m in a band, 805 in
+    // bands of 8 at the time)
     const uint32_t tiles = p.tiles_m * p.tiles_n, per = tiles / 8, more = tiles % 8, xcd = blockIdx.x % 8;
     const uint32_t t = xcd * per + min(xcd, more) + blockIdx.x / 8;
     const uint32_t band = t / (kBand * p.tiles_n), in_band = t - band * kBand * p.tiles_n;
@@ -416,6 +424,14 @@ tile_kernel(MulParams p) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(to + (i * kTileWaves + wave) * 1024), 16,
                                                      off + 4 * kTileWaves * i * row_bytes, k0, 0, 0);
     };
+    // scales of the wave's 64 rows: 16 bytes of a row, four stages', in one load
+    // into the wave's part of LDS, two parts in turn
+    uint8_t *scale_part = s_scale + (group * kTileWaves + wave) * 2048;
+    auto load_scales = [&](uint32_t four) {
+        const uint32_t row = 64 * wave + lane;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (LdsPtr)(scale_part + (four & 1) * 1024), 16, row * p.blocks,
+                                                 __builtin_amdgcn_readfirstlane(four * 16), 0, 0);
+    };
     struct W {
         v4u code[4];
         uint32_t scale[4];
@@ -427,8 +443,13 @@ tile_kernel(MulParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w.code[i] = __builtin_amdgcn_raw_buffer_load_b128(wr, code_off + 4 * i * p.blocks * 16, at * 16, 0);
-            w.scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, scale_off + 4 * i * p.blocks, at, 0);
+            if (!kWide) w.scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, scale_off + 4 * i * p.blocks, at, 0);
         }
+    };
+    auto read_scales = [&](uint32_t stage, W &w) {
+        const uint8_t *at = scale_part + (stage / 4 & 1) * 1024 + (16 * (r / 4) + r % 4) * 16 + stage % 4 * 4 + q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.scale[i] = at[4 * i * 16];
     };
 
     // Stage: 4 steps of 32 along k, in each 4 kTiles matrix instructions.  A
@@ -475,22 +496,45 @@ tile_kernel(MulParams p) {
     };
 
     W w, next;
-    if (stages) {
-        load_x(0, s_x);
-        load_w(0, w);
+    if (group < stages) {
+        load_x(group, s_x);
+        load_w(group, w);
+        if (kWide) load_scales(group / 4);
     }
     uint32_t flip = 0;
-    for (uint32_t s = 0; s < stages; ++s) {
+    for (uint32_t s0 = 0; s0 < stages; s0 += kGroups) {  // the same count for all waves, which meet in it
+        const uint32_t s = s0 + group;
         arrived();
-        __syncthreads();  // stage s is there, stage s - 1 is read
+        __syncthreads();  // stage s is there, the one before is read
         const uint32_t other = flip ^ (kRowsM * kRowBytes);
-        if (s + 1 < stages) {
-            load_x(s + 1, s_x + other);
-            load_w(s + 1, next);
+        if (s + kGroups < stages) {
+            load_x(s + kGroups, s_x + other);
+            load_w(s + kGroups, next);
+            if (kWide && (s + kGroups) / 4 != s / 4) load_scales((s + kGroups) / 4);
         }
-        compute(s_x + flip, w);
+        if (s < stages) {
+            if (kWide) read_scales(s, w);
+            compute(s_x + flip, w);
+        }
         w = next;
         flip = other;
+    }
+    if (kGroups == 2) {  // the second group's sums through LDS to the first
+        static_assert(kRowsM * kRowsN * 4 <= 2 * kGroupBytes, "a group's sums fit");
+        f4 *sum = reinterpret_cast<f4 *>(s_all) + (wave * 64 + lane);
+        __syncthreads();
+        if (group == 1) {
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[(4 * m + i) * 64 * kTileWaves] = acc[m][i];
+        }
+        __syncthreads();
+        if (group == 1) return;
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][i] += sum[(4 * m + i) * 64 * kTileWaves];
     }
 
     // a lane: columns 16 q .. 16 q + 15 of the wave's 64, row r of each tile
@@ -574,17 +618,19 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
 // by 256 of w.
 //  - Up to 32 rows, and as long as 64 x 64 pieces make no more than two for
 //    each of 256 compute units, the token form, whose waves share k, is the
-//    faster one: 512 x 4096 x 4096 32.2 us against 36.6 for the best of the tile
-//    form (then with k split over workgroups and joined), 256 x 14336 x 4096 (896 pieces) 64.0
-//    against 46.8.
+//    faster one: 512 x 4096 x 4096 33.7 us against 35.7 for the best tiles, 256 x
+//    14336 x 4096 (896 pieces) 65.0 against 36.9.
 //  - In the token form the largest piece that leaves 160 workgroups (256 of
 //    16 rows): 64 x 4096 x 4096 8.2 us by 32 x 32 (256 workgroups), 10.8 by 64 x 32 (128)
 //    and 15.8 by 64 x 64 (64); 16 x 14336 x 4096 9.5 by 16 x 32 (448), 10.1 by 16 x 64 (224),
 //    11.7 by 16 x 16.
-//  - In the tile form 128 rows where those give 160 tiles, else 64: 1536 x 4096
-//    x 4096 (192 tiles of 128) 60 us against 75, 1024 x 4096 x 4096 (128) 57
-//    against 47.  256 rows by eight waves were no faster: 2048 x 14336 x 4096 204
-//    us against 197, 4096 x 4096 x 4096 105 against 109.
+//  - In the tile form 128 rows where those give 256 tiles, else 64: 2048 x 4096 x
+//    4096 (256 tiles of 128) 56.8 us against 58.8, 1536 x 4096 x 4096 (192) 54.7
+//    against 52.4, 1024 x 4096 x 4096 (128) 51 against 39.
+//  - Up to 256 tiles, one for a compute unit, a tile has two groups of waves
+//    that take stages in turn: 1024 x 4096 x 4096 39.0 us against 42.2, 2048 x 4096 x
+//    14336 188 against 212; with more tiles other workgroups are there to fill
+//    the waits (1536 x 4096 x 4096, 384 tiles of 64: 68 against 52).
 struct Form {
     bool token;
     uint32_t x, rows;  // rows of x in a piece or tile; token form: tiles of 16 rows of w
@@ -595,7 +641,7 @@ uint64_t pieces(uint64_t m, uint64_t x, uint64_t n, uint64_t w) { return ((m + x
 Form form_of(uint64_t m, uint64_t n) {
     if (m <= 4) return {true, 4, 1};
     if (m > 32 && pieces(m, 64, n, 64) > 512)
-        return {false, pieces(m, 128, n, 256) >= 160 ? 128u : 64u, 0};
+        return {false, pieces(m, 128, n, 256) >= 256 ? 128u : 64u, 0};
     if (m > 32)
         for (uint32_t rows : {4u, 2u})
             if (pieces(m, 64, n, 16 * rows) >= 160) return {true, 64, rows};
@@ -666,12 +712,12 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         p.x = static_cast<const uint16_t *>(workspace);
         p.x_stride = width;
     }
+    const bool wide = p.blocks % 16 == 0 && aligned16(scales);
     if (f.token) {
         // kReadWide gives a wave 512 of k at a time: below 2,048 that leaves more
         // than half of the waves idle (512 x 4096 x 1024 18.7 us against 16.5; at
         // 2,048 16 x 14336 takes 6.1 against 7.5)
-        const bool wide = p.blocks % 16 == 0 && p.blocks >= 64 && aligned16(scales);
-        const int reads = !readable || k % kBlock != 0 ? kReadAny : wide ? kReadWide : kReadNarrow;
+        const int reads = !readable || k % kBlock != 0 ? kReadAny : wide && p.blocks >= 64 ? kReadWide : kReadNarrow;
         switch (f.x + f.rows) {
             case 4 + 1: return launched(launch_token<4, 1, 4>(reads, st, p));
             case 16 + 1: return launched(launch_token<16, 1, 2>(reads, st, p));
@@ -686,8 +732,13 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
     p.tiles_n = static_cast<uint32_t>((n + 255) / 256);
     const dim3 grid(static_cast<uint32_t>(tiles));
-    return launched(f.x == 128 ? launch(tile_kernel<8>, grid, 64 * kTileWaves, st, p)
-                               : launch(tile_kernel<4>, grid, 64 * kTileWaves, st, p));
+    const bool two = tiles <= 256;
+    const uint32_t threads = 64 * kTileWaves * (two ? 2 : 1);
+    return launched(launch(f.x == 128 ? wide ? (two ? tile_kernel<8, 2, true> : tile_kernel<8, 1, true>)
+                                             : (two ? tile_kernel<8, 2, false> : tile_kernel<8, 1, false>)
+                           : wide     ? (two ? tile_kernel<4, 2, true> : tile_kernel<4, 1, true>)
+                                      : (two ? tile_kernel<4, 2, false> : tile_kernel<4, 1, false>),
+                           grid, threads, st, p));
 }
 
 }  // namespace
