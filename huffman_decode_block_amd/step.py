@@ -11,6 +11,7 @@ allocates belongs to that stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 _u64 = ctypes.c_uint64
 _u32 = ctypes.c_uint32
@@ -150,14 +151,15 @@ def _codes(codes, scales, cols, dev):
     """Checks codes and scale bytes of a matrix with `cols` columns; returns its rows and GPU."""
     u8 = _torch.uint8
     dev = _tensor(codes, "codes", u8, 2, dev)
-    _tensor(scales, "scales", u8, 2, dev)
-    if not (codes.is_contiguous() and scales.is_contiguous()):
-        raise ValueError("codes and scales must be contiguous")
-    blocks = (cols + 31) // 32
     rows, width = codes.shape
-    if width != 16 * blocks or scales.shape != (rows, blocks):
+    blocks = (cols + 31) // 32
+    if not (isinstance(scales, _torch.Tensor) and scales.dtype is u8 and scales.get_device() == dev):
+        _tensor(scales, "scales", u8, 2, dev)
+    if scales.shape != (rows, blocks) or width != 16 * blocks:
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {cols} columns: "
                          f"[rows, {16 * blocks}] and [rows, {blocks}] expected")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
     return rows, dev
 
 
@@ -233,28 +235,33 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
     when None and needed.  Returns out."""
     torch = _torch or _load()
     dev = _tensor(x, "x", torch.bfloat16, 2, -1)
-    _last_dense(x, "x")
-    n, _ = _codes(codes, scales, x.shape[1], dev)
+    m, k = x.shape
+    xs, x1 = x.stride()
+    if x1 != 1 and k > 1:
+        raise ValueError("the last dimension of x must be contiguous")
+    if m <= 1:  # torch leaves the stride of a single row open
+        xs = k or 1
+    n, _ = _codes(codes, scales, k, dev)
     handle, ctx = _place(dev, stream)
     if ctx is None:
-        return _matmul(x, codes, scales, n, out, workspace, dev, handle)
+        return _matmul(x, m, k, xs, codes, scales, n, out, workspace, dev, handle)
     with ctx:
-        return _matmul(x, codes, scales, n, out, workspace, dev, handle)
+        return _matmul(x, m, k, xs, codes, scales, n, out, workspace, dev, handle)
 
 
-def _matmul(x, codes, scales, n, out, workspace, dev, handle):
-    m, k = x.shape
+def _matmul(x, m, k, xs, codes, scales, n, out, workspace, dev, handle):
     if out is None:
-        out, ys = x.new_empty((m, n)), n if n else 1
+        out, ys = x.new_empty((m, n)), n or 1
     else:
         ys = _row_stride(_out(out, x, (m, n), _torch.bfloat16, dev))
-    xs, xp = _row_stride(x), x.data_ptr()
+    xp = x.data_ptr()
     keep, ws, size = workspace, None, 0
     if workspace is not None or k % 32 or xs % 8 or xp % 16 or xs > 1 << 21:
         need = _L.df11_mx4_matmul_workspace_bytes(m, n, k, xs % 8 == 0 and xp % 16 == 0 and xs <= 1 << 21)
         keep, ws, size = _workspace(workspace, need, x, dev)
-    _check(_L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), ys, ws, size, handle),
-           "df11_mx4_matmul")
+    st = _L.df11_mx4_matmul(xp, m, k, xs, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), ys, ws, size, handle)
+    if st:
+        _check(st, "df11_mx4_matmul")
     return out
 
 
@@ -267,13 +274,18 @@ def _cache(k_pages, v_pages, k_scale, v_scale, dev):
         raise TypeError(f"pages must be device tensors of bfloat16 or float8_e4m3fn, got {dtype}")
     _tensor(k_pages, "k_pages", dtype, 4, dev)
     _tensor(v_pages, "v_pages", dtype, 4, dev)
-    n, h, page, d = k_pages.shape
-    if v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    if v_pages.shape != shape:
         raise ValueError("k_pages and v_pages differ in shape")
+    n, h, page, d = shape
     k0, k1, k2, k3 = k_pages.stride()
     v0, v1, v2, v3 = v_pages.stride()
     if k3 != 1 or v3 != 1:
         raise ValueError("the last dimension of the pages must be contiguous")
+    if n == 1:  # torch leaves the strides of single pages and heads open
+        k0 = v0 = 0
+    if h == 1:
+        k1 = v1 = 0
     ks = vs = None
     if e4m3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
@@ -351,13 +363,14 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
     c = _cache(k_pages, v_pages, k_scale, v_scale, dev)
     _tensor(page_table, "page_table", i32, 2, dev)
     _last_dense(page_table, "page_table")
-    _tensor(lens, "lens", i32, 1, dev)
-    _dense(lens, "lens")
     batch, heads, dim = q.shape
-    if dim != c.head_dim or c.kv_heads == 0 or heads % c.kv_heads:
-        raise ValueError(f"q {tuple(q.shape)} does not fit pages of {c.kv_heads} heads of {c.head_dim}")
+    kv_heads = c.kv_heads
+    if dim != c.head_dim or kv_heads == 0 or heads % kv_heads:
+        raise ValueError(f"q {tuple(q.shape)} does not fit pages of {kv_heads} heads of {c.head_dim}")
+    _tensor(lens, "lens", i32, 1, dev)
     if page_table.shape[0] != batch or lens.shape[0] != batch:
         raise ValueError(f"page_table and lens must hold {batch} sequences")
+    _dense(lens, "lens")
     if starts is not None:
         _tensor(starts, "starts", i32, 1, dev)
         _dense(starts, "starts")
@@ -382,11 +395,18 @@ def _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, 
     else:
         _dense(_out(lse, q, (batch, heads), _torch.float32, dev, "lse"), "lse")
     width = page_table.shape[1]
-    need = _L.df11_paged_attention_workspace_bytes(batch, heads, c.kv_heads, dim, c.page_size, width)
+    need = _attention_need(batch, heads, c.kv_heads, dim, c.page_size, width)
     keep, ws, size = _workspace(workspace, need, q, dev)
     q0, q1, _ = q.stride()
-    _check(_L.df11_paged_attention(ctypes.byref(c), q.data_ptr(), batch, heads, q0, q1, page_table.data_ptr(),
-                                   page_table.stride(0) if batch > 1 else width, width, lens.data_ptr(),
-                                   None if starts is None else starts.data_ptr(), scale, out.data_ptr(),
-                                   lse.data_ptr(), ws, size, handle), "df11_paged_attention")
+    st = _L.df11_paged_attention(ctypes.byref(c), q.data_ptr(), batch, heads, q0, q1, page_table.data_ptr(),
+                                 page_table.stride(0) if batch > 1 else width, width, lens.data_ptr(),
+                                 None if starts is None else starts.data_ptr(), scale, out.data_ptr(), lse.data_ptr(),
+                                 ws, size, handle)
+    if st:
+        _check(st, "df11_paged_attention")
     return out, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_need(*sizes):
+    return int(_L.df11_paged_attention_workspace_bytes(*sizes))
