@@ -184,6 +184,31 @@ def test_product_against_64_bits(torch, m, n, k):
     assert torch.equal(y, hdb.df11_mx4_matmul(x, c, s)), "a second call differs"
 
 
+# One for each way a product is taken: pieces of 16 x 32, 16 x 64, 32 x 32, 32 x 64, 64 x 32 and
+# 64 x 64, tiles of 64 and 128 rows with one group of waves and with two; k in whole
+# 512s, whole 32s, and ending inside a block.
+FORMS = [
+    (16, 8210, 2048), (16, 16390, 2048), (16, 16390, 160), (7, 16390, 77), (32, 5130, 2048), (30, 5130, 99), (32, 10250, 2048),
+    (20, 10250, 160), (29, 10250, 45), (130, 2100, 2048), (64, 10250, 2048), (100, 5200, 333), (1100, 5000, 512), (1100, 5000, 96),
+    (1024, 4096, 1536), (900, 4100, 1056), (2048, 4100, 512), (2050, 4100, 160), (2048, 4096, 1024), (2040, 4090, 544),
+    (2048, 4096, 70), (16, 8192, 11008),
+]
+
+
+@pytest.mark.parametrize("m,n,k", FORMS)
+def test_product_in_every_form(torch, m, n, k):
+    """The same bound, with the 64-bit sums taken on the GPU."""
+    say(f"product {m}x{n}x{k}")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k)
+    xd = torch.from_numpy(bf16_values(xb)).cuda()
+    wd = torch.from_numpy(values(codes, scales, k)).cuda().T.contiguous()
+    ref, total = xd @ wd, xd.abs() @ wd.abs()
+    bound = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * k * 2.0 ** -23 * total
+    y = hdb.df11_mx4_matmul(x, c, s)
+    assert bool(((y.double() - ref).abs() <= bound).all())
+    assert torch.equal(y, hdb.df11_mx4_matmul(x, c, s)), "a second call differs"
+
+
 @pytest.mark.parametrize("m,n,k,pad,offset", [
     (1, 96, 128, 0, 1), (4, 96, 128, 8, 8), (19, 50, 256, 3, 2), (90, 200, 96, 5, 0), (150, 129, 100, 0, 4), (260, 140, 64, 8, 3),
     (1500, 1500, 70, 1, 0), (1600, 1411, 64, 0, 1), (70, 3000, 515, 0, 0),
