@@ -129,12 +129,17 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 }
 
 // ---- Attention of one token ------------------------------------------------
-// A sequence's positions are cut into up to `splits` chunks of the same size, a
-// multiple of 128, by the lengths as the device finds them; a workgroup takes one
-// chunk of one cache head for up to 16 of its query heads, its four waves the
-// chunk's steps of 32 positions in turn.  Each wave keeps the running maximum,
-// sum and weighted values of what it has seen, the waves join in LDS, and a
-// second kernel joins the chunks.
+// A sequence's positions are cut into chunks of multiples of 128 positions, by the
+// lengths as the device finds them; a workgroup takes one chunk of one cache head
+// for up to 16 of its query heads, its four waves the chunk's steps of 32
+// positions in turn.  Each wave keeps the running maximum, sum and weighted values
+// of what it has seen, the waves join in LDS, and a second kernel joins the
+// chunks.  The host knows the page table's width and not the lengths, so it
+// chooses one of three ways to share the work (Order), and the device fits it to
+// the lengths:
+//   kAsGiven   every sequence is cut into up to `splits` chunks
+//   kByLength  one chunk each; compute units get long and short sequences in turn
+//   kEvenly    chunks of one length for all sequences, long ones have more of them
 //
 // Products are matrix instructions of 16 x 16 x 32 in this orientation:
 //   scores^T [position, head] = K [position, d] Q^T [d, head]
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 // and 64 query heads: BF16 1.07 GB in 187 us, 5.7 TB/s; E4M3 537 MB in 99 us, 5.4
 // TB/s.  Where there is less to read the start and the end count: one sequence
 // of 8,192 takes 9.7 us and its join 3.9 (33.5 MB would take 5.9 at the former
-// rate), 64 ragged ones up to 1,024 positions 33 us for 124 MB.
+// rate), 64 ragged ones up to 1,024 positions 28 us for 124 MB.
 
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;
@@ -163,6 +168,11 @@ constexpr uint32_t kMinChunk = kWaves * kStep;
 constexpr uint32_t kMaxChunk = 4096;
 constexpr uint32_t kMinPage = 8, kMaxPage = 1024;
 constexpr uint32_t kHeadTile = 16;
+constexpr uint32_t kComputeUnits = 256;
+constexpr uint32_t kLaneSequences = 256;  // sequences that a wave's lanes can hold
+constexpr uint32_t kClassBits = 8;
+
+enum Order { kAsGiven, kByLength, kEvenly };  // order_of has the rule and its figures
 constexpr uint32_t kPad = 4;  // floats between a head's values in LDS: the heads start in different banks
 
 struct AttnParams {
@@ -175,6 +185,9 @@ struct AttnParams {
     float *stats;  // [batch * q_heads][splits][2]: maximum (of log2 units) and sum
     uint64_t q_batch, q_head, table_stride, n_pages;
     uint32_t batch, q_heads, kv_heads, group, tiles, splits, page_shift, positions;  // positions: table_width * page_size
+    uint32_t class_shift;  // kByLength: classes of lengths
+    uint32_t slots;        // kEvenly: chunks that there is room for
+    uint32_t *cuts;        // kEvenly: [batch][2]: a sequence's first chunk, and how many it has
     float scale;  // times log2 e
 };
 
@@ -183,9 +196,8 @@ struct Range {
     uint32_t chunk, chunks;     // positions of a chunk, chunks that hold any
 };
 
-__device__ __forceinline__ Range range_of(const AttnParams &p, uint32_t b) {
+__device__ __forceinline__ Range range_of(const AttnParams &p, int32_t len, int32_t start) {
     Range r;
-    const int32_t len = p.lens[b], start = p.starts ? p.starts[b] : 0;
     r.len = min(static_cast<uint32_t>(max(len, 0)), p.positions);
     r.start = min(static_cast<uint32_t>(max(start, 0)), r.len);
     r.base = r.start & ~(kStep - 1);
@@ -193,6 +205,135 @@ __device__ __forceinline__ Range range_of(const AttnParams &p, uint32_t b) {
     r.chunk = ((span + p.splits - 1) / p.splits + kMinChunk - 1) / kMinChunk * kMinChunk;
     r.chunks = span ? (span + r.chunk - 1) / r.chunk : 0;
     return r;
+}
+
+// The lengths of up to 64 kSets sequences in a wave's lanes.
+template <int kSets>
+struct Lanes {
+    int32_t len[kSets], start[kSets];
+    uint32_t span[kSets];
+    bool have[kSets];
+
+    __device__ __forceinline__ Lanes(const AttnParams &p, uint32_t lane) {
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+            const uint32_t i = 64 * g + lane, at = min(i, p.batch - 1);
+            len[g] = p.lens[at];
+            start[g] = p.starts ? p.starts[at] : 0;
+            have[g] = i < p.batch;
+        }
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+            const uint32_t l = min(static_cast<uint32_t>(max(len[g], 0)), p.positions);
+            const uint32_t s = min(static_cast<uint32_t>(max(start[g], 0)), l);
+            span[g] = have[g] && l > s ? l - (s & ~(kStep - 1)) : 0;
+        }
+    }
+};
+
+struct Sequence {
+    uint32_t b;
+    int32_t len, start;
+};
+
+// The sequence of this rank by length, longest first, found by every wave for
+// itself: a ballot for each bit of the lengths' classes keeps the half in which
+// the rank lies.  Sequences of a class go in their order.
+template <int kSets>
+__device__ __forceinline__ Sequence sequence_of(const AttnParams &p, uint32_t rank, uint32_t lane) {
+    const Lanes<kSets> lanes(p, lane);
+    uint64_t left[kSets];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) left[g] = __ballot(lanes.have[g]);
+#pragma unroll
+    for (int bit = kClassBits - 1; bit >= 0; --bit) {
+        uint64_t set[kSets];
+        uint32_t n = 0;
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+            const uint32_t key = min(lanes.span[g] >> p.class_shift, (1u << kClassBits) - 1);
+            set[g] = left[g] & __ballot(key >> bit & 1u);
+            n += __popcll(set[g]);
+        }
+        const bool in = rank < n;
+        rank -= in ? 0 : n;
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) left[g] = in ? set[g] : left[g] & ~set[g];
+    }
+    Sequence found = {0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+        const uint32_t n = __popcll(left[g]);
+        const uint32_t before = __builtin_amdgcn_mbcnt_hi(left[g] >> 32, __builtin_amdgcn_mbcnt_lo(left[g], 0));
+        const uint64_t mine = __ballot((left[g] >> lane & 1u) && before == rank);
+        if (mine) {  // of one set at most: past it the rank wraps below zero
+            const uint32_t at = __builtin_ctzll(mine);
+            found = {64 * g + at, __builtin_amdgcn_readlane(lanes.len[g], at), __builtin_amdgcn_readlane(lanes.start[g], at)};
+        }
+        rank -= n;
+    }
+    return found;
+}
+
+// Lane i receives op over lanes 0..i (op(0, x) = x): shifts inside rows of 16
+// lanes, then each row's last value to the rows above.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), kCtrl, kRows, 0xF, false));
+}
+
+template <class Op>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x, Op op) {
+    x = op(x, dpp<0x111, 0xF>(x));
+    x = op(x, dpp<0x112, 0xF>(x));
+    x = op(x, dpp<0x114, 0xF>(x));
+    x = op(x, dpp<0x118, 0xF>(x));
+    x = op(x, dpp<0x142, 0xA>(x));
+    return op(x, dpp<0x143, 0xC>(x));
+}
+
+struct Cut {
+    Sequence seq;
+    uint32_t chunk, chunks, units;  // units: of kMinChunk positions, in the sequence; chunks: 0 past the last sequence's
+};
+
+// The chunk in this slot where all sequences are cut to one length: as many
+// units as let p.slots - p.batch chunks hold them all, or p.splits for each
+// sequence where the longest is within an eighth of the mean.  A sequence's last
+// chunk need not be full, and an empty sequence has an empty one: hence p.batch
+// more.
+template <int kSets>
+__device__ __forceinline__ Cut cut_of(const AttnParams &p, uint32_t slot, uint32_t lane) {
+    const Lanes<kSets> lanes(p, lane);
+    uint32_t units[kSets], sum = 0, most = 0;
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+        units[g] = (lanes.span[g] + kMinChunk - 1) / kMinChunk;
+        sum += units[g];
+        most = max(most, units[g]);
+    }
+    const auto add = [](uint32_t a, uint32_t b) { return a + b; };
+    const auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+    sum = __builtin_amdgcn_readlane(wave_scan(sum, add), 63);
+    most = __builtin_amdgcn_readlane(wave_scan(most, larger), 63);
+    const uint32_t full = most * p.batch - sum <= sum / 8 ? p.batch * p.splits : p.slots - p.batch, each = max((sum + full - 1) / full, 1u);
+    Cut found = {};
+    uint32_t first = 0;
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+        const uint32_t n = lanes.have[g] ? max((units[g] + each - 1) / each, 1u) : 0;
+        const uint32_t end = first + wave_scan(n, add);
+        const uint64_t mine = __ballot(slot < end && slot >= end - n);
+        if (mine) {
+            const uint32_t at = __builtin_ctzll(mine);
+            found.seq = {64 * g + at, __builtin_amdgcn_readlane(lanes.len[g], at), __builtin_amdgcn_readlane(lanes.start[g], at)};
+            found.chunks = __builtin_amdgcn_readlane(n, at);
+            found.chunk = slot - (__builtin_amdgcn_readlane(end, at) - found.chunks);
+            found.units = __builtin_amdgcn_readlane(units[g], at);
+        }
+        first = __builtin_amdgcn_readlane(end, 63);
+    }
+    return found;
 }
 
 // Two BF16 values from two bytes of E4M3 (exact).
@@ -220,7 +361,7 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // left one wave, as two spill: 8 x 8,192 of 8 heads 94 us against 118.
 constexpr int waves_for(int dim, bool e4m3) { return dim == 64 ? 4 : dim == 128 ? (e4m3 ? 4 : 3) : e4m3 ? 2 : 1; }
 
-template <int kDim, bool kE4M3>
+template <int kDim, bool kE4M3, Order kOrder>
 __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim, kE4M3))))
 attend_kernel(AttnParams p) {
     constexpr int kPiece = kDim / 16;              // values of a V row in a lane; tiles of out^T
@@ -237,26 +378,57 @@ attend_kernel(AttnParams p) {
     // go round the 8 XCDs, and the first chunks, which every sequence has,
     // spread over all of them
     const uint32_t units = p.batch * p.kv_heads * p.tiles;
-    const uint32_t split = blockIdx.x / units;
+    const uint32_t split = kOrder == kAsGiven ? blockIdx.x / units : 0;
     uint32_t rest = blockIdx.x - split * units;
+    // workgroups i and i + 256 share a compute unit: every other 256 go from the
+    // shorter of their sequences to the longer
+    if (kOrder == kByLength && rest / kComputeUnits % 2 == 0) {
+        const uint32_t turn = rest / kComputeUnits * kComputeUnits;
+        rest = turn + min(turn + kComputeUnits, units) - 1 - rest;
+    }
     const uint32_t tile = rest % p.tiles;
     rest /= p.tiles;
-    const uint32_t h = rest % p.kv_heads, b = rest / p.kv_heads;
-    const Range range = range_of(p, b);
-    const uint32_t c0 = range.base + split * range.chunk;
+    const uint32_t h = rest % p.kv_heads;
+    rest /= p.kv_heads;
     const uint32_t heads = min(kHeadTile, p.group - tile * kHeadTile);
     const uint32_t head0 = h * p.group + tile * kHeadTile;
     const uint32_t out_heads = min(kHeadTile, p.group);  // as the host sizes s_out
-    const bool single = p.splits == 1;
-    if (split >= range.chunks && !single) {  // nothing here: the join gives it no weight
-        for (uint32_t g = threadIdx.x; g < heads; g += 64 * kWaves) {
-            float *to = p.stats + 2 * ((uint64_t{b} * p.q_heads + head0 + g) * p.splits + split);
-            to[0] = -INFINITY;
-            to[1] = 0;
+    const bool single = kOrder == kByLength || (kOrder == kAsGiven && p.splits == 1);
+    Sequence seq = {rest, 0, 0};
+    Cut cut = {};
+    if (kOrder == kAsGiven) {
+        seq.len = p.lens[rest];
+        seq.start = p.starts ? p.starts[rest] : 0;
+    } else if (kOrder == kByLength) {
+        seq = p.batch <= 64 ? sequence_of<1>(p, rest, lane) : sequence_of<kLaneSequences / 64>(p, rest, lane);
+    } else {
+        cut = p.batch <= 64 ? cut_of<1>(p, rest, lane) : cut_of<kLaneSequences / 64>(p, rest, lane);
+        if (cut.chunks == 0) return;
+        seq = cut.seq;
+        if (cut.chunk == 0 && h == 0 && tile == 0 && threadIdx.x == 0) {
+            p.cuts[2 * seq.b] = rest;
+            p.cuts[2 * seq.b + 1] = cut.chunks;
         }
-        return;
     }
-    const uint32_t c1 = split < range.chunks ? min(c0 + range.chunk, range.len) : c0;  // a single chunk may be empty
+    const uint32_t b = seq.b;
+    const Range range = range_of(p, seq.len, seq.start);
+    uint32_t c0, c1;
+    if (kOrder == kEvenly) {  // the sequence's units over its chunks, the first ones with one more
+        const uint32_t each = cut.units / cut.chunks, more = cut.units - each * cut.chunks;
+        c0 = range.base + (cut.chunk * each + min(cut.chunk, more)) * kMinChunk;
+        c1 = cut.units ? min(c0 + (each + (cut.chunk < more)) * kMinChunk, range.len) : c0;
+    } else {
+        c0 = range.base + split * range.chunk;
+        if (split >= range.chunks && !single) {  // nothing here: the join gives it no weight
+            for (uint32_t g = threadIdx.x; g < heads; g += 64 * kWaves) {
+                float *to = p.stats + 2 * ((uint64_t{b} * p.q_heads + head0 + g) * p.splits + split);
+                to[0] = -INFINITY;
+                to[1] = 0;
+            }
+            return;
+        }
+        c1 = split < range.chunks ? min(c0 + range.chunk, range.len) : c0;  // a single chunk may be empty
+    }
 
     // the chunk's pages; -1 masks
     const uint32_t first = c0 >> p.page_shift;
@@ -320,10 +492,19 @@ attend_kernel(AttnParams p) {
     uint32_t p0 = c0 + wave * kStep;
     if (p0 < c1) {
         load_k(p0);
+        // K's loads before V's, as in the loop: a wave waits for the oldest ones, and
+        // otherwise for V's at the head of every step.  The two empty statements, which
+        // differ, keep the compiler from joining both loads of V at that head.
+        __builtin_amdgcn_sched_barrier(0);
         load_v(p0);
+        asm volatile("; V of the first step" ::: "memory");
     }
     while (p0 < c1) {
-        // the registers of K and V are loaded again as soon as they are used up
+        // The registers of K and V are loaded again as soon as they are used up, past
+        // the last step with the chunk's last row: where some steps left a load out,
+        // the wait for V would have to be one for the next K too (one sequence of
+        // 65,536 positions in E4M3 31.0 us, so 27.8; 32 x 2,048 of 8 BF16 heads of 64
+        // 23.4, 22.0).
         const uint32_t next = p0 + kWaves * kStep;
         f4 s[2] = {};
 #pragma unroll
@@ -337,7 +518,7 @@ attend_kernel(AttnParams p) {
                     kw = kr[t][kE4M3 ? 0 : i];
                 s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[i], s[t], 0, 0, 0);
             }
-        if (next < c1) load_k(next);
+        load_k(next);
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -396,7 +577,8 @@ attend_kernel(AttnParams p) {
                 acc[j + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w_lo, o, 0, 0, 0);
             }
         }
-        if (next < c1) load_v(next);
+        load_v(next);
+        asm volatile("; V of the next step" ::: "memory");
         p0 = next;
     }
 
@@ -437,7 +619,7 @@ attend_kernel(AttnParams p) {
             p.out[row * kDim + d] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum == 0 ? 0.0f : o / sum));
             if (d == 0 && p.lse) p.lse[row] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
         } else {
-            const uint64_t at = row * p.splits + split;
+            const uint64_t at = kOrder == kEvenly ? uint64_t{head0 + g} * p.slots + rest : row * p.splits + split;
             p.part[at * kDim + d] = o;
             if (d == 0) {
                 p.stats[2 * at] = top;
@@ -473,28 +655,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p) {
     __shared__ f4 s_part[kGroups][kQuads];
     const uint64_t row = blockIdx.x;
     const uint32_t lane = threadIdx.x & 63u, d = threadIdx.x % kQuads, group = threadIdx.x / kQuads;
-    const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row * p.splits;
-    const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
+    uint64_t at = row * p.splits;
+    uint32_t splits = p.splits;
+    if (p.cuts) {
+        const uint32_t b = static_cast<uint32_t>(row / p.q_heads);
+        at = (row - uint64_t{b} * p.q_heads) * p.slots + p.cuts[2 * b];
+        splits = p.cuts[2 * b + 1];
+    }
+    const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + at;
+    const f4 *part = reinterpret_cast<const f4 *>(p.part + at * kDim) + d;
     constexpr int kAhead = 4;
     v2f first = {-INFINITY, 0};
-    if (lane < p.splits) first = stats[lane];
+    if (lane < splits) first = stats[lane];
     f4 v[kAhead] = {};
     float m[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
         const uint32_t i = group + a * kGroups;
         m[a] = -INFINITY;
-        if (i < p.splits) {
+        if (i < splits) {
             m[a] = stats[i].x;
             v[a] = part[uint64_t{i} * kQuads];
         }
     }
     float top = first.x;
-    for (uint32_t i = lane + 64; i < p.splits; i += 64) top = fmaxf(top, stats[i].x);
+    for (uint32_t i = lane + 64; i < splits; i += 64) top = fmaxf(top, stats[i].x);
     top = wave_max(top);
     const float ref = top == -INFINITY ? 0.0f : top;
     float sum = first.y * exp2_(first.x - ref);
-    for (uint32_t i = lane + 64; i < p.splits; i += 64) sum += stats[i].y * exp2_(stats[i].x - ref);
+    for (uint32_t i = lane + 64; i < splits; i += 64) sum += stats[i].y * exp2_(stats[i].x - ref);
     sum = wave_sum(sum);
     f4 o = {};
 #pragma unroll
@@ -503,7 +692,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] += m[a] == -INFINITY ? 0.0f : v[a][j] * f;
     }
-    for (uint32_t i = group + kAhead * kGroups; i < p.splits; i += kGroups) {
+    for (uint32_t i = group + kAhead * kGroups; i < splits; i += kGroups) {
         const float mi = stats[i].x, f = exp2_(mi - ref);
         const f4 w = part[uint64_t{i} * kQuads];
 #pragma unroll
@@ -614,11 +803,11 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
 // page table's width only bounds them: as many as give each of 256 compute
 // units a workgroup, no more than chunks of kMinChunk, and enough that none
 // exceeds kMaxChunk; none where the table holds at most 256 positions (a second
-// kernel takes longer than the second step of a wave).  Measured with 256, 512 and 1,024 workgroups wanted: 8 x
-// 32,768 BF16 positions of 8 heads (1.07 GB) 188, 188 and 190 us; one sequence of
-// 65,536 52.1, 53.2 and 55.9; 16 windows of 1,024 over 4 heads of 256 17.3, 20.2
-// and 22.7.
-constexpr uint64_t kWantGroups = 256;
+// kernel takes longer than the second step of a wave).  Measured with 256, 512 and
+// 1,024 workgroups wanted: 8 x 32,768 BF16 positions of 8 heads (1.07 GB) 188, 188
+// and 190 us; one sequence of 65,536 52.1, 53.2 and 55.9; 16 windows of 1,024 over
+// 4 heads of 256 17.3, 20.2 and 22.7.
+constexpr uint64_t kWantGroups = kComputeUnits;
 
 uint32_t splits_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions) {
     if (positions <= 2 * kMinChunk) return 1;
@@ -628,13 +817,54 @@ uint32_t splits_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t p
     return static_cast<uint32_t>(std::max(std::min(want, most), std::max<uint64_t>(least, 1)));
 }
 
-uint64_t attention_workspace(uint64_t rows, uint32_t head_dim, uint32_t splits) {
-    return splits <= 1 ? 0 : rows * splits * (head_dim + 2) * sizeof(float);
+// Chunks that there is room for where all sequences are cut to one length; 0: each
+// is cut by itself.  Cut by itself, a short sequence's chunks end early and leave
+// their compute units idle; cut evenly, a longer start (all lengths have to be
+// read and summed) and a longer join.  So only where the chunks would be long.
+// Measured by itself and evenly, BF16 sequences of 8 heads of 128: 8 ragged ones up
+// to 32,768 119 and 92 us, up to 8,192 34.5 and 28.8, 16 up to 4,096 34.5 and 29.6, 8
+// of the same 32,768 186 and 187, of the same 8,192 52.3 and 52.8; with chunks of
+// 1,024, 4 ragged ones up to 8,192, 16.5 and 17.2.  Ragged sequences get up to four
+// chunks for each compute unit, none under kMinEvenChunk (8 ragged up to 32,768: 104
+// us with one, 94 with four, 97 with eight); nearly equal ones as many as kAsGiven
+// (8 of the same 32,768 190 us with four).
+constexpr uint64_t kMinEven = 2048, kMinEvenChunk = 1024, kWantEven = 4 * kComputeUnits;
+
+uint64_t slots_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions, uint32_t splits) {
+    if (splits <= 1 || batch < 2 || batch > kLaneSequences || positions / splits < kMinEven || positions >= (1u << 30)) return 0;
+    const uint64_t units = batch * kv_heads * tiles;
+    return batch * (std::max<uint64_t>(splits, std::min((kWantEven + units - 1) / units, positions / kMinEvenChunk)) + 1);
+}
+
+// By length where compute units share whole sequences: 64 ragged ones of 8 BF16 heads
+// of 128 up to 1,024 positions 33.8 us as given, 28.4 by length, up to 2,048 59 and 51,
+// 48 up to 1,024 26.1 and 21.2; 64 of the same 512 23.6 and 24.0.  Ranking takes the
+// longer the more sequences there are and gains nothing where all are short: 64 ragged
+// ones up to 256 11.6 and 11.6, 256 up to 256 27.8 and 30.6, up to 1,024 107 and 99.
+Order order_of(uint64_t batch, uint64_t units, uint64_t positions, uint32_t splits, uint64_t slots) {
+    if (slots) return kEvenly;
+    return splits == 1 && units > kComputeUnits && batch <= kLaneSequences && positions >= std::max<uint64_t>(512, 4 * batch)
+               ? kByLength
+               : kAsGiven;
+}
+
+uint64_t attention_workspace(uint64_t batch, uint64_t q_heads, uint32_t head_dim, uint32_t splits, uint64_t slots) {
+    if (splits <= 1) return 0;
+    return (slots ? slots : batch * splits) * q_heads * (head_dim + 2) * sizeof(float) + (slots ? 2 * batch * sizeof(uint32_t) : 0);
 }
 
 bool attention_sizes_ok(uint64_t batch, uint64_t q_heads, uint32_t kv_heads, uint32_t page_size, uint64_t width) {
     return batch <= (1u << 24) && kv_heads > 0 && q_heads > 0 && q_heads <= (1u << 20) && q_heads % kv_heads == 0 &&
            width > 0 && width <= 0x7FFFFFFFu / page_size;
+}
+
+template <int kDim>
+auto attend_of(bool e4m3, Order order) {
+    switch (order) {
+        case kByLength: return e4m3 ? attend_kernel<kDim, true, kByLength> : attend_kernel<kDim, false, kByLength>;
+        case kEvenly: return e4m3 ? attend_kernel<kDim, true, kEvenly> : attend_kernel<kDim, false, kEvenly>;
+        default: return e4m3 ? attend_kernel<kDim, true, kAsGiven> : attend_kernel<kDim, false, kAsGiven>;
+    }
 }
 
 df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t batch, uint64_t q_heads, uint64_t q_batch,
@@ -674,21 +904,24 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     p.positions = static_cast<uint32_t>(width * c->page_size);
     p.scale = scale * kLog2e;
     p.splits = splits_of(batch, p.kv_heads, p.tiles, p.positions);
-    const uint64_t rows = batch * q_heads;
-    if (workspace_bytes < attention_workspace(rows, c->head_dim, p.splits)) return DF11_E_BUFFER_TOO_SMALL;
+    const uint64_t units = batch * p.kv_heads * p.tiles, rows = batch * q_heads;
+    p.slots = static_cast<uint32_t>(slots_of(batch, p.kv_heads, p.tiles, p.positions, p.splits));
+    const bool even = p.slots != 0;
+    p.class_shift = p.positions >> kClassBits ? log2_of(p.positions - 1) + 1 - kClassBits : 0;
+    if (workspace_bytes < attention_workspace(batch, q_heads, c->head_dim, p.splits, p.slots)) return DF11_E_BUFFER_TOO_SMALL;
     if (p.splits > 1 && !workspace) return DF11_E_INVALID_ARG;
     p.part = static_cast<float *>(workspace);
-    p.stats = p.part + (p.splits > 1 ? rows * p.splits * c->head_dim : 0);
-    const uint64_t groups = batch * p.kv_heads * p.tiles * p.splits;
+    const uint64_t chunks = even ? p.slots : p.splits > 1 ? batch * p.splits : 0;
+    p.stats = p.part + chunks * q_heads * c->head_dim;
+    p.cuts = even ? reinterpret_cast<uint32_t *>(p.stats + chunks * q_heads * 2) : nullptr;
+    const uint64_t groups = even ? chunks * p.kv_heads * p.tiles : units * p.splits;
     if (groups > 0x7FFFFFFFu || rows > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
     const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    auto fn = attend_kernel<128, false>;
-    switch (c->head_dim) {
-        case 64: fn = e4m3 ? attend_kernel<64, true> : attend_kernel<64, false>; break;
-        case 128: fn = e4m3 ? attend_kernel<128, true> : attend_kernel<128, false>; break;
-        default: fn = e4m3 ? attend_kernel<256, true> : attend_kernel<256, false>; break;
-    }
+    const Order order = order_of(batch, units, p.positions, p.splits, p.slots);
+    auto fn = c->head_dim == 64    ? attend_of<64>(e4m3, order)
+              : c->head_dim == 128 ? attend_of<128>(e4m3, order)
+                                   : attend_of<256>(e4m3, order);
     hipError_t err = launch(fn, static_cast<uint32_t>(groups), 64 * kWaves,
                             kWaves * std::min(kHeadTile, p.group) * (c->head_dim + kPad) * sizeof(float), st, p);
     if (err == hipSuccess && p.splits > 1)
@@ -715,7 +948,9 @@ extern "C" uint64_t df11_paged_attention_workspace_bytes(uint64_t batch, uint64_
     if (!page_ok(page_size) || !attention_sizes_ok(batch, q_heads, kv_heads, page_size, table_width)) return 0;
     const uint32_t group = static_cast<uint32_t>(q_heads / kv_heads);
     const uint32_t tiles = (group + kHeadTile - 1) / kHeadTile;
-    return attention_workspace(batch * q_heads, head_dim, splits_of(batch, kv_heads, tiles, table_width * page_size));
+    const uint64_t positions = table_width * page_size;
+    const uint32_t splits = splits_of(batch, kv_heads, tiles, positions);
+    return attention_workspace(batch, q_heads, head_dim, splits, slots_of(batch, kv_heads, tiles, positions, splits));
 }
 
 extern "C" df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch,

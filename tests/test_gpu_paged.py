@@ -352,3 +352,67 @@ def test_refusals(torch):
         hdb.df11_paged_append(q[:, :2], q[:, :2], torch.zeros(2, dtype=torch.int32, device="cuda"), kp, vp)
     assert hdb.df11_paged_attention(q[:0], kp, vp, table[:0], lens[:0])[0].shape == (0, 4, 128)
     hdb.df11_paged_append(q[:0, :2], q[:0, :2], torch.zeros(0, dtype=torch.int64, device="cuda"), kp, vp)
+
+
+def ragged(batch, most, seed):
+    """Lengths with the ends of chunks, steps and classes among them, and sequences of the same length."""
+    g = np.random.default_rng(seed)
+    lens = g.integers(0, most + 1, batch)
+    edges = [0, most, 1, most - 1, 127, 128, 129, 0, most // 2, most // 2, 33, 31]
+    lens[g.permutation(batch)[:min(batch, len(edges))]] = edges[:batch]
+    return lens.tolist()
+
+
+# more heads than compute units and one chunk: the longest sequences first
+BY_LENGTH = [(33, 8, 1, 64, 16, 520), (64, 5, 3, 128, 32, 1000), (65, 4, 1, 256, 16, 700), (130, 2, 17, 64, 64, 900),
+             (256, 2, 1, 64, 16, 1100), (257, 1, 1, 64, 16, 1100), (200, 2, 2, 128, 16, 600)]
+# chunks of one length for all sequences
+EVENLY = [(16, 8, 2, 64, 16, 4100), (2, 4, 3, 64, 16, 65530), (70, 2, 1, 64, 64, 4200), (9, 16, 17, 64, 32, 4095),
+          (17, 8, 1, 128, 128, 4090), (11, 4, 33, 256, 16, 4090), (5, 8, 1, 128, 128, 8300)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch,heads,group,dim,page,most", BY_LENGTH + EVENLY)
+def test_attention_ragged(torch, fp8, batch, heads, group, dim, page, most):
+    say(f"attention {batch} ragged of {most} {heads}x{group} dim {dim} page {page} fp8={fp8}")
+    q, kp, vp, table, lens, ks, vs = build(torch, ragged(batch, most, most), heads, group, dim, page, fp8)
+    check(torch, q, kp, vp, table, lens, None, ks, vs)
+
+
+@pytest.mark.parametrize("batch,heads,group,dim,page,most", BY_LENGTH[:1] + BY_LENGTH[3:4] + EVENLY[:2])
+def test_attention_ragged_starts_masks_and_lengths(torch, batch, heads, group, dim, page, most):
+    """Windows, masked pages, equal lengths, one sequence that holds all, none that holds any, one past the table."""
+    say(f"attention {batch} of {most} {heads}x{group} dim {dim} page {page}: starts, masks, lengths")
+    q, kp, vp, table, lens, ks, vs = build(torch, [most] * batch, heads, group, dim, page, False)
+    check(torch, q, kp, vp, table, lens, None, ks, vs)
+    starts = torch.tensor(ragged(batch, most, 3), dtype=torch.int32, device="cuda")
+    check(torch, q, kp, vp, table, lens, starts, ks, vs)
+    table = table.clone()
+    table[0] = -1
+    table[1, 3], table[1, 7] = -1, kp.shape[0]
+    one = torch.zeros_like(lens)
+    one[batch - 1] = most
+    for ln in (one, torch.zeros_like(lens), torch.full_like(lens, -9), torch.tensor(ragged(batch, most, 4), device="cuda").int()):
+        check(torch, q, kp, vp, table, ln, starts, ks, vs)
+        check(torch, q, kp, vp, table, ln, None, ks, vs)
+
+
+@pytest.mark.parametrize("batch,heads,group,dim,page,most", BY_LENGTH[:1] + EVENLY[:1])
+def test_attention_ragged_in_a_graph(torch, batch, heads, group, dim, page, most):
+    """A replay orders and cuts the sequences by the lengths that it finds."""
+    say(f"attention {batch} of {most} in a graph")
+    q, kp, vp, table, lens, ks, vs = build(torch, [most] * batch, heads, group, dim, page, False)
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    hdb.df11_paged_attention(q, kp, vp, table, lens, out=out, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hdb.df11_paged_attention(q, kp, vp, table, lens, out=out, lse=lse)
+    for step in range(4):
+        lens.copy_(torch.tensor(ragged(batch, most, step), dtype=torch.int32))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = check(torch, q, kp, vp, table, lens, None, ks, vs)
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
