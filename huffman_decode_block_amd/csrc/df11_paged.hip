@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "df11_internal.h"
 #include "df11_step.h"
@@ -129,15 +130,14 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 }
 
 // ---- Attention of one token ------------------------------------------------
-// A sequence's positions are cut into chunks of multiples of 128 positions, by the
+// A sequence's positions are cut into chunks of steps of 32 positions, by the
 // lengths as the device finds them; a workgroup takes one chunk of one cache head
-// for up to 16 of its query heads, its four waves the chunk's steps of 32
-// positions in turn.  Each wave keeps the running maximum, sum and weighted values
+// for up to 16 of its query heads, its four waves the chunk's steps in turn.  Each wave keeps the running maximum, sum and weighted values
 // of what it has seen, the waves join in LDS, and a second kernel joins the
 // chunks.  The host knows the page table's width and not the lengths, so it
 // chooses one of three ways to share the work (Order), and the device fits it to
 // the lengths:
-//   kAsGiven   every sequence is cut into up to `splits` chunks
+//   kAsGiven   every sequence is cut into up to `splits` chunks of 128 or more
 //   kByLength  one chunk each; compute units get long and short sequences in turn
 //   kEvenly    chunks of one length for all sequences, long ones have more of them
 //
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 // large as the output's own rounding, so they are given as two, high part and
 // remainder.  The matrix unit has time for it: the kernel is bound by reading
 // K and V, each once.  At 8 sequences of 32,768 positions, 8 cache heads of 128
-// and 64 query heads: BF16 1.07 GB in 187 us, 5.7 TB/s; E4M3 537 MB in 99 us, 5.4
+// and 64 query heads: BF16 1.07 GB in 185 us, 5.8 TB/s; E4M3 537 MB in 99 us, 5.4
 // TB/s.  Where there is less to read the start and the end count: one sequence
 // of 8,192 takes 9.7 us and its join 3.9 (33.5 MB would take 5.9 at the former
 // rate), 64 ragged ones up to 1,024 positions 28 us for 124 MB.
@@ -193,7 +193,7 @@ struct AttnParams {
 
 struct Range {
     uint32_t start, len, base;  // base: start down to a multiple of the step
-    uint32_t chunk, chunks;     // positions of a chunk, chunks that hold any
+    uint32_t steps;
 };
 
 __device__ __forceinline__ Range range_of(const AttnParams &p, int32_t len, int32_t start) {
@@ -201,9 +201,7 @@ __device__ __forceinline__ Range range_of(const AttnParams &p, int32_t len, int3
     r.len = min(static_cast<uint32_t>(max(len, 0)), p.positions);
     r.start = min(static_cast<uint32_t>(max(start, 0)), r.len);
     r.base = r.start & ~(kStep - 1);
-    const uint32_t span = r.len > r.start ? r.len - r.base : 0;
-    r.chunk = ((span + p.splits - 1) / p.splits + kMinChunk - 1) / kMinChunk * kMinChunk;
-    r.chunks = span ? (span + r.chunk - 1) / r.chunk : 0;
+    r.steps = r.len > r.start ? (r.len - r.base + kStep - 1) / kStep : 0;
     return r;
 }
 
@@ -294,7 +292,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x, Op op) {
 
 struct Cut {
     Sequence seq;
-    uint32_t chunk, chunks, units;  // units: of kMinChunk positions, in the sequence; chunks: 0 past the last sequence's
+    uint32_t chunk, chunks;  // chunks: 0 past the last sequence's
 };
 
 // The chunk in this slot where all sequences are cut to one length: as many
@@ -329,7 +327,6 @@ __device__ __forceinline__ Cut cut_of(const AttnParams &p, uint32_t slot, uint32
             found.seq = {64 * g + at, __builtin_amdgcn_readlane(lanes.len[g], at), __builtin_amdgcn_readlane(lanes.start[g], at)};
             found.chunks = __builtin_amdgcn_readlane(n, at);
             found.chunk = slot - (__builtin_amdgcn_readlane(end, at) - found.chunks);
-            found.units = __builtin_amdgcn_readlane(units[g], at);
         }
         first = __builtin_amdgcn_readlane(end, 63);
     }
@@ -412,23 +409,22 @@ attend_kernel(AttnParams p) {
     }
     const uint32_t b = seq.b;
     const Range range = range_of(p, seq.len, seq.start);
-    uint32_t c0, c1;
-    if (kOrder == kEvenly) {  // the sequence's units over its chunks, the first ones with one more
-        const uint32_t each = cut.units / cut.chunks, more = cut.units - each * cut.chunks;
-        c0 = range.base + (cut.chunk * each + min(cut.chunk, more)) * kMinChunk;
-        c1 = cut.units ? min(c0 + (each + (cut.chunk < more)) * kMinChunk, range.len) : c0;
-    } else {
-        c0 = range.base + split * range.chunk;
-        if (split >= range.chunks && !single) {  // nothing here: the join gives it no weight
-            for (uint32_t g = threadIdx.x; g < heads; g += 64 * kWaves) {
-                float *to = p.stats + 2 * ((uint64_t{b} * p.q_heads + head0 + g) * p.splits + split);
-                to[0] = -INFINITY;
-                to[1] = 0;
-            }
-            return;
+    if (kOrder == kAsGiven)
+        cut = {seq, split, min(p.splits, (range.steps + kMinChunk / kStep - 1) / (kMinChunk / kStep))};
+    else if (kOrder == kByLength)
+        cut = {seq, 0, 1};
+    if (kOrder == kAsGiven && !single && cut.chunk >= cut.chunks) {  // nothing here: the join gives it no weight
+        for (uint32_t g = threadIdx.x; g < heads; g += 64 * kWaves) {
+            float *to = p.stats + 2 * ((uint64_t{b} * p.q_heads + head0 + g) * p.splits + split);
+            to[0] = -INFINITY;
+            to[1] = 0;
         }
-        c1 = split < range.chunks ? min(c0 + range.chunk, range.len) : c0;  // a single chunk may be empty
+        return;
     }
+    // the sequence's steps over its chunks, the first ones with one more; a single chunk may be empty
+    const uint32_t chunks = max(cut.chunks, 1u), each = range.steps / chunks, more = range.steps - each * chunks;
+    const uint32_t c0 = range.base + (cut.chunk * each + min(cut.chunk, more)) * kStep;
+    const uint32_t c1 = max(c0, min(c0 + (each + (cut.chunk < more)) * kStep, range.len));
 
     // the chunk's pages; -1 masks
     const uint32_t first = c0 >> p.page_shift;
@@ -499,13 +495,13 @@ attend_kernel(AttnParams p) {
         load_v(p0);
         asm volatile("; V of the first step" ::: "memory");
     }
-    while (p0 < c1) {
-        // The registers of K and V are loaded again as soon as they are used up, past
-        // the last step with the chunk's last row: where some steps left a load out,
-        // the wait for V would have to be one for the next K too (one sequence of
-        // 65,536 positions in E4M3 31.0 us, so 27.8; 32 x 2,048 of 8 BF16 heads of 64
-        // 23.4, 22.0).
-        const uint32_t next = p0 + kWaves * kStep;
+    // The registers of K and V are loaded again as soon as they are used up.  The
+    // last step, which loads nothing, is a copy of its own: where the loads are left
+    // out on a condition, the wait for V has to be one for the next K too (one
+    // sequence of 65,536 positions in E4M3 30.9 us, so 26.7; 32 x 2,048 of 8 BF16
+    // heads of 64 23.4, so 21.4; where the last step loads in vain 27.4 and 21.9).
+    auto step = [&](uint32_t next, auto more) {
+        constexpr bool kMore = decltype(more)::value;
         f4 s[2] = {};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -518,7 +514,7 @@ attend_kernel(AttnParams p) {
                     kw = kr[t][kE4M3 ? 0 : i];
                 s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[i], s[t], 0, 0, 0);
             }
-        load_k(next);
+        if (kMore) load_k(next);
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -577,9 +573,14 @@ attend_kernel(AttnParams p) {
                 acc[j + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w_lo, o, 0, 0, 0);
             }
         }
-        load_v(next);
-        asm volatile("; V of the next step" ::: "memory");
-        p0 = next;
+        if (kMore) {
+            load_v(next);
+            asm volatile("; V of the next step" ::: "memory");
+        }
+    };
+    if (p0 < c1) {
+        for (uint32_t next = p0 + kWaves * kStep; next < c1; next += kWaves * kStep) step(next, std::true_type());
+        step(0, std::false_type());
     }
 
     // join the waves
@@ -822,12 +823,12 @@ uint32_t splits_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t p
 // their compute units idle; cut evenly, a longer start (all lengths have to be
 // read and summed) and a longer join.  So only where the chunks would be long.
 // Measured by itself and evenly, BF16 sequences of 8 heads of 128: 8 ragged ones up
-// to 32,768 119 and 92 us, up to 8,192 34.5 and 28.8, 16 up to 4,096 34.5 and 29.6, 8
-// of the same 32,768 186 and 187, of the same 8,192 52.3 and 52.8; with chunks of
-// 1,024, 4 ragged ones up to 8,192, 16.5 and 17.2.  Ragged sequences get up to four
-// chunks for each compute unit, none under kMinEvenChunk (8 ragged up to 32,768: 104
-// us with one, 94 with four, 97 with eight); nearly equal ones as many as kAsGiven
-// (8 of the same 32,768 190 us with four).
+// to 32,768 119 and 92 us, up to 8,192 34.4 and 28.3, 8 of the same 32,768 185.4 and
+// 185.5, of the same 8,192 52.2 and 52.5; with chunks of 1,024, 4 ragged ones up to
+// 8,192, 16.5 and 17.2.  Ragged sequences get up to four chunks for each compute
+// unit, none under kMinEvenChunk (8 ragged up to 32,768: 104 us with one, 94 with
+// four, 97 with eight); nearly equal ones as many as kAsGiven (8 of the same 32,768
+// 190 us with four).
 constexpr uint64_t kMinEven = 2048, kMinEvenChunk = 1024, kWantEven = 4 * kComputeUnits;
 
 uint64_t slots_of(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint64_t positions, uint32_t splits) {
