@@ -353,18 +353,19 @@ token_kernel(MulParams p) {
 }
 
 // Tile form, for many rows: a workgroup computes a tile of 16 kTiles rows of x
-// by 256 rows of w, each wave of a group of four 16 kTiles by 64 of it, in stages
-// of 128 along k; two groups take the stages in turn and add their sums.  x goes to LDS by loads that write there directly, two
-// stages, the next one loading while one is computed.  The codes go from
+// by 64 kCols rows of w, each wave of a group of four 16 kTiles by 16 kCols of it, in
+// stages of 128 along k; two groups take the stages in turn and add their sums.  x
+// goes to LDS by loads that write there directly, two stages, the next one loading
+// while one is computed.  The codes go from
 // memory to the registers of the waves that use them and are expanded there:
 // a lane's 16 bytes are one block of 32, k as in the token form.  A row of x
 // in LDS is 16 pieces of 16 bytes; piece c of row i lies at c ^ (i % 16), so
 // that the 16 rows a read touches use all banks once.  Row m of a wave's t-th
-// tile of w is row 16 (m / 4) + 4 t + m % 4 of its 64, which leaves a lane
-// with 16 neighbouring columns of y in the end.
+// tile of w is row 4 kCols (m / 4) + 4 t + m % 4 of its 16 kCols, which leaves a lane
+// with 4 kCols neighbouring columns of y in the end.
 // Scales come with kWide, for k in multiples of 512, for four stages at a time
 // and through LDS like x; else by a byte for each block (8192 x 8192 x 8192: 744
-// us against 805, 1024 x 4096 x 4096 39 against 46).
+// us against 805).
 // Bound by the matrix unit, held back by the loads of a stage: 8192 x 8192 x 8192
 // in 744 us, 1.48 PFLOP/s (a large BF16 product of the vendor's library reaches
 // 1.39 on the same card), 2048 x 14336 x 4096 in 186, 1.30; expanding the codes
@@ -378,10 +379,10 @@ constexpr uint32_t kRowBytes = kStageK * 2;
 constexpr uint32_t kTileWaves = 4;
 constexpr uint32_t kBand = 8;
 
-template <int kTiles, int kGroups, bool kWide>
+template <int kTiles, int kCols, int kGroups, bool kWide>
 __global__ void __launch_bounds__(64 * kTileWaves * kGroups) __attribute__((amdgpu_waves_per_eu(2)))
 tile_kernel(MulParams p) {
-    constexpr uint32_t kRowsM = 16 * kTiles, kRowsN = 64 * kTileWaves;
+    constexpr uint32_t kRowsM = 16 * kTiles, kWaveN = 16 * kCols, kRowsN = kWaveN * kTileWaves;
     constexpr int kLoads = kRowsM / 4 / kTileWaves;  // a wave's loads of a stage: 4 rows each, 16 rows from one another
     constexpr uint32_t kGroupBytes = 2 * kRowsM * kRowBytes;  // two stages; as many bytes as a group's sums
     __shared__ __attribute__((aligned(1024))) uint8_t s_all[kGroups * kGroupBytes];
@@ -414,7 +415,7 @@ tile_kernel(MulParams p) {
     const uint32_t rows_n = min(kRowsN, p.n - n0);
     const Rsrc wr = rsrc(p.codes + uint64_t{n0} * p.blocks * 16, rows_n * p.blocks * 16);
     const Rsrc sr = rsrc(p.scales + uint64_t{n0} * p.blocks, rows_n * p.blocks);
-    const uint32_t w_off = (64 * wave + 16 * (r / 4) + r % 4) * p.blocks + q;
+    const uint32_t w_off = (kWaveN * wave + 4 * kCols * (r / 4) + r % 4) * p.blocks + q;
 
     auto load_x = [&](uint32_t stage, uint8_t *to) {
         const uint32_t k0 = __builtin_amdgcn_readfirstlane(stage * kRowBytes);
@@ -424,32 +425,33 @@ tile_kernel(MulParams p) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (LdsPtr)(to + (i * kTileWaves + wave) * 1024), 16,
                                                      off + 4 * kTileWaves * i * row_bytes, k0, 0, 0);
     };
-    // scales of the wave's 64 rows: 16 bytes of a row, four stages', in one load
+    // scales of the wave's rows: 16 bytes of a row, four stages', in one load (of 64
+    // rows: with kCols of 2 the other half are not its own)
     // into the wave's part of LDS, two parts in turn
     uint8_t *scale_part = s_scale + (group * kTileWaves + wave) * 2048;
     auto load_scales = [&](uint32_t four) {
-        const uint32_t row = 64 * wave + lane;
+        const uint32_t row = kWaveN * wave + lane;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (LdsPtr)(scale_part + (four & 1) * 1024), 16, row * p.blocks,
                                                  __builtin_amdgcn_readfirstlane(four * 16), 0, 0);
     };
     struct W {
-        v4u code[4];
-        uint32_t scale[4];
+        v4u code[kCols];
+        uint32_t scale[kCols];
     };
     auto load_w = [&](uint32_t stage, W &w) {
         const uint32_t at = __builtin_amdgcn_readfirstlane(stage * kStageBlocks);
         const bool in = at + q < p.blocks;
         const uint32_t code_off = in ? w_off * 16 : kOff, scale_off = in ? w_off : kOff;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kCols; ++i) {
             w.code[i] = __builtin_amdgcn_raw_buffer_load_b128(wr, code_off + 4 * i * p.blocks * 16, at * 16, 0);
             if (!kWide) w.scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, scale_off + 4 * i * p.blocks, at, 0);
         }
     };
     auto read_scales = [&](uint32_t stage, W &w) {
-        const uint8_t *at = scale_part + (stage / 4 & 1) * 1024 + (16 * (r / 4) + r % 4) * 16 + stage % 4 * 4 + q;
+        const uint8_t *at = scale_part + (stage / 4 & 1) * 1024 + (4 * kCols * (r / 4) + r % 4) * 16 + stage % 4 * 4 + q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w.scale[i] = at[4 * i * 16];
+        for (int i = 0; i < kCols; ++i) w.scale[i] = at[4 * i * 16];
     };
 
     // Stage: 4 steps of 32 along k, in each 4 kTiles matrix instructions.  A
@@ -457,15 +459,15 @@ tile_kernel(MulParams p) {
     // the registers it goes to, and the next step's codes are expanded beside;
     // the order is given to the compiler in groups (left to itself it read just
     // before use: 2048 x 14336 x 4096 239 us against 212, in tiles of 256 rows).
-    f4 acc[kTiles][4] = {};
-    auto expand = [&](const W &w, int j, bf8 (&to)[4]) {
+    f4 acc[kTiles][kCols] = {};
+    auto expand = [&](const W &w, int j, bf8 (&to)[kCols]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kCols; ++i)
             to[i] = __builtin_bit_cast(bf8, expand8(w.code[i][j], __builtin_bit_cast(float, (w.scale[i] & 255u) << 23)));
     };
     auto compute = [&](const uint8_t *x, const W &w) {
         const uint8_t *row = x + r * kRowBytes;
-        bf8 xf[kTiles], wf[2][4];
+        bf8 xf[kTiles], wf[2][kCols];
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
             xf[m] = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + ((4 * q) ^ r) * 16);
@@ -478,16 +480,16 @@ tile_kernel(MulParams p) {
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kCols; ++i)
                     acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[j & 1][i], xf[m], acc[m][i], 0, 0, 0);
                 if (j < 3) xf[m] = *reinterpret_cast<const bf8 *>(row + m * 16 * kRowBytes + piece);
             }
             if (j < 3) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                 // matrix instructions
-                    __builtin_amdgcn_sched_group_barrier(0x002, 16 / kTiles, 0);      // expansion
-                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, kCols / 2, 0);         // matrix instructions
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4 * kCols / kTiles, 0);  // expansion
+                    __builtin_amdgcn_sched_group_barrier(0x008, kCols / 2, 0);
                     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 // LDS read
                 }
             }
@@ -519,40 +521,43 @@ tile_kernel(MulParams p) {
         w = next;
         flip = other;
     }
-    if (kGroups == 2) {  // the second group's sums through LDS to the first
-        static_assert(kRowsM * kRowsN * 4 <= 2 * kGroupBytes, "a group's sums fit");
+    if (kGroups > 1) {  // the other groups' sums through LDS to the first
+        static_assert((kGroups - 1) * kRowsM * kRowsN * 4 <= kGroups * kGroupBytes, "the groups' sums fit");
         f4 *sum = reinterpret_cast<f4 *>(s_all) + (wave * 64 + lane);
         __syncthreads();
-        if (group == 1) {
+        if (group > 0) {
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[(4 * m + i) * 64 * kTileWaves] = acc[m][i];
+                for (int i = 0; i < kCols; ++i) sum[(((group - 1) * kTiles + m) * kCols + i) * 64 * kTileWaves] = acc[m][i];
         }
         __syncthreads();
-        if (group == 1) return;
+        if (group > 0) return;
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
+        for (int g = 0; g < kGroups - 1; ++g)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][i] += sum[(4 * m + i) * 64 * kTileWaves];
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[m][i] += sum[((g * kTiles + m) * kCols + i) * 64 * kTileWaves];
     }
 
-    // a lane: columns 16 q .. 16 q + 15 of the wave's 64, row r of each tile
-    const uint32_t col = n0 + 64 * wave + 16 * q;
+    // a lane: 4 kCols columns of the wave's 16 kCols, row r of each tile
+    const uint32_t col = n0 + kWaveN * wave + 4 * kCols * q;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) {
         const uint32_t row = m0 + 16 * m + r;
         if (row >= p.m || col >= p.n) continue;
         uint16_t *to = p.y + uint64_t{row} * p.y_stride + col;
-        uint32_t o[8];
+        uint32_t o[2 * kCols];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
-        if (p.y_wide && col + 16 <= p.n) {
-            *reinterpret_cast<v4u *>(to) = v4u{o[0], o[1], o[2], o[3]};
-            *reinterpret_cast<v4u *>(to + 8) = v4u{o[4], o[5], o[6], o[7]};
+        for (int i = 0; i < 2 * kCols; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
+        if (p.y_wide && col + 4 * kCols <= p.n) {
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i)
+                *reinterpret_cast<v4u *>(to + 8 * i) = v4u{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i)
+            for (uint32_t i = 0; i < 4 * kCols; ++i)
                 if (col + i < p.n) to[i] = static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1)));
         }
     }
@@ -614,34 +619,41 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
 }
 
 // The form of a product.  A workgroup of the token form takes a piece of 4, 16,
-// 32 or 64 rows of x by 16, 32 or 64 of w, one of the tile form 64 or 128 rows of x
-// by 256 of w.
-//  - Up to 32 rows, and as long as 64 x 64 pieces make no more than two for
-//    each of 256 compute units, the token form, whose waves share k, is the
-//    faster one: 512 x 4096 x 4096 33.7 us against 35.7 for the best tiles, 256 x
-//    14336 x 4096 (896 pieces) 65.0 against 36.9.
+// 32 or 64 rows of x by 16, 32 or 64 of w, one of the tile form 64 rows of x by 128 or
+// 256 of w or 128 by 256.
+//  - Up to 32 rows, and as long as 64 x 64 pieces make no more than one for each of
+//    256 compute units, the token form, whose waves share k, is the faster one: 256 x
+//    4096 x 4096 (256 pieces) 17.9 us against 24.5 for the best tiles, 320 (320) 32.4
+//    against 24.9, 96 x 14336 x 4096 (448) 33.4 against 26.2.  Where k is at most 1,024
+//    a wave has little to do, and half as many pieces are the limit: 256 x 4096 x 512
+//    (256) 7.8 against 5.8, 128 x 4096 x 512 (128) 5.4 against 5.6.
 //  - In the token form the largest piece that leaves 160 workgroups (256 of
 //    16 rows): 64 x 4096 x 4096 8.2 us by 32 x 32 (256 workgroups), 10.8 by 64 x 32 (128)
 //    and 15.8 by 64 x 64 (64); 16 x 14336 x 4096 9.5 by 16 x 32 (448), 10.1 by 16 x 64 (224),
 //    11.7 by 16 x 16.
-//  - In the tile form 128 rows where those give 256 tiles, else 64: 2048 x 4096 x
+//  - Tiles of 64 x 128 up to three for each compute unit, four of which fit it at a
+//    time: 1536 x 4096 x 4096 (768 tiles) 49.3 us against 51.2 for 64 x 256, 384 x 14336 x
+//    4096 (672) 46.9 against 52.1, 512 x 14336 x 4096 (896) 63.3 against 54.8.
+//  - Larger ones of 128 rows where those give 256 tiles, else 64: 2048 x 4096 x
 //    4096 (256 tiles of 128) 56.8 us against 58.8, 1536 x 4096 x 4096 (192) 54.7
-//    against 52.4, 1024 x 4096 x 4096 (128) 51 against 39.
+//    against 52.4.
 //  - Up to 256 tiles, one for a compute unit, a tile has two groups of waves
-//    that take stages in turn: 1024 x 4096 x 4096 39.0 us against 42.2, 2048 x 4096 x
+//    that take stages in turn: 512 x 4096 x 4096 27.6 us against 32.3, 2048 x 4096 x
 //    14336 188 against 212; with more tiles other workgroups are there to fill
-//    the waits (1536 x 4096 x 4096, 384 tiles of 64: 68 against 52).
+//    the waits (768 x 4096 x 4096, 384 tiles of 64 x 128: 37.0 against 34.7).
 struct Form {
     bool token;
-    uint32_t x, rows;  // rows of x in a piece or tile; token form: tiles of 16 rows of w
+    uint32_t x, rows;  // of x and of w in a piece or tile; token form: tiles of 16 rows of w
 };
 
 uint64_t pieces(uint64_t m, uint64_t x, uint64_t n, uint64_t w) { return ((m + x - 1) / x) * ((n + w - 1) / w); }
 
-Form form_of(uint64_t m, uint64_t n) {
+Form form_of(uint64_t m, uint64_t n, uint64_t k) {
     if (m <= 4) return {true, 4, 1};
-    if (m > 32 && pieces(m, 64, n, 64) > 512)
-        return {false, pieces(m, 128, n, 256) >= 256 ? 128u : 64u, 0};
+    if (m > 32 && pieces(m, 64, n, 64) > (k <= 1024 ? 128 : 256)) {
+        if (pieces(m, 64, n, 128) <= 768) return {false, 64, 128};
+        return {false, pieces(m, 128, n, 256) >= 256 ? 128u : 64u, 256};
+    }
     if (m > 32)
         for (uint32_t rows : {4u, 2u})
             if (pieces(m, 64, n, 16 * rows) >= 160) return {true, 64, rows};
@@ -662,13 +674,19 @@ hipError_t launch_token(int reads, hipStream_t st, const MulParams &p) {
                   grid, 64 * kTokenWaves, st, p);
 }
 
+template <int kTiles, int kCols, int kGroups>
+hipError_t launch_tile(bool wide, dim3 grid, hipStream_t st, const MulParams &p) {
+    return launch(wide ? tile_kernel<kTiles, kCols, kGroups, true> : tile_kernel<kTiles, kCols, kGroups, false>, grid,
+                  64 * kTileWaves * kGroups, st, p);
+}
+
 // Rows of x are read 16 bytes and whole blocks at a time, with byte offsets of
 // 31 bits in a tile.  The token form has another way for those that cannot be
 // (kReadAny); for the tile form they are copied into the workspace first.
 constexpr uint64_t kMaxRead = uint64_t{1} << 21;  // stride of x for 256 rows in 2^30 bytes
 
 uint64_t copy_bytes(uint64_t m, uint64_t n, uint64_t k, bool x_readable) {
-    if ((x_readable && k % kBlock == 0) || m == 0 || n == 0 || form_of(m, n).token) return 0;
+    if ((x_readable && k % kBlock == 0) || m == 0 || n == 0 || form_of(m, n, k).token) return 0;
     return (m * ((k + kBlock - 1) / kBlock) * kBlock * 2 + 15) / 16 * 16;
 }
 
@@ -686,8 +704,8 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     const uint64_t copy = copy_bytes(m, n, k, readable);
     if (workspace_bytes < copy) return DF11_E_BUFFER_TOO_SMALL;
     if (copy && !workspace) return DF11_E_INVALID_ARG;
-    const Form f = form_of(m, n);
-    const uint64_t tiles = f.token ? 0 : pieces(m, f.x, n, 256);
+    const Form f = form_of(m, n, k);
+    const uint64_t tiles = f.token ? 0 : pieces(m, f.x, n, f.rows);
     if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     MulParams p = {};
@@ -730,15 +748,12 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         }
     }
     p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
-    p.tiles_n = static_cast<uint32_t>((n + 255) / 256);
+    p.tiles_n = static_cast<uint32_t>((n + f.rows - 1) / f.rows);
     const dim3 grid(static_cast<uint32_t>(tiles));
     const bool two = tiles <= 256;
-    const uint32_t threads = 64 * kTileWaves * (two ? 2 : 1);
-    return launched(launch(f.x == 128 ? wide ? (two ? tile_kernel<8, 2, true> : tile_kernel<8, 1, true>)
-                                             : (two ? tile_kernel<8, 2, false> : tile_kernel<8, 1, false>)
-                           : wide     ? (two ? tile_kernel<4, 2, true> : tile_kernel<4, 1, true>)
-                                      : (two ? tile_kernel<4, 2, false> : tile_kernel<4, 1, false>),
-                           grid, threads, st, p));
+    if (f.rows == 128) return launched(two ? launch_tile<4, 2, 2>(wide, grid, st, p) : launch_tile<4, 2, 1>(wide, grid, st, p));
+    if (f.x == 64) return launched(launch_tile<4, 4, 1>(wide, grid, st, p));  // always more than 256 tiles
+    return launched(two ? launch_tile<8, 4, 2>(wide, grid, st, p) : launch_tile<8, 4, 1>(wide, grid, st, p));
 }
 
 }  // namespace

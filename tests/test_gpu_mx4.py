@@ -209,6 +209,23 @@ def test_product_in_every_form(torch, m, n, k):
     assert torch.equal(y, hdb.df11_mx4_matmul(x, c, s)), "a second call differs"
 
 
+TILES = [
+    (100, 5200, 1100), (100, 8192, 2048), (100, 8100, 1999), (64, 10250, 2112), (40, 16390, 2048), (640, 2048, 512), (333, 2050, 333),
+    (900, 2100, 96), (1030, 4090, 512), (1100, 3000, 1056), (130, 16380, 45), (512, 14336, 512), (512, 14300, 96), (520, 14300, 96),
+    (520, 14336, 1024), (320, 4096, 4096), (45, 16300, 32),
+]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_product_in_every_tile(torch, m, n, k):
+    test_product_in_every_form(torch, m, n, k)
+
+
+@pytest.mark.parametrize("m,n,k,pad,offset", [(100, 6200, 333, 3, 1), (500, 4100, 96, 1, 0), (450, 14200, 70, 8, 2), (330, 4097, 512, 5, 8)])
+def test_tiles_of_strided_rows(torch, m, n, k, pad, offset):
+    test_product_of_strided_rows(torch, m, n, k, pad, offset)
+
+
 @pytest.mark.parametrize("m,n,k,pad,offset", [
     (1, 96, 128, 0, 1), (4, 96, 128, 8, 8), (19, 50, 256, 3, 2), (90, 200, 96, 5, 0), (150, 129, 100, 0, 4), (260, 140, 64, 8, 3),
     (1500, 1500, 70, 1, 0), (1600, 1411, 64, 0, 1), (70, 3000, 515, 0, 0),
