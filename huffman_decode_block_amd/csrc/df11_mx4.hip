@@ -733,7 +733,7 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     const bool wide = p.blocks % 16 == 0 && aligned16(scales);
     if (f.token) {
         // kReadWide gives a wave 512 of k at a time: below 2,048 that leaves more
-        // than half of the waves idle (512 x 4096 x 1024 18.7 us against 16.5; at
+        // than half of the waves idle (512 x 4096 x 1024 in pieces 18.7 us against 16.5; at
         // 2,048 16 x 14336 takes 6.1 against 7.5)
         const int reads = !readable || k % kBlock != 0 ? kReadAny : wide && p.blocks >= 64 ? kReadWide : kReadNarrow;
         switch (f.x + f.rows) {
