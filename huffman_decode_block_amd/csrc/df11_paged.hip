@@ -660,8 +660,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p) {
     uint32_t splits = p.splits;
     if (p.cuts) {
         const uint32_t b = static_cast<uint32_t>(row / p.q_heads);
-        at = (row - uint64_t{b} * p.q_heads) * p.slots + p.cuts[2 * b];
-        splits = p.cuts[2 * b + 1];
+        // within the workspace also where the lengths were written to during the call
+        const uint32_t first = min(p.cuts[2 * b], p.slots);
+        at = (row - uint64_t{b} * p.q_heads) * p.slots + first;
+        splits = min(p.cuts[2 * b + 1], p.slots - first);
     }
     const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + at;
     const f4 *part = reinterpret_cast<const f4 *>(p.part + at * kDim) + d;
