@@ -91,7 +91,8 @@ def _place(dev, stream):
         handle = int(stream)
         if here and handle == torch._C._cuda_getCurrentRawStream(dev):
             return handle, None
-        stream = torch.cuda.ExternalStream(handle, device=dev)
+        # the null stream has no ExternalStream: torch takes its handle, 0, for one that was not given
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 

@@ -416,3 +416,23 @@ def test_attention_ragged_in_a_graph(torch, batch, heads, group, dim, page, most
         torch.cuda.synchronize()
         eager = check(torch, q, kp, vp, table, lens, None, ks, vs)
         assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+
+
+def test_the_null_stream_by_its_handle(torch):
+    """stream=0 is the null stream also where another one is current: the call follows what was put there before it."""
+    say("null stream by its handle")
+    q, kp, vp, table, lens, ks, vs = build(torch, [3000, 10], 2, 4, 128, 16, False)
+    want = hdb.df11_paged_attention(q, kp, vp, table, lens)
+    late = torch.zeros_like(q)
+    a = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    assert torch.cuda.default_stream().cuda_stream == 0
+    for _ in range(20):  # some milliseconds in front of the query
+        a = (a @ a).clamp(max=1)
+    late.copy_(q)
+    with torch.cuda.stream(side):
+        assert hdb.step._place(0, 0)[0] == 0
+        got = hdb.df11_paged_attention(late, kp, vp, table, lens, stream=0)
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

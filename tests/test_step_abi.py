@@ -146,3 +146,46 @@ def test_workspace_sizes():
     # calls that the operators refuse need none
     assert hdb.df11_paged_attention_workspace_bytes(1, 33, 8, 128, 16, 4096) == 0
     assert hdb.df11_paged_attention_workspace_bytes(1, 32, 8, 128, 17, 4096) == 0
+
+
+class Streams:
+    """torch as far as a call's place goes: GPU 0 with a current stream, and ExternalStream, which takes a handle of 0 for
+    none and gives another stream."""
+
+    def __init__(self, current):
+        class Stream:
+            def __init__(self, handle, device):
+                self.cuda_stream, self.device_index = handle, device
+
+        class ExternalStream(Stream):
+            def __init__(self, handle, device=None):
+                super().__init__(handle or 0xABC0, device)
+
+        class cuda:
+            pass
+
+        cuda.Stream, cuda.ExternalStream = Stream, ExternalStream
+        cuda.default_stream = staticmethod(lambda dev: Stream(0, dev))
+        cuda.stream = staticmethod(lambda s: ("on", s.cuda_stream))
+        cuda.device = staticmethod(lambda d: ("device", d))
+
+        class _C:
+            _cuda_getDevice = staticmethod(lambda: 0)
+            _cuda_getCurrentRawStream = staticmethod(lambda dev: current)
+
+        self.cuda, self._C = cuda, _C
+
+
+@pytest.mark.parametrize("current", [0, 0x40])
+@pytest.mark.parametrize("given", [None, 0, 0x40, 0x80])
+@pytest.mark.parametrize("gpu", [0, 1])
+def test_place_of_a_raw_handle(monkeypatch, current, given, gpu):
+    """A call runs on the handle that it is given, the null stream's among them, and allocates there."""
+    monkeypatch.setattr(hdb.step, "_torch", Streams(current))
+    handle, ctx = hdb.step._place(gpu, given)
+    want = current if given is None else given
+    assert handle == want
+    if given is None:
+        assert ctx == (None if gpu == 0 else ("device", gpu))
+    else:
+        assert ctx == (None if gpu == 0 and given == current else ("on", want))
