@@ -155,7 +155,11 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 //
 // The weights exp(s - m) lie in [0, 1]; one BF16 number would add an error as
 // large as the output's own rounding, so they are given as two, high part and
-// remainder.  The matrix unit has time for it: the kernel is bound by reading
+// remainder.  A BF16 V may hold infinities, which a weight keeps only if neither
+// part is zero or negative: there the high part is cut off, not rounded, which
+// leaves a remainder that is not negative, and the remainder is at least
+// 2^-126 (both parts together are off by up to 2^-16 of the weight, by 2^-17
+// with a rounded high part, which E4M3's V, without infinities, gets).  The matrix unit has time for it: the kernel is bound by reading
 // K and V, each once.  At 8 sequences of 32,768 positions, 8 cache heads of 128
 // and 64 query heads: BF16 1.07 GB in 185 us, 5.8 TB/s; E4M3 537 MB in 99 us, 5.4
 // TB/s.  Where there is less to read the start and the end count: one sequence
@@ -350,6 +354,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Two floats cut off to BF16.
+__device__ __forceinline__ uint32_t cut2(float a, float b) {
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+}
+
+// Two BF16 values that are not negative (or NaN), each held to at least the one in `least`.
+__device__ __forceinline__ uint32_t at_least2(uint32_t v, uint32_t least) {
+    typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u2, v), __builtin_bit_cast(u2, least)));
+}
+
+constexpr uint32_t kLeastPart = 0x00800080u;  // twice 2^-126, the smallest normal number
+
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Waves of a SIMD that the registers are held to (without it the compiler takes
@@ -537,9 +554,10 @@ attend_kernel(AttnParams p) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hi[i] = pack2(w[2 * i], w[2 * i + 1]);
+            hi[i] = kE4M3 ? pack2(w[2 * i], w[2 * i + 1]) : cut2(w[2 * i], w[2 * i + 1]);
             lo[i] = pack2(w[2 * i] - __builtin_bit_cast(float, hi[i] << 16),
                           w[2 * i + 1] - __builtin_bit_cast(float, hi[i] & 0xFFFF0000u));
+            if (!kE4M3) lo[i] = at_least2(lo[i], kLeastPart);
         }
         const bf8 w_hi = __builtin_bit_cast(bf8, v4u{hi[0], hi[1], hi[2], hi[3]});
         const bf8 w_lo = __builtin_bit_cast(bf8, v4u{lo[0], lo[1], lo[2], lo[3]});

@@ -118,8 +118,11 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  *   out[b, g, :] = sum_j exp(s_j) v_j / sum_j exp(s_j)   (BF16, contiguous,
  *                  16-byte aligned)
  *   lse[b, g]    = log sum_j exp(s_j)                    (32 bits; NULL = not wanted)
- * and where no position is left, zeros and -infinity.  What masked positions
- * hold, NaN included, does not matter.  Scores, maxima, sums and the weighted
+ * and where that sum is zero (no position is left, or only scores of
+ * -infinity), zeros and -infinity.  What masked positions hold, NaN included,
+ * does not matter.  An infinity in v_j gives infinities of its sign (and with
+ * one of the other sign, NaN), if exp(s_j) is above 2^-126 of the largest: below, a
+ * weight is zero in 32 bits, and zero times infinity NaN.  Scores, maxima, sums and the weighted
  * values are held in 32 bits; the weights exp(s_j) enter the product as two
  * BF16 parts (16 bits of mantissa).  The result does not depend on what runs
  * beside it.  workspace: df11_paged_attention_workspace_bytes bytes of device

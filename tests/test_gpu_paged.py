@@ -436,3 +436,72 @@ def test_the_null_stream_by_its_handle(torch):
         got = hdb.df11_paged_attention(late, kp, vp, table, lens, stream=0)
     torch.cuda.default_stream().synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def score(q, kp, table, b, h, g, group, length):
+    """Scores of one query head over a sequence's first positions, in 64 bits."""
+    page, dim = kp.shape[2], kp.shape[3]
+    at = np.arange(length)
+    rows = kp[table[b, at // page], h, at % page]
+    return dim ** -0.5 * (rows @ q[b, h * group + g]), at
+
+
+@pytest.mark.parametrize("lens,heads,group,dim,page", [
+    ([100, 37, 1, 2], 2, 4, 64, 16), ([100, 37, 1, 2], 1, 17, 128, 8), ([250, 33, 5], 2, 3, 256, 64),
+    ([3000, 700, 1], 2, 4, 128, 16),  # cut into chunks
+    (ragged(33, 520, 1), 8, 1, 64, 16), (ragged(16, 4100, 2), 8, 2, 64, 16),  # by length; chunks of one length
+])
+def test_attention_infinite_values(torch, lens, heads, group, dim, page):
+    """Infinities in V make a sum infinite, of both signs NaN, whatever weight they have, the largest among them."""
+    say(f"attention infinite values, {len(lens)} sequences, {heads}x{group} dim {dim}")
+    q, kp, vp, table, ln, ks, vs = build(torch, lens, heads, group, dim, page, False)
+    clean, clean_lse = check(torch, q, kp, vp, table, ln, None, ks, vs)
+    want = clean.float().cpu().numpy().reshape(len(lens), heads, group, dim)
+    rng = np.random.default_rng(len(lens))
+    qn, kn, tn = q.double().cpu().numpy(), kp.double().cpu().numpy(), table.cpu().numpy()
+    inf = float("inf")
+    for b, length in enumerate(lens):
+        if length == 0:
+            continue
+        for h in range(heads):
+            top = int(np.argmax(score(qn, kn, tn, b, h, 0, group, length)[0]))
+            one, two = rng.integers(0, length, 2)
+            for col, at, sign in ((3, one, 1), (7, two, -1), (13, top, 1), (20, top, -1), (11, one, 1), (11, two, 1), (9, one, 1), (9, two, -1)):
+                if col == 9 and one == two:
+                    continue
+                vp[int(tn[b, at // page]), h, int(at) % page, col] = sign * inf
+            for col, value in ((3, inf), (7, -inf), (13, inf), (20, -inf), (11, inf), (9, np.nan)):
+                if col != 9 or one != two:
+                    want[b, h, :, col] = value
+    out, lse = hdb.df11_paged_attention(q, kp, vp, table, ln)
+    assert np.array_equal(out.float().cpu().numpy().reshape(want.shape), want, equal_nan=True)
+    assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("length", [60, 3000])
+def test_attention_infinite_keys(torch, length):
+    """A score of -infinity is a weight of zero; one of +infinity leaves no number."""
+    say(f"attention infinite keys, length {length}")
+    q, kp, vp, table, ln, ks, vs = build(torch, [length, 5], 2, 4, 64, 16, False)
+    at = length // 2
+    q[0, :, 5] = torch.tensor([1.0, -1.0] * 4, device="cuda")
+    kp[int(table[0, at // 16]), :, at % 16, 5] = float("inf")
+    kp[int(table[0, 0]), :, 3, 5] = float("inf")
+    out, lse = hdb.df11_paged_attention(q, kp, vp, table, ln)
+    assert bool(out[0, ::2].isnan().all())
+    qn, kn, vn, tn = q.double().cpu().numpy(), kp.double().cpu().numpy(), vp.double().cpu().numpy(), table.cpu().numpy()
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for head in range(1, 8, 2):
+        h, g = head // 4, head % 4
+        s, pos = score(qn, kn, tn, 0, h, g, 4, length)
+        v = vn[tn[0, pos // 16], h, pos % 16]
+        live = np.isfinite(s)
+        assert live.sum() == length - 2
+        k = kn[tn[0, pos // 16], h, pos % 16][live]
+        e = 68 * 2.0 ** -23 / 8 * (np.abs(k) @ np.abs(qn[0, head])).max() + 2.0 ** -22 * np.abs(s[live]).max()
+        w = np.exp(s[live] - s[live].max())
+        ref_lse, w = s[live].max() + math.log(w.sum()), w / w.sum()
+        ref = w @ v[live]
+        bound = 2.0 ** -8 * np.abs(ref) + (4 * e + 2.0 ** -14 + length * 2.0 ** -22) * (w @ np.abs(v[live]))
+        assert (np.abs(got[0, head] - ref) <= bound).all()
+        assert abs(got_lse[0, head] - ref_lse) <= 2 * e + 2.0 ** -17 + length * 2.0 ** -22 + 2.0 ** -22 * abs(ref_lse)
