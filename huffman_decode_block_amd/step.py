@@ -7,6 +7,11 @@ tensors, allocates what it returns and its workspace with torch, and launches
 HIP kernels of the library on `stream` (torch stream, raw handle, or None for
 the current stream).  With a stream other than the current one, what a call
 allocates belongs to that stream.
+
+No call has a derivative.  df11_mx4_matmul, df11_paged_append and
+df11_paged_attention refuse a tensor that asks for one (requires_grad where
+gradients are enabled, or a forward-mode tangent) rather than lose it; call them
+under torch.no_grad() or with detached tensors.
 """
 from __future__ import annotations
 
@@ -50,7 +55,8 @@ _SIGNATURES = {
 }
 
 
-_torch = None  # torch and the library, from the first call on
+_torch = None  # torch, its forward-mode derivatives and the library, from the first call on
+_forward_ad = None
 _L = None
 
 
@@ -62,11 +68,13 @@ def declare(L) -> None:
 
 
 def _load():
-    global _torch, _L
+    global _torch, _forward_ad, _L
     import torch
+    from torch.autograd import forward_ad
 
     from . import lib
     _L = lib()
+    _forward_ad = forward_ad
     _torch = torch
     return torch
 
@@ -110,6 +118,19 @@ def _tensor(t, name, dtype, ndim, dev):
     if at != dev and dev >= 0:
         raise ValueError(f"{name} is on GPU {at}, not {dev}")
     return at
+
+
+def _no_gradient(what, *tensors):
+    """Refuses tensors (or None) that ask for a derivative: what a call returns has no history."""
+    if _torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{what} has no backward and was given a tensor that requires a gradient: call it under "
+                                 "torch.no_grad() or with detached tensors")
+    if _forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{what} has no derivative and was given a tensor with a tangent")
 
 
 def _last_dense(t, name):
@@ -243,6 +264,7 @@ def df11_mx4_matmul(x, codes, scales, out=None, workspace=None, stream=None):
     if m <= 1:  # torch leaves the stride of a single row open
         xs = k or 1
     n, _ = _codes(codes, scales, k, dev)
+    _no_gradient("df11_mx4_matmul", x, out)
     handle, ctx = _place(dev, stream)
     if ctx is None:
         return _matmul(x, m, k, xs, codes, scales, n, out, workspace, dev, handle)
@@ -323,6 +345,7 @@ def df11_paged_append(k, v, slots, k_pages, v_pages, k_scale=None, v_scale=None,
     want = (t, c.kv_heads, c.head_dim)
     if k.shape != want or v.shape != want:
         raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    _no_gradient("df11_paged_append", k, v, k_pages, v_pages, k_scale, v_scale)
     handle, ctx = _place(dev, stream)
     k0, k1, _ = k.stride()
     v0, v1, _ = v.stride()
@@ -378,6 +401,7 @@ def df11_paged_attention(q, k_pages, v_pages, page_table, lens, starts=None, sca
         if starts.shape[0] != batch:
             raise ValueError(f"starts must hold {batch} sequences")
     scale = dim ** -0.5 if scale is None else float(scale)
+    _no_gradient("df11_paged_attention", q, k_pages, v_pages, k_scale, v_scale, out, lse)
     handle, ctx = _place(dev, stream)
     if ctx is None:
         return _attention(q, c, page_table, lens, starts, scale, out, lse, workspace, dev, handle)

@@ -322,3 +322,26 @@ def test_refusals(torch):
     with pytest.raises(hdb.DF11Error) as e:
         hdb.df11_mx4_matmul(wide, *hdb.df11_mx4_quantize(wide), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == hdb.DF11_E_BUFFER_TOO_SMALL
+
+
+def test_derivatives_are_refused(torch):
+    """The product loses no gradient and no tangent silently; codes are whole numbers and have none to lose."""
+    say("derivatives")
+    from torch.autograd import forward_ad
+    _, _, _, x, c, s = product_inputs(torch, 3, 40, 64)
+    want = hdb.df11_mx4_matmul(x, c, s)
+    wants = x.clone().requires_grad_()
+    with pytest.raises(ValueError, match="no backward"):
+        hdb.df11_mx4_matmul(wants, c, s)
+    with pytest.raises(ValueError, match="no backward"):
+        hdb.df11_mx4_matmul(wants * 2, c, s)
+    with pytest.raises(ValueError, match="no backward"):
+        hdb.df11_mx4_matmul(x, c, s, out=torch.empty_like(want).requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(hdb.df11_mx4_matmul(wants, c, s), want)
+    assert torch.equal(hdb.df11_mx4_matmul(wants.detach(), c, s), want)
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="no derivative"):
+            hdb.df11_mx4_matmul(forward_ad.make_dual(x, torch.ones_like(x)), c, s)
+    for got, ref in zip(hdb.df11_mx4_quantize(wants), hdb.df11_mx4_quantize(x)):
+        assert torch.equal(got, ref)

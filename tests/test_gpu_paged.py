@@ -505,3 +505,40 @@ def test_attention_infinite_keys(torch, length):
         bound = 2.0 ** -8 * np.abs(ref) + (4 * e + 2.0 ** -14 + length * 2.0 ** -22) * (w @ np.abs(v[live]))
         assert (np.abs(got[0, head] - ref) <= bound).all()
         assert abs(got_lse[0, head] - ref_lse) <= 2 * e + 2.0 ** -17 + length * 2.0 ** -22 + 2.0 ** -22 * abs(ref_lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_derivatives_are_refused(torch, fp8):
+    """No call loses a gradient or a tangent silently: not of q, k, v, pages, scales or outputs."""
+    say(f"derivatives fp8={fp8}")
+    from torch.autograd import forward_ad
+    q, kp, vp, table, lens, ks, vs = build(torch, [20, 3], 2, 2, 128, 16, fp8)
+    want = hdb.df11_paged_attention(q, kp, vp, table, lens, k_scale=ks, v_scale=vs)
+    k, slots = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16), table[:, -1].long() * 16  # past the lengths
+    a = dict(q=q, k_pages=kp, v_pages=vp, k_scale=ks, v_scale=vs, out=torch.empty_like(q), lse=torch.empty_like(want[1]))
+    w = dict(k=k, v=k, k_pages=kp, v_pages=vp, k_scale=ks, v_scale=vs)
+    held = kp.clone()
+
+    def attend(**more):
+        return hdb.df11_paged_attention(page_table=table, lens=lens, **{**a, **more})
+
+    def append(**more):
+        hdb.df11_paged_append(slots=slots, **{**w, **more})
+
+    for call, given in ((attend, a), (append, w)):
+        for name, t in given.items():
+            if t is None:
+                continue
+            wants = t.detach().clone().requires_grad_()
+            with pytest.raises(ValueError, match="no backward"):
+                call(**{name: wants})
+            if t.dtype is not torch.float8_e4m3fn:
+                with forward_ad.dual_level(), torch.no_grad():
+                    dual = forward_ad.make_dual(t.detach(), torch.ones_like(t))
+                    with pytest.raises(ValueError, match="no derivative"):
+                        call(**{name: dual})
+    assert torch.equal(kp.view(torch.uint8), held.view(torch.uint8)), "a refused call wrote"
+    with torch.no_grad():
+        got = attend(q=q.clone().requires_grad_())
+        append(k=k.clone().requires_grad_())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

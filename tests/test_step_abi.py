@@ -189,3 +189,27 @@ def test_place_of_a_raw_handle(monkeypatch, current, given, gpu):
         assert ctx == (None if gpu == 0 else ("device", gpu))
     else:
         assert ctx == (None if gpu == 0 and given == current else ("on", want))
+
+
+def test_a_derivative_is_refused():
+    """What asks for a gradient or carries a tangent is told apart from what does not, on the CPU's tensors."""
+    import torch
+    from torch.autograd import forward_ad
+
+    step = hdb.step
+    step._torch or step._load()
+    leaf, plain = torch.zeros(2, requires_grad=True), torch.zeros(2)
+    for t in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="an_entry has no backward"):
+            step._no_gradient("an_entry", None, plain, t)
+        step._no_gradient("an_entry", plain, t.detach())
+        with torch.no_grad():
+            step._no_gradient("an_entry", plain, t)
+    with torch.inference_mode():
+        step._no_gradient("an_entry", leaf)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(plain, torch.ones(2))
+        step._no_gradient("an_entry", plain, None)
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad), pytest.raises(ValueError, match="an_entry has no derivative"):
+                step._no_gradient("an_entry", None, dual)
