@@ -79,9 +79,9 @@ __device__ __forceinline__ float to_e4m3_range(uint32_t bits, const Scale &s) {
         v = x / s.s;
     } else {
         const float q = x * s.r;
-        v = fabsf(q) < 1024.0f ? fmaf(fmaf(-q, s.s, x), s.r, q) : q;
+        // the correction turns -0 into 0
+        v = copysignf(fabsf(q) < 1024.0f ? fmaf(fmaf(-q, s.s, x), s.r, q) : q, q);
     }
-    v = copysignf(v, x * s.r);  // the correction turns -0 into 0
     return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
 }
 

@@ -542,3 +542,33 @@ def test_derivatives_are_refused(torch, fp8):
         got = attend(q=q.clone().requires_grad_())
         append(k=k.clone().requires_grad_())
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def bits_of_e4m3(values):
+    """E4M3 bytes of values that E4M3 has (NaN as 0x7F), the sign of zero kept."""
+    a = np.abs(values)
+    e = np.maximum(np.frexp(np.where(np.isnan(a) | (a == 0), 2.0 ** -6, a))[1] - 1, -6)
+    m = np.ldexp(np.where(np.isnan(a), 0, a), 3 - e)
+    b = np.where(m >= 8, (e + 7) * 8 + m - 8, m)
+    return np.where(np.isnan(values), 0x7F, b + np.where(np.signbit(values), 0x80, 0)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.37, -0.5, 3e-5, 1e-30, 1e-36, 2.0 ** -140, 1e31, 1e38])
+def test_append_every_bf16_pattern_with_its_sign(torch, scale):
+    """The bytes that are stored, minus zero among them, for scales with a normal reciprocal, past it and negative."""
+    say(f"append every pattern to bytes, scale {scale}")
+    x = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16).view(512, 1, 128)
+    kp = torch.zeros(32, 1, 16, 128, device="cuda").to(torch.float8_e4m3fn)
+    vp = torch.zeros_like(kp)
+    s = torch.full((1,), scale, device="cuda")
+    hdb.df11_paged_append(x, x, torch.arange(512, device="cuda"), kp, vp, s, s)
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        v = (x.float().cpu().numpy().reshape(-1) / np.float32(scale)).astype(np.float64)  # the 32-bit quotient, on the host
+        a = np.minimum(np.abs(v), 448)
+        e = np.maximum(np.frexp(np.where(a > 0, a, 1.0))[1] - 1, -6)
+        want = bits_of_e4m3(np.copysign(np.ldexp(np.rint(np.ldexp(a, 3 - e)), e - 3), v))
+    for p in (kp, vp):
+        got = p.view(torch.uint8).cpu().numpy().reshape(-1)
+        nan = np.isnan(v)
+        assert np.array_equal(got[~nan], want[~nan])
+        assert (got[nan] & 0x7F == 0x7F).all()
