@@ -345,3 +345,109 @@ def test_derivatives_are_refused(torch):
             hdb.df11_mx4_matmul(forward_ad.make_dual(x, torch.ones_like(x)), c, s)
     for got, ref in zip(hdb.df11_mx4_quantize(wants), hdb.df11_mx4_quantize(x)):
         assert torch.equal(got, ref)
+
+
+# A product in each way that it is taken: the token form with scales in one load, by the byte, and with x through
+# registers; tiles of 64 x 128 with two groups of waves and with one, of an x that is copied first, of 64 x 256, and
+# of 128 x 256 with two groups and with one.
+EVERY_WAY = [
+    (1, 300, 4096), (4, 130, 320), (20, 200, 96), (64, 520, 2048), (33, 150, 333),
+    (640, 2048, 512), (1100, 5000, 96), (333, 2050, 333), (1600, 4096, 512), (2048, 4096, 1536), (2100, 5000, 160),
+]
+
+
+@pytest.mark.parametrize("m,n,k", EVERY_WAY)
+def test_product_of_quantised_nan_and_infinity(torch, m, n, k):
+    """A weight that is NaN or infinite makes its block NaN, and so its column of the product, for x of zeros too;
+    the other columns are those of the matrix without it."""
+    say(f"product {m}x{n}x{k} of quantised NaN and infinities")
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    x = torch.randn(m, k, generator=g, device="cuda").to(torch.bfloat16)
+    x[m // 2] = 0
+    w = torch.randn(n, k, generator=g, device="cuda").to(torch.bfloat16)
+    clean = hdb.df11_mx4_matmul(x, *hdb.df11_mx4_quantize(w))
+    at = [(0, 0), (5, k - 1), (n // 2, k // 2), (n - 1, k - 1), (17, 31)]
+    for i, (row, col) in enumerate(at):
+        w[row, col] = float("nan") if i % 2 else float("-inf")
+    codes, scales = hdb.df11_mx4_quantize(w)
+    for row, col in at:
+        assert int(scales[row, col // 32]) == 255 and bool((codes[row, col // 32 * 16:col // 32 * 16 + 16] == 0).all())
+    y = hdb.df11_mx4_matmul(x, codes, scales)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[row for row, _ in at]] = True
+    assert bool(y[:, bad].isnan().all())
+    assert torch.equal(y[:, ~bad], clean[:, ~bad])
+
+
+def sums_on_gpu(torch, xb, codes, scales, k):
+    """(64-bit products, bound) of bit patterns and codes, taken on the GPU."""
+    xd = torch.from_numpy(bf16_values(xb)).cuda()
+    wd = torch.from_numpy(values(codes, scales, k)).cuda().T.contiguous()
+    ref = xd @ wd
+    return ref, 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * k * 2.0 ** -23 * (xd.abs() @ wd.abs())
+
+
+@pytest.mark.parametrize("m,n,k", EVERY_WAY)
+def test_product_of_nan_and_infinity_in_x(torch, m, n, k):
+    """NaN and infinities in x, of one sign and of both, stay in their rows."""
+    say(f"product {m}x{n}x{k} with NaN and infinities in x")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k)
+    cols = (0, k // 2, k - 1)
+    for col in cols:  # of no row of w zero
+        codes[:, col // 2] |= 0x66
+    if k % 2:
+        codes[:, (k - 1) // 2] &= 0x0F
+    c.copy_(torch.from_numpy(codes))
+    rows = {0: ((0, 0x7FC0),), m // 3: ((k // 2, 0x7F80),), m // 2: ((k - 1, 0xFF80),), m - 1: ((0, 0x7F80), (k - 1, 0x7F80))}
+    for row, bits in rows.items():
+        for col, b in bits:
+            xb[row, col] = b
+    x.copy_(torch.from_numpy(xb.view(np.int16)).view(torch.bfloat16))
+    ref, bound = sums_on_gpu(torch, xb, codes, scales, k)
+    got = hdb.df11_mx4_matmul(x, c, s).double()
+    fine = ref.isfinite()
+    assert int((~fine).sum()) == n * len(rows) and bool(ref.isinf().any())
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got[ref.isinf()], ref[ref.isinf()])
+    assert bool(((got - ref).abs()[fine] <= bound[fine]).all())
+
+
+@pytest.mark.parametrize("m,n,k", EVERY_WAY)
+def test_product_of_denormals(torch, m, n, k):
+    """BF16 denormals count: in x (times large weights) and as what small weights expand to (times large x)."""
+    say(f"product {m}x{n}x{k} of denormals")
+    rng = np.random.default_rng([m, n, k])
+    xb, codes, _, _, c, _ = product_inputs(torch, m, n, k)
+    for tiny_x in (True, False):
+        bits = rng.integers(1, 128, (m, k)).astype(np.uint16) if tiny_x else (xb & 0x807F | (rng.integers(240, 250, (m, k)) << 7)).astype(np.uint16)
+        bits[rng.random((m, k)) < 0.5] ^= 0x8000
+        sc = rng.integers(230, 240, (n, -(-k // 32))) if tiny_x else rng.integers(0, 3, (n, -(-k // 32)))
+        sc = sc.astype(np.uint8)
+        ref, bound = sums_on_gpu(torch, bits, codes, sc, k)
+        assert float(ref.abs().max()) > 2.0 ** -40
+        got = hdb.df11_mx4_matmul(on_gpu(torch, bits), c, torch.from_numpy(sc).cuda()).double()
+        assert bool(((got - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(640, 2048, 512), (333, 2050, 333), (1600, 4096, 96), (2048, 4096, 512)])
+def test_tiles_on_another_stream_and_in_a_graph(torch, m, n, k):
+    """Also where x is copied in front of the product (333 columns): two launches, with a workspace between them."""
+    say(f"tiles {m}x{n}x{k} on a side stream and in a graph")
+    xb, codes, scales, x, c, s = product_inputs(torch, m, n, k)
+    want = hdb.df11_mx4_matmul(x, c, s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = hdb.df11_mx4_matmul(x, c, s, stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want)
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hdb.df11_mx4_matmul(x, c, s, out=out)
+    for _ in range(4):
+        x.mul_(-0.5)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, hdb.df11_mx4_matmul(x, c, s))

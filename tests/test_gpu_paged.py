@@ -572,3 +572,24 @@ def test_append_every_bf16_pattern_with_its_sign(torch, scale):
         nan = np.isnan(v)
         assert np.array_equal(got[~nan], want[~nan])
         assert (got[nan] & 0x7F == 0x7F).all()
+
+
+def test_append_keeps_bf16_bits(torch):
+    say("append every pattern to BF16 pages")
+    x = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16).view(512, 1, 128)
+    kp = torch.zeros(32, 1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    hdb.df11_paged_append(x, x, torch.arange(512, device="cuda"), kp, vp)
+    for p in (kp, vp):
+        assert torch.equal(p.view(torch.int16).view(-1), x.view(torch.int16).view(-1))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_chunks_of_one_length_over_few_sequences(torch, fp8):
+    """Five sequences of up to 16,500 positions: about 2,400 to a chunk, all sequences cut to one length."""
+    say(f"attention 5 ragged of 16500 fp8={fp8}")
+    q, kp, vp, table, lens, ks, vs = build(torch, ragged(5, 16500, 1), 8, 1, 128, 128, fp8)
+    # more room than chunks of each sequence by itself would take: heads x (128 values, maximum and sum)
+    splits = -(-256 // (5 * 8))
+    assert hdb.df11_paged_attention_workspace_bytes(5, 8, 8, 128, 128, table.shape[1]) > 5 * splits * 8 * 130 * 4
+    check(torch, q, kp, vp, table, lens, None, ks, vs)
