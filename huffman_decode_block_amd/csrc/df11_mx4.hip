@@ -26,6 +26,7 @@ constexpr uint64_t kMaxK = uint64_t{1} << 21;       // of a product: 256 rows of
 constexpr uint64_t kMaxRows = 0x7FFFFFFFu;
 constexpr uint64_t kMaxStride = uint64_t{1} << 32;
 constexpr uint64_t kMaxValues = uint64_t{1} << 40;  // values of one matrix
+constexpr uint64_t kMaxExtent = uint64_t{1} << 48;  // rows times stride
 constexpr uint32_t kBlock = 32;                     // values that share a scale
 constexpr uint32_t kNanScale = 255;
 
@@ -586,7 +587,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool matrix_ok(uint64_t rows, uint64_t cols, uint64_t stride) {
     return cols > 0 && cols <= kMaxCols && rows <= kMaxValues / cols && stride >= cols &&
-           (rows == 0 || stride <= (uint64_t{1} << 48) / rows);
+           (rows == 0 || stride <= kMaxExtent / rows);
 }
 
 uint32_t quant_grid(uint64_t items) {
@@ -694,7 +695,7 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
                    const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                    uint64_t workspace_bytes, void *hip_stream) {
     if (m > kMaxRows || n > kMaxRows || k > kMaxK || x_stride > kMaxStride || x_stride < k || y_stride < n ||
-        y_stride > kMaxStride)
+        y_stride > kMaxStride || m * std::max(x_stride, y_stride) > kMaxExtent)
         return DF11_E_INVALID_ARG;
     if (m == 0 || n == 0) return DF11_OK;
     if (!y || (k && (!x || !codes || !scales)) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(x) & 1u) ||

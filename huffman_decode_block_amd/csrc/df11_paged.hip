@@ -763,7 +763,11 @@ bool dim_ok(uint32_t d) { return d == 64 || d == 128 || d == 256; }
 
 bool page_ok(uint32_t n) { return n >= kMinPage && n <= kMaxPage && (n & (n - 1)) == 0; }
 
-constexpr uint64_t kMaxStride = uint64_t{1} << 40;  // elements; with the limits on counts no address overflows
+constexpr uint64_t kMaxStride = uint64_t{1} << 40, kMaxExtent = uint64_t{1} << 48;  // elements
+
+// What `n` steps of `stride` span, held to kMaxExtent; a few of these together
+// are in bounds below that and cannot overflow.
+uint64_t span(uint64_t n, uint64_t stride) { return n && stride > kMaxExtent / n ? kMaxExtent : n * stride; }
 
 df11_status check_cache(const df11_paged_cache *c) {
     if (!c) return DF11_E_INVALID_ARG;
@@ -774,6 +778,12 @@ df11_status check_cache(const df11_paged_cache *c) {
     const uint64_t unit = e4m3 ? 16 : 8;  // elements in 16 bytes
     for (uint64_t s : {c->k_page_stride, c->k_head_stride, c->k_row_stride, c->v_page_stride, c->v_head_stride, c->v_row_stride})
         if (s % unit != 0 || s > kMaxStride) return DF11_E_INVALID_ARG;
+    const auto extent = [&](uint64_t page, uint64_t head, uint64_t row) {
+        return span(c->n_pages, page) + span(c->kv_heads, head) + span(c->page_size, row);
+    };
+    if (extent(c->k_page_stride, c->k_head_stride, c->k_row_stride) >= kMaxExtent ||
+        extent(c->v_page_stride, c->v_head_stride, c->v_row_stride) >= kMaxExtent)
+        return DF11_E_INVALID_ARG;
     if (e4m3 && (!c->k_scale || !c->v_scale)) return DF11_E_INVALID_ARG;
     return DF11_OK;
 }
@@ -800,6 +810,9 @@ df11_status append(const df11_paged_cache *c, const uint16_t *k, uint64_t k_toke
         return DF11_E_INVALID_ARG;
     for (uint64_t s : {k_token, k_head, v_token, v_head})
         if (s > kMaxStride) return DF11_E_INVALID_ARG;
+    if (span(tokens, k_token) + span(c->kv_heads, k_head) >= kMaxExtent ||
+        span(tokens, v_token) + span(c->kv_heads, v_head) >= kMaxExtent)
+        return DF11_E_INVALID_ARG;
     AppendParams p;
     p.k = k_of(c);
     p.v = v_of(c);
@@ -895,7 +908,8 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     const df11_status rc = check_cache(c);
     if (rc != DF11_OK) return rc;
     if (!attention_sizes_ok(batch, q_heads, c->kv_heads, c->page_size, width) || table_stride < width ||
-        table_stride > kMaxStride || q_batch > kMaxStride || q_head > kMaxStride)
+        table_stride > kMaxStride || q_batch > kMaxStride || q_head > kMaxStride ||
+        span(batch, table_stride) >= kMaxExtent || span(batch, q_batch) + span(q_heads, q_head) >= kMaxExtent)
         return DF11_E_INVALID_ARG;
     if (batch == 0) return DF11_OK;
     if (!q || !table || !lens || !out || (reinterpret_cast<uintptr_t>(q) & 1u) || !aligned16(out) ||

@@ -63,8 +63,9 @@ df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, uin
  * m = 0 or n = 0 is a no-op; k = 0 gives zeros.  The result does not depend
  * on what runs beside it: every sum has a fixed order.  y must not overlap
  * the inputs.  Errors: DF11_E_INVALID_ARG (null or misaligned pointers,
- * strides below k or n or over 2^32, m or n over 2^31 - 1, k over 2^21),
- * DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
+ * strides below k or n or over 2^32, m times a stride over 2^48, m or n over
+ * 2^31 - 1, k over 2^21), DF11_E_BUFFER_TOO_SMALL (workspace_bytes),
+ * DF11_E_HIP. */
 df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
                             const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                             uint64_t workspace_bytes, void *hip_stream);
@@ -81,7 +82,9 @@ uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int
  * strides: the row of position r of head h in page p starts at
  * pages + p * page_stride + h * head_stride + r * row_stride.  Rows start at
  * multiples of 16 bytes.  head_dim 64, 128 or 256; page_size a power of two
- * from 8 to 1024. */
+ * from 8 to 1024; kv_heads up to 65536; n_pages below 2^31; strides up to
+ * 2^40, and n_pages, kv_heads and page_size times their strides below 2^48
+ * together. */
 #define DF11_CACHE_BF16 0u
 #define DF11_CACHE_E4M3 1u
 
@@ -101,7 +104,9 @@ typedef struct df11_paged_cache {
  * the page; a slot below 0 or past the cache is skipped (padding).  E4M3: the
  * stored value is x / scale[h] rounded to nearest even, magnitudes over 448
  * (infinities too) become 448, NaN stays NaN.  Two tokens with one slot leave
- * either's values.  tokens = 0 is a no-op.  Errors: DF11_E_INVALID_ARG,
+ * either's values.  tokens = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null
+ * or misaligned pointers, sizes past the limits above, 2^31 tokens or more,
+ * strides over 2^40 or, times what they step over, 2^48 together),
  * DF11_E_UNSUPPORTED (head_dim, page_size or dtype), DF11_E_HIP. */
 df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, uint64_t k_token_stride,
                               uint64_t k_head_stride, const uint16_t *v, uint64_t v_token_stride,
@@ -128,7 +133,10 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  * beside it.  workspace: df11_paged_attention_workspace_bytes bytes of device
  * memory, 16-byte aligned (NULL when that is 0), not kept between calls;
  * calls that run at the same time need one each.  batch = 0 is a no-op.
- * Errors: DF11_E_INVALID_ARG, DF11_E_UNSUPPORTED (as above),
+ * page_table, lens and starts must not be written to while the call runs.
+ * Errors: DF11_E_INVALID_ARG (null or misaligned pointers; table_width 0, or
+ * 2^31 positions or more in it; table_stride below table_width; strides as for
+ * the append; more than 2^20 query heads), DF11_E_UNSUPPORTED (as above),
  * DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
 df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch, uint64_t q_heads,
                                  uint64_t q_batch_stride, uint64_t q_head_stride, const int32_t *page_table,

@@ -213,3 +213,57 @@ def test_a_derivative_is_refused():
         for grad in (True, False):
             with torch.set_grad_enabled(grad), pytest.raises(ValueError, match="an_entry has no derivative"):
                 step._no_gradient("an_entry", None, dual)
+
+
+@pytest.mark.parametrize("change", [
+    # rows of x or y past 2^48 values
+    dict(m=1 << 20, xs=1 << 32), dict(m=1 << 20, n=64, ys=1 << 32),
+])
+def test_products_past_a_launch_or_the_addresses(change):
+    a = dict(x=P, m=3, k=64, xs=64, codes=P, scales=P, n=40, y=P, ws=P, size=1 << 62)
+    a.update(change)
+    ys = a.get("ys", a["n"])
+    L = hdb.lib()
+    assert L.df11_mx4_matmul(a["x"], a["m"], a["k"], a["xs"], a["codes"], a["scales"], a["n"], a["y"], ys, a["ws"], a["size"],
+                             None) == hdb.DF11_E_INVALID_ARG
+    if "xs" not in change and "ys" not in change:
+        assert hdb.df11_mx4_matmul_workspace_bytes(a["m"], a["n"], 63, False) == 0
+
+
+@pytest.mark.parametrize("change", [
+    dict(n_pages=1 << 30, k_page_stride=1 << 18), dict(n_pages=(1 << 31) - 1, v_page_stride=1 << 40),
+    dict(kv_heads=1 << 16, k_head_stride=1 << 32), dict(page_size=1024, v_row_stride=1 << 38),
+    dict(n_pages=1 << 29, k_page_stride=1 << 18, kv_heads=1 << 15, k_head_stride=1 << 32),  # half of it each
+])
+def test_caches_past_the_addresses(change):
+    L = hdb.lib()
+    c = cache(**change)
+    heads = c.kv_heads
+    assert L.df11_paged_append(ctypes.byref(c), P, 1024, 128, P, 1024, 128, P, 1, None) == hdb.DF11_E_INVALID_ARG
+    assert L.df11_paged_attention(ctypes.byref(c), P, 1, heads, 1024, 128, P, 4, 4, P, None, 1.0, P, P, P, 1 << 62, None) == \
+        hdb.DF11_E_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [dict(tokens=1 << 30, ks=1 << 18), dict(tokens=1 << 30, vs=1 << 40), dict(kh=1 << 40, kv_heads=256),
+                                    dict(vh=1 << 40, kv_heads=256)])
+def test_appends_past_the_addresses(change):
+    a = dict(tokens=1, ks=1024, kh=128, vs=1024, vh=128, kv_heads=8)
+    a.update(change)
+    c = cache(kv_heads=a["kv_heads"])
+    assert hdb.lib().df11_paged_append(ctypes.byref(c), P, a["ks"], a["kh"], P, a["vs"], a["vh"], P, a["tokens"], None) == \
+        hdb.DF11_E_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    # addresses
+    dict(batch=1 << 15, qb=1 << 33), dict(heads=1 << 20, qh=1 << 40), dict(batch=1 << 15, ts=1 << 33),
+])
+def test_attention_past_a_launch_or_the_addresses(change):
+    a = dict(batch=2, heads=8, kv_heads=8, qb=4096, qh=128, width=4)
+    a.update(change)
+    c = cache(kv_heads=a["kv_heads"])
+    got = hdb.lib().df11_paged_attention(ctypes.byref(c), P, a["batch"], a["heads"], a["qb"], a["qh"], P, a.get("ts", a["width"]),
+                                         a["width"], P, None, 1.0, P, None, P, 1 << 62, None)
+    assert got == hdb.DF11_E_INVALID_ARG
+    if not {"qb", "qh", "ts"} & set(change):
+        assert hdb.df11_paged_attention_workspace_bytes(a["batch"], a["heads"], a["kv_heads"], 128, 16, a["width"]) == 0
