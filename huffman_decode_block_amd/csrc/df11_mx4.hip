@@ -666,6 +666,13 @@ Form form_of(uint64_t m, uint64_t n, uint64_t k) {
     return {true, 16, 1};
 }
 
+// Whether a product's work items fit a launch, which holds fewer than 2^32 in a
+// dimension; the token form's other dimension has at most 1,024 workgroups.
+bool launchable(const Form &f, uint64_t m, uint64_t n) {
+    const uint64_t groups = f.token ? pieces(1, 1, n, 16 * f.rows) : pieces(m, f.x, n, f.rows);
+    return groups * 64 * (f.token ? kTokenWaves : kTileWaves) < uint64_t{1} << 32;
+}
+
 template <int kX, int kRows, int kAhead>
 hipError_t launch_token(int reads, hipStream_t st, const MulParams &p) {
     const dim3 grid((p.n + 16 * kRows - 1) / (16 * kRows), (p.m + kX - 1) / kX);
@@ -702,12 +709,13 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
         (reinterpret_cast<uintptr_t>(y) & 1u) || !aligned16(workspace))
         return DF11_E_INVALID_ARG;
     const bool readable = aligned16(x) && x_stride % 8 == 0 && x_stride <= kMaxRead;
+    const Form f = form_of(m, n, k);
+    if (!launchable(f, m, n)) return DF11_E_INVALID_ARG;
     const uint64_t copy = copy_bytes(m, n, k, readable);
     if (workspace_bytes < copy) return DF11_E_BUFFER_TOO_SMALL;
     if (copy && !workspace) return DF11_E_INVALID_ARG;
-    const Form f = form_of(m, n, k);
     const uint64_t tiles = f.token ? 0 : pieces(m, f.x, n, f.rows);
-    if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
+    const bool two = tiles <= 256;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     MulParams p = {};
     p.x = x;
@@ -751,7 +759,6 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
     p.tiles_n = static_cast<uint32_t>((n + f.rows - 1) / f.rows);
     const dim3 grid(static_cast<uint32_t>(tiles));
-    const bool two = tiles <= 256;
     if (f.rows == 128) return launched(two ? launch_tile<4, 2, 2>(wide, grid, st, p) : launch_tile<4, 2, 1>(wide, grid, st, p));
     if (f.x == 64) return launched(launch_tile<4, 4, 1>(wide, grid, st, p));  // always more than 256 tiles
     return launched(two ? launch_tile<8, 4, 2>(wide, grid, st, p) : launch_tile<8, 4, 1>(wide, grid, st, p));
@@ -770,7 +777,7 @@ extern "C" df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *
 }
 
 extern "C" uint64_t df11_mx4_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int32_t x_aligned) {
-    if (m > kMaxRows || n > kMaxRows || k > kMaxK) return 0;  // refused by the product
+    if (m > kMaxRows || n > kMaxRows || k > kMaxK || !launchable(form_of(m, n, k), m, n)) return 0;  // refused by the product
     return copy_bytes(m, n, k, x_aligned != 0);
 }
 

@@ -887,6 +887,18 @@ uint64_t attention_workspace(uint64_t batch, uint64_t q_heads, uint32_t head_dim
     return (slots ? slots : batch * splits) * q_heads * (head_dim + 2) * sizeof(float) + (slots ? 2 * batch * sizeof(uint32_t) : 0);
 }
 
+uint64_t workgroups(uint64_t batch, uint32_t kv_heads, uint32_t tiles, uint32_t splits, uint64_t slots) {
+    return (slots ? slots : batch * splits) * kv_heads * tiles;
+}
+
+// Whether both kernels' work items fit a launch, which holds fewer than 2^32
+// (the counts that can get here stay within 64 bits).
+bool launchable(uint64_t batch, uint64_t q_heads, uint32_t kv_heads, uint32_t tiles, uint32_t splits, uint64_t slots) {
+    constexpr uint64_t kItems = uint64_t{1} << 32;
+    return workgroups(batch, kv_heads, tiles, splits, slots) < kItems / (64 * kWaves) &&
+           (splits == 1 || batch * q_heads < kItems / kJoinThreads);
+}
+
 bool attention_sizes_ok(uint64_t batch, uint64_t q_heads, uint32_t kv_heads, uint32_t page_size, uint64_t width) {
     return batch <= (1u << 24) && kv_heads > 0 && q_heads > 0 && q_heads <= (1u << 20) && q_heads % kv_heads == 0 &&
            width > 0 && width <= 0x7FFFFFFFu / page_size;
@@ -943,14 +955,14 @@ df11_status attention(const df11_paged_cache *c, const uint16_t *q, uint64_t bat
     p.slots = static_cast<uint32_t>(slots_of(batch, p.kv_heads, p.tiles, p.positions, p.splits));
     const bool even = p.slots != 0;
     p.class_shift = p.positions >> kClassBits ? log2_of(p.positions - 1) + 1 - kClassBits : 0;
+    if (!launchable(batch, q_heads, p.kv_heads, p.tiles, p.splits, p.slots)) return DF11_E_INVALID_ARG;
     if (workspace_bytes < attention_workspace(batch, q_heads, c->head_dim, p.splits, p.slots)) return DF11_E_BUFFER_TOO_SMALL;
     if (p.splits > 1 && !workspace) return DF11_E_INVALID_ARG;
     p.part = static_cast<float *>(workspace);
     const uint64_t chunks = even ? p.slots : p.splits > 1 ? batch * p.splits : 0;
     p.stats = p.part + chunks * q_heads * c->head_dim;
     p.cuts = even ? reinterpret_cast<uint32_t *>(p.stats + chunks * q_heads * 2) : nullptr;
-    const uint64_t groups = even ? chunks * p.kv_heads * p.tiles : units * p.splits;
-    if (groups > 0x7FFFFFFFu || rows > 0x7FFFFFFFu) return DF11_E_INVALID_ARG;
+    const uint64_t groups = workgroups(batch, p.kv_heads, p.tiles, p.splits, p.slots);
     const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const Order order = order_of(batch, units, p.positions, p.splits, p.slots);
@@ -985,7 +997,9 @@ extern "C" uint64_t df11_paged_attention_workspace_bytes(uint64_t batch, uint64_
     const uint32_t tiles = (group + kHeadTile - 1) / kHeadTile;
     const uint64_t positions = table_width * page_size;
     const uint32_t splits = splits_of(batch, kv_heads, tiles, positions);
-    return attention_workspace(batch, q_heads, head_dim, splits, slots_of(batch, kv_heads, tiles, positions, splits));
+    const uint64_t slots = slots_of(batch, kv_heads, tiles, positions, splits);
+    if (!launchable(batch, q_heads, kv_heads, tiles, splits, slots)) return 0;
+    return attention_workspace(batch, q_heads, head_dim, splits, slots);
 }
 
 extern "C" df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch,

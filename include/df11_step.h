@@ -64,8 +64,9 @@ df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, uin
  * on what runs beside it: every sum has a fixed order.  y must not overlap
  * the inputs.  Errors: DF11_E_INVALID_ARG (null or misaligned pointers,
  * strides below k or n or over 2^32, m times a stride over 2^48, m or n over
- * 2^31 - 1, k over 2^21), DF11_E_BUFFER_TOO_SMALL (workspace_bytes),
- * DF11_E_HIP. */
+ * 2^31 - 1, k over 2^21, more rows of w than a launch holds: 2^27 with up to 4
+ * rows of x, 2^29 with up to 32, m n of 2^37 with more), DF11_E_BUFFER_TOO_SMALL
+ * (workspace_bytes), DF11_E_HIP. */
 df11_status df11_mx4_matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride, const uint8_t *codes,
                             const uint8_t *scales, uint64_t n, uint16_t *y, uint64_t y_stride, void *workspace,
                             uint64_t workspace_bytes, void *hip_stream);
@@ -136,8 +137,10 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  * page_table, lens and starts must not be written to while the call runs.
  * Errors: DF11_E_INVALID_ARG (null or misaligned pointers; table_width 0, or
  * 2^31 positions or more in it; table_stride below table_width; strides as for
- * the append; more than 2^20 query heads), DF11_E_UNSUPPORTED (as above),
- * DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
+ * the append; more than 2^20 query heads; more than a launch holds: batch x
+ * kv_heads x ceil(q_heads / kv_heads / 16), times the chunks of a sequence where they
+ * are split, below 2^24, and there batch x q_heads too), DF11_E_UNSUPPORTED
+ * (as above), DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
 df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch, uint64_t q_heads,
                                  uint64_t q_batch_stride, uint64_t q_head_stride, const int32_t *page_table,
                                  uint64_t table_stride, uint64_t table_width, const int32_t *lens,

@@ -216,6 +216,9 @@ def test_a_derivative_is_refused():
 
 
 @pytest.mark.parametrize("change", [
+    # more rows of w than a launch has work items for, with 1, 4, 5 and 32 rows of x, and more tiles than that
+    dict(m=1, n=1 << 27), dict(m=4, n=(1 << 27) - 15), dict(m=1, n=(1 << 31) - 1), dict(m=5, n=1 << 29), dict(m=32, n=1 << 30),
+    dict(m=1 << 19, n=1 << 20), dict(m=1 << 31 - 1, n=1 << 31 - 1),
     # rows of x or y past 2^48 values
     dict(m=1 << 20, xs=1 << 32), dict(m=1 << 20, n=64, ys=1 << 32),
 ])
@@ -255,6 +258,9 @@ def test_appends_past_the_addresses(change):
 
 
 @pytest.mark.parametrize("change", [
+    # workgroups: a cache head of a sequence each, cut into chunks, and rows of the join
+    dict(batch=1 << 21), dict(batch=1 << 24), dict(batch=1 << 17, heads=128, kv_heads=128), dict(batch=1 << 20, width=512),
+    dict(batch=1 << 19, heads=32, kv_heads=2, width=512),
     # addresses
     dict(batch=1 << 15, qb=1 << 33), dict(heads=1 << 20, qh=1 << 40), dict(batch=1 << 15, ts=1 << 33),
 ])
