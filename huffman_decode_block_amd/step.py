@@ -101,6 +101,8 @@ def _place(dev, stream):
             return handle, None
         # the null stream has no ExternalStream: torch takes its handle, 0, for one that was not given
         stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"stream belongs to GPU {stream.device_index}, the tensors to {dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 

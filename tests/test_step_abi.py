@@ -273,3 +273,11 @@ def test_attention_past_a_launch_or_the_addresses(change):
     assert got == hdb.DF11_E_INVALID_ARG
     if not {"qb", "qh", "ts"} & set(change):
         assert hdb.df11_paged_attention_workspace_bytes(a["batch"], a["heads"], a["kv_heads"], 128, 16, a["width"]) == 0
+
+
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    fake = Streams(0x40)
+    monkeypatch.setattr(hdb.step, "_torch", fake)
+    assert hdb.step._place(1, fake.cuda.Stream(0x80, 1)) == (0x80, ("on", 0x80))
+    with pytest.raises(ValueError, match="GPU 0, the tensors to 1"):
+        hdb.step._place(1, fake.cuda.Stream(0x80, 0))
