@@ -635,13 +635,22 @@ df11_status dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t row
 //  - Tiles of 64 x 128 up to three for each compute unit, four of which fit it at a
 //    time: 1536 x 4096 x 4096 (768 tiles) 49.3 us against 51.2 for 64 x 256, 384 x 14336 x
 //    4096 (672) 46.9 against 52.1, 512 x 14336 x 4096 (896) 63.3 against 54.8.
-//  - Larger ones of 128 rows where those give 256 tiles, else 64: 2048 x 4096 x
-//    4096 (256 tiles of 128) 56.8 us against 58.8, 1536 x 4096 x 4096 (192) 54.7
-//    against 52.4.
-//  - Up to 256 tiles, one for a compute unit, a tile has two groups of waves
-//    that take stages in turn: 512 x 4096 x 4096 27.6 us against 32.3, 2048 x 4096 x
-//    14336 188 against 212; with more tiles other workgroups are there to fill
-//    the waits (768 x 4096 x 4096, 384 tiles of 64 x 128: 37.0 against 34.7).
+//  - Larger ones of 64 or 128 rows, by the tiles of 128 rows that there would be (us with 64
+//    and with 128; k of 2,080 and 11,008 is read with a byte of scales for each block):
+//      up to 256, one for a compute unit, where 128 has two groups of waves: 1792 x 4096 (224)
+//      with k of 1,024, 4,096, 14,336: 24.5 and 25.9, 61.5 and 60.9, 199 and 193, of 1,056,
+//      2,080, 11,008: 27.5 and 27.8, 40.7 and 39.5, 198 and 148.  832 x 8192 the same, but for
+//      k of 4,096: 59.3 and 61.7;
+//      up to 384: 2304 x 4096 (288) with k of 1,024, 4,096, 14,336: 30.5 and 34.2, 87.4 and
+//      96.3, 283 and 271, of 1,056, 2,080, 11,008: 33.5 and 37.5, 53.5 and 59.9, 286 and 260;
+//      1536 x 8192 (384) with k of 14,336: 310 and 320, of 11,008 298 and 264;
+//      past 384: 1664 x 8192 (416) with k of 1,024, 4,096, 14,336: 38.3 and 36.2, 118 and 102,
+//      381 and 316.  Past 512 a last round that is not full favours 64 by up to a tenth (576,
+//      2304 x 8192 x 4096: 139 and 152), a full one 128 (1,024: 231 and 218; 1,792: 405 and 367).
+//  - Two groups of waves in a tile, which take stages in turn, up to 256 tiles, one for a
+//    compute unit: 512 x 4096 x 4096 in 64 x 128 27.6 us against 32.3, 1792 x 4096 x 4096 in
+//    128 x 256 60.9 against 69.2; with more tiles other workgroups are there to fill the
+//    waits (768 x 4096 x 4096, 384 tiles of 64 x 128: 37.0 against 34.7).
 struct Form {
     bool token;
     uint32_t x, rows;  // of x and of w in a piece or tile; token form: tiles of 16 rows of w
@@ -649,11 +658,18 @@ struct Form {
 
 uint64_t pieces(uint64_t m, uint64_t x, uint64_t n, uint64_t w) { return ((m + x - 1) / x) * ((n + w - 1) / w); }
 
+// Whether tiles of 128 rows, of which there would be this many, take less time than those of 64.
+bool large_tiles(uint64_t tiles, uint64_t k) {
+    const bool narrow = k % 512 != 0;  // scales by the byte
+    if (tiles <= 256) return k > (narrow ? 1536 : 4096);
+    return tiles > 384 || (narrow && k > 8192);
+}
+
 Form form_of(uint64_t m, uint64_t n, uint64_t k) {
     if (m <= 4) return {true, 4, 1};
     if (m > 32 && pieces(m, 64, n, 64) > (k <= 1024 ? 128 : 256)) {
         if (pieces(m, 64, n, 128) <= 768) return {false, 64, 128};
-        return {false, pieces(m, 128, n, 256) >= 256 ? 128u : 64u, 256};
+        return {false, large_tiles(pieces(m, 128, n, 256), k) ? 128u : 64u, 256};
     }
     if (m > 32)
         for (uint32_t rows : {4u, 2u})
@@ -715,7 +731,6 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     if (workspace_bytes < copy) return DF11_E_BUFFER_TOO_SMALL;
     if (copy && !workspace) return DF11_E_INVALID_ARG;
     const uint64_t tiles = f.token ? 0 : pieces(m, f.x, n, f.rows);
-    const bool two = tiles <= 256;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     MulParams p = {};
     p.x = x;
@@ -759,6 +774,7 @@ df11_status matmul(const uint16_t *x, uint64_t m, uint64_t k, uint64_t x_stride,
     p.tiles_m = static_cast<uint32_t>((m + f.x - 1) / f.x);
     p.tiles_n = static_cast<uint32_t>((n + f.rows - 1) / f.rows);
     const dim3 grid(static_cast<uint32_t>(tiles));
+    const bool two = tiles <= 256;
     if (f.rows == 128) return launched(two ? launch_tile<4, 2, 2>(wide, grid, st, p) : launch_tile<4, 2, 1>(wide, grid, st, p));
     if (f.x == 64) return launched(launch_tile<4, 4, 1>(wide, grid, st, p));  // always more than 256 tiles
     return launched(two ? launch_tile<8, 4, 2>(wide, grid, st, p) : launch_tile<8, 4, 1>(wide, grid, st, p));

@@ -353,6 +353,7 @@ def test_derivatives_are_refused(torch):
 EVERY_WAY = [
     (1, 300, 4096), (4, 130, 320), (20, 200, 96), (64, 520, 2048), (33, 150, 333),
     (640, 2048, 512), (1100, 5000, 96), (333, 2050, 333), (1600, 4096, 512), (2048, 4096, 1536), (2100, 5000, 160),
+    (1600, 4096, 4608), (1610, 4090, 1568), (2100, 6200, 160), (3200, 4096, 512),
 ]
 
 
@@ -451,3 +452,12 @@ def test_tiles_on_another_stream_and_in_a_graph(torch, m, n, k):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, hdb.df11_mx4_matmul(x, c, s))
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (2100, 6200, 160), (3137, 4100, 544), (4096, 4096, 512), (2049, 6145, 70), (1300, 10250, 1030), (1290, 10250, 2048),  # one group
+    (1600, 4096, 4608), (2040, 4090, 5120), (1610, 4090, 1568), (820, 8190, 1999),                                          # two
+    (2100, 4100, 8224),  # one, for a long k
+])
+def test_product_in_tiles_of_128_rows(torch, m, n, k):
+    test_product_in_every_form(torch, m, n, k)
