@@ -118,7 +118,9 @@ quantize_kernel(const uint16_t *x, uint64_t row_stride, uint32_t cols, uint32_t 
 // ---- Expansion to BF16 -----------------------------------------------------
 
 // Two BF16 values of one byte of codes under scale byte s; the conversion
-// takes the scale as a 32-bit float of which it reads the exponent.
+// takes the scale as a 32-bit float of which it reads the exponent.  Under an
+// exponent of 255 every code gives NaN, that of zero too, which is what the
+// product needs of a block with s = 255; the expansion writes one NaN for all.
 template <int kByte>
 __device__ __forceinline__ uint32_t expand2(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, kByte));
@@ -202,22 +204,6 @@ typedef __attribute__((address_space(3))) void *LdsPtr;
 // not (vmcnt 0; the other counters as they are).
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
-// Token form, for few rows: a workgroup takes 16 kRows rows of w by kX of x, its
-// waves share k between them and add their sums in LDS.  A lane reads 16 bytes
-// of codes at a time, which is one block of one row: lane l has row l % 16 and
-// block 4 s + l / 16 of step s.  The matrix instruction's k index is ours to
-// choose, as long as both operands agree: its i-th instruction of a step takes
-// codes 8 i .. 8 i + 7 of every lane's block, so nothing moves between lanes and
-// one scale serves all of a lane's codes.
-// Bound by HBM for the largest (1 x 128256 x 4096: 279 MB in 48 us, 5.8 TB/s), by
-// a kernel's own start and end for the smallest (1 x 4096 x 4096: 4 us), and by
-// the path of vector loads as soon as those are not few and wide.  So x comes
-// in rows of 256 bytes a step by loads into the wave's own part of LDS, one
-// instruction for 4 rows (piece c of row i lies at c ^ (i % 16), as in the tile
-// form), and the scales of four steps in one load of 16 bytes.  With x read
-// from memory in the order of the matrix instruction, four loads a step, and a
-// byte of scales for each block, 1 x 128256 x 4096 took 88 us and 16 x 4096 x
-// 14336 21 where it is 10.6 now.
 // Eight values of a row of k values, from column col on, zeros past its end.
 __device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint32_t k) {
     uint32_t w[4] = {0, 0, 0, 0};
@@ -234,9 +220,26 @@ __device__ __forceinline__ v4u piece_of(const uint16_t *row, uint32_t col, uint3
     return v4u{w[0], w[1], w[2], w[3]};
 }
 
-// How the token form reads: kReadWide as above, for k in multiples of 512;
-// kReadNarrow with a byte of scales for each block; kReadAny also takes rows of
-// x that start anywhere and end inside a block, through registers.
+// Token form, for few rows: a workgroup takes 16 kRows rows of w by kX of x, its
+// waves share k between them and add their sums in LDS.  A lane reads 16 bytes
+// of codes at a time, which is one block of one row: lane l has row l % 16 and
+// block 4 s + l / 16 of step s.  The matrix instruction's k index is ours to
+// choose, as long as both operands agree: its i-th instruction of a step takes
+// codes 8 i .. 8 i + 7 of every lane's block, so nothing moves between lanes and
+// one scale serves all of a lane's codes.
+// Bound by HBM for the largest (1 x 128256 x 4096: 279 MB in 48 us, 5.8 TB/s), by
+// a kernel's own start and end for the smallest (1 x 4096 x 4096: 4 us), and by
+// the path of vector loads as soon as those are not few and wide.  So x comes
+// in rows of 256 bytes a step by loads into the wave's own part of LDS, one
+// instruction for 4 rows (piece c of row i lies at c ^ (i % 16), as in the tile
+// form), and the scales of four steps in one load of 16 bytes.  With x read
+// from memory in the order of the matrix instruction, four loads a step, and a
+// byte of scales for each block, 1 x 128256 x 4096 took 88 us and 16 x 4096 x
+// 14336 21 where it is 10.6 now.
+//
+// How it reads: kReadWide as above, for k in multiples of 512; kReadNarrow with
+// a byte of scales for each block; kReadAny also takes rows of x that start
+// anywhere and end inside a block, through registers.
 enum TokenReads : int { kReadWide, kReadNarrow, kReadAny };
 
 constexpr int kTokenWaves = 8;
@@ -354,19 +357,20 @@ token_kernel(MulParams p) {
 }
 
 // Tile form, for many rows: a workgroup computes a tile of 16 kTiles rows of x
-// by 64 kCols rows of w, each wave of a group of four 16 kTiles by 16 kCols of it, in
-// stages of 128 along k; two groups take the stages in turn and add their sums.  x
-// goes to LDS by loads that write there directly, two stages, the next one loading
-// while one is computed.  The codes go from
-// memory to the registers of the waves that use them and are expanded there:
-// a lane's 16 bytes are one block of 32, k as in the token form.  A row of x
-// in LDS is 16 pieces of 16 bytes; piece c of row i lies at c ^ (i % 16), so
-// that the 16 rows a read touches use all banks once.  Row m of a wave's t-th
-// tile of w is row 4 kCols (m / 4) + 4 t + m % 4 of its 16 kCols, which leaves a lane
-// with 4 kCols neighbouring columns of y in the end.
+// by 64 kCols rows of w, each wave of a group of four 16 kTiles by 16 kCols of
+// it, in stages of 128 along k; two groups take the stages in turn and add their
+// sums.  x goes to LDS by loads that write there directly, two stages, the next
+// one loading while one is computed.  The codes go from memory to the registers
+// of the waves that use them and are expanded there: a lane's 16 bytes are one
+// block of 32, k as in the token form.  A row of x in LDS is 16 pieces of 16
+// bytes; piece c of row i lies at c ^ (i % 16), so that the 16 rows a read
+// touches use all banks once.  Row m of a wave's t-th tile of w is row
+// 4 kCols (m / 4) + 4 t + m % 4 of its 16 kCols, which leaves a lane with
+// 4 kCols neighbouring columns of y in the end.
 // Scales come with kWide, for k in multiples of 512, for four stages at a time
 // and through LDS like x; else by a byte for each block (8192 x 8192 x 8192: 744
-// us against 805).
+// us against 805; it costs more where tiles are many and k is long: 64 x 256
+// tiles of 1792 x 4096 take 199 us for k of 14,336 and 198 for 11,008).
 // Bound by the matrix unit, held back by the loads of a stage: 8192 x 8192 x 8192
 // in 744 us, 1.48 PFLOP/s (a large BF16 product of the vendor's library reaches
 // 1.39 on the same card), 2048 x 14336 x 4096 in 186, 1.30; expanding the codes
@@ -427,8 +431,8 @@ tile_kernel(MulParams p) {
                                                      off + 4 * kTileWaves * i * row_bytes, k0, 0, 0);
     };
     // scales of the wave's rows: 16 bytes of a row, four stages', in one load (of 64
-    // rows: with kCols of 2 the other half are not its own)
-    // into the wave's part of LDS, two parts in turn
+    // rows: with kCols of 2 the other half are not its own) into the wave's part of
+    // LDS, two parts in turn
     uint8_t *scale_part = s_scale + (group * kTileWaves + wave) * 2048;
     auto load_scales = [&](uint32_t four) {
         const uint32_t row = kWaveN * wave + lane;

@@ -31,9 +31,12 @@ struct Pages {
 
 // ---- Append ----------------------------------------------------------------
 // A lane moves 8 values of K and the same 8 of V.  Bound by the launch for the
-// tokens of a step (32 tokens of 8 heads of 128: 2.6 us, the shortest a kernel
-// takes here), by HBM for a prompt (8,192 tokens into E4M3 pages: 50 MB in 11.3
-// us, 4.5 TB/s, where a large copy reaches 4.7).
+// tokens of a step (32 tokens of 8 heads of 128: 2.7 us, the shortest a kernel
+// takes here), by HBM for a prompt (8,192 tokens into BF16 pages: 67 MB in 12.8
+// us, 5.2 TB/s).  Into E4M3 pages, a tenth of the tokens padding, 46 MB take
+// 13.0 us, 3.5 TB/s (11.4 for a call among others, whose start the one before
+// hides): not by HBM alone; the conversion's arithmetic and stores half as wide
+// are what differs.
 
 struct AppendParams {
     Pages k, v;
@@ -131,12 +134,12 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 
 // ---- Attention of one token ------------------------------------------------
 // A sequence's positions are cut into chunks of steps of 32 positions, by the
-// lengths as the device finds them; a workgroup takes one chunk of one cache head
-// for up to 16 of its query heads, its four waves the chunk's steps in turn.  Each wave keeps the running maximum, sum and weighted values
-// of what it has seen, the waves join in LDS, and a second kernel joins the
-// chunks.  The host knows the page table's width and not the lengths, so it
-// chooses one of three ways to share the work (Order), and the device fits it to
-// the lengths:
+// lengths as the device finds them; a workgroup takes one chunk of one cache
+// head for up to 16 of its query heads, its four waves the chunk's steps in
+// turn.  Each wave keeps the running maximum, sum and weighted values of what it
+// has seen, the waves join in LDS, and a second kernel joins the chunks.  The
+// host knows the page table's width and not the lengths, so it chooses one of
+// three ways to share the work (Order), and the device fits it to the lengths:
 //   kAsGiven   every sequence is cut into up to `splits` chunks of 128 or more
 //   kByLength  one chunk each; compute units get long and short sequences in turn
 //   kEvenly    chunks of one length for all sequences, long ones have more of them
@@ -157,14 +160,15 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
 // large as the output's own rounding, so they are given as two, high part and
 // remainder.  A BF16 V may hold infinities, which a weight keeps only if neither
 // part is zero or negative: there the high part is cut off, not rounded, which
-// leaves a remainder that is not negative, and the remainder is at least
-// 2^-126 (both parts together are off by up to 2^-16 of the weight, by 2^-17
-// with a rounded high part, which E4M3's V, without infinities, gets).  The matrix unit has time for it: the kernel is bound by reading
-// K and V, each once.  At 8 sequences of 32,768 positions, 8 cache heads of 128
-// and 64 query heads: BF16 1.07 GB in 185 us, 5.8 TB/s; E4M3 537 MB in 99 us, 5.4
-// TB/s.  Where there is less to read the start and the end count: one sequence
-// of 8,192 takes 9.7 us and its join 3.9 (33.5 MB would take 5.9 at the former
-// rate), 64 ragged ones up to 1,024 positions 28 us for 124 MB.
+// leaves a remainder that is not negative, and the remainder is at least 2^-126
+// (both parts together are off by up to 2^-16 of the weight, by 2^-17 with a
+// rounded high part, which E4M3's V, without infinities, gets; no time was
+// lost by it).  The matrix unit has time for two products: the kernel is bound
+// by reading K and V, each once.  At 8 sequences of 32,768 positions, 8 cache
+// heads of 128 and 64 query heads: BF16 1.07 GB in 184 us, 5.8 TB/s; E4M3 537 MB
+// in 94, 5.7 TB/s.  Where there is less to read the start and the end count: one
+// sequence of 8,192 takes 9.2 us and its join 3.8 (33.5 MB would take 5.8 at the
+// former rate), 64 ragged ones up to 1,024 positions 27 us for 134 MB.
 
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;

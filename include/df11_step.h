@@ -49,9 +49,9 @@ df11_status df11_mx4_quantize(const uint16_t *x, uint64_t rows, uint64_t cols, u
                               uint8_t *codes, uint8_t *scales, void *hip_stream);
 
 /* out (BF16, out_stride >= cols) := the values that codes and scales stand
- * for.  Exact, but for values below BF16's smallest magnitude (2^-133; only
- * s < 5 gives any), which do not occur in what df11_mx4_quantize writes from
- * BF16 and round to nearest even.  Errors as above. */
+ * for.  Exact: the smallest, 2^-128, is a BF16 denormal.  Those of 2^128 and
+ * more (s of 253 and 254, which df11_mx4_quantize does not write) become
+ * infinities, in the product too.  Errors as above. */
 df11_status df11_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, uint64_t rows, uint64_t cols,
                                 uint16_t *out, uint64_t out_stride, void *hip_stream);
 
