@@ -104,8 +104,8 @@ typedef struct df11_paged_cache {
  * device, one 64-bit number for each token, page * page_size + position in
  * the page; a slot below 0 or past the cache is skipped (padding).  E4M3: the
  * stored value is x / scale[h] rounded to nearest even, magnitudes over 448
- * (infinities too) become 448, NaN stays NaN.  Two tokens with one slot leave
- * either's values.  tokens = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null
+ * (infinities too) become 448, NaN stays NaN.  Of two tokens with one slot each
+ * 8 values are either's.  tokens = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null
  * or misaligned pointers, sizes past the limits above, 2^31 tokens or more,
  * strides over 2^40 or, times what they step over, 2^48 together),
  * DF11_E_UNSUPPORTED (head_dim, page_size or dtype), DF11_E_HIP. */
@@ -127,10 +127,12 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  * and where that sum is zero (no position is left, or only scores of
  * -infinity), zeros and -infinity.  What masked positions hold, NaN included,
  * does not matter.  An infinity in v_j gives infinities of its sign (and with
- * one of the other sign, NaN), if exp(s_j) is above 2^-126 of the largest: below, a
- * weight is zero in 32 bits, and zero times infinity NaN.  Scores, maxima, sums and the weighted
- * values are held in 32 bits; the weights exp(s_j) enter the product as two
- * BF16 parts (16 bits of mantissa).  The result does not depend on what runs
+ * one of the other sign, NaN), if exp(s_j) is above 2^-126 of the largest:
+ * below, a weight is zero in 32 bits, and zero times infinity NaN.  Scores,
+ * maxima, sums and the weighted values are held in 32 bits (their sum before
+ * the division, which values of 2^128 over the number of positions can take
+ * past the largest number); the weights exp(s_j) enter the product as two BF16
+ * parts (16 bits of mantissa).  The result does not depend on what runs
  * beside it.  workspace: df11_paged_attention_workspace_bytes bytes of device
  * memory, 16-byte aligned (NULL when that is 0), not kept between calls;
  * calls that run at the same time need one each.  batch = 0 is a no-op.
@@ -138,9 +140,10 @@ df11_status df11_paged_append(const df11_paged_cache *cache, const uint16_t *k, 
  * Errors: DF11_E_INVALID_ARG (null or misaligned pointers; table_width 0, or
  * 2^31 positions or more in it; table_stride below table_width; strides as for
  * the append; more than 2^20 query heads; more than a launch holds: batch x
- * kv_heads x ceil(q_heads / kv_heads / 16), times the chunks of a sequence where they
- * are split, below 2^24, and there batch x q_heads too), DF11_E_UNSUPPORTED
- * (as above), DF11_E_BUFFER_TOO_SMALL (workspace_bytes), DF11_E_HIP. */
+ * kv_heads x ceil(q_heads / kv_heads / 16), times the chunks of a sequence
+ * where they are split, below 2^24, and there batch x q_heads too),
+ * DF11_E_UNSUPPORTED (as above), DF11_E_BUFFER_TOO_SMALL (workspace_bytes),
+ * DF11_E_HIP. */
 df11_status df11_paged_attention(const df11_paged_cache *cache, const uint16_t *q, uint64_t batch, uint64_t q_heads,
                                  uint64_t q_batch_stride, uint64_t q_head_stride, const int32_t *page_table,
                                  uint64_t table_stride, uint64_t table_width, const int32_t *lens,
