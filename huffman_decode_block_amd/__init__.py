@@ -1,6 +1,8 @@
 """Python binding of libdf11 (include/df11.h): DFloat11 block encoding on the
-host and block decoding on an MI355X; and, in the step module, the operators
-of include/df11_step.h (4-bit weights, paged key-value cache).
+host and block decoding on an MI355X; in the step module, the operators of
+include/df11_step.h (4-bit weights, paged key-value cache); and, in the search
+module, those of include/df11_search.h (attention of drafted trees, pages copied,
+forked and compacted, a beam search's selection).
 
 Argument marshalling only: every step of the encoder runs in the library's
 C++ code and every step of the decode runs in its HIP kernel.  PyTorch is used
@@ -18,7 +20,12 @@ import os
 
 import numpy as np
 
-from . import step
+from . import search, step
+from .search import (  # noqa: F401
+    DF11_LOGITS_BF16, DF11_LOGITS_FP32, SEARCH_EXPORTS, df11_beam_select, df11_beam_select_workspace_bytes,
+    df11_paged_compact, df11_paged_copy, df11_paged_fork, df11_paged_fork_workspace_bytes, df11_paged_tree_attention,
+    df11_paged_tree_attention_workspace_bytes,
+)
 from .step import (  # noqa: F401
     DF11_CACHE_BF16, DF11_CACHE_E4M3, STEP_EXPORTS, df11_mx4_dequantize, df11_mx4_matmul,
     df11_mx4_matmul_workspace_bytes, df11_mx4_quantize, df11_paged_append, df11_paged_attention,
@@ -178,6 +185,7 @@ def lib():
     L.df11_hip_error_name.argtypes = [ctypes.c_int32]
     L.df11_hip_error_name.restype = ctypes.c_char_p
     step.declare(L)
+    search.declare(L)
     _lib = L
     return L
 
@@ -674,4 +682,7 @@ __all__ = [
     "df11_mx4_quantize", "df11_mx4_dequantize", "df11_mx4_matmul", "df11_mx4_matmul_workspace_bytes",
     "df11_paged_append", "df11_paged_attention", "df11_paged_attention_workspace_bytes",
     "DF11_CACHE_BF16", "DF11_CACHE_E4M3",
+    "df11_paged_tree_attention", "df11_paged_tree_attention_workspace_bytes", "df11_paged_copy", "df11_paged_compact",
+    "df11_paged_fork", "df11_paged_fork_workspace_bytes", "df11_beam_select", "df11_beam_select_workspace_bytes",
+    "DF11_LOGITS_BF16", "DF11_LOGITS_FP32",
 ]
