@@ -18,7 +18,8 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;
 constexpr uint32_t kMinChunk = kWaves * kStep;
-constexpr uint32_t kMaxChunk = 16384;
+constexpr uint32_t kMaxChunk = 4096;  // positions whose pages LDS holds
+constexpr uint32_t kChunkPages = kMaxChunk / kMinPage + 1;
 constexpr uint32_t kPad = 4;  // floats between rows in LDS: they start in different banks
 constexpr float kSlack = 8;   // powers of two that weights may grow to before their reference follows
 
@@ -44,12 +45,10 @@ __device__ __forceinline__ uint32_t bits_between(int32_t lo, int32_t hi) {
     return static_cast<uint32_t>(below_h & ~below_l);
 }
 
-__device__ __forceinline__ uint32_t pack2h(float a, float b) {
-    h2 v;
-    v.x = static_cast<_Float16>(a);
-    v.y = static_cast<_Float16>(b);
-    return __builtin_bit_cast(uint32_t, v);
-}
+// Two floats rounded to FP16, and to BF16, by one instruction.
+__device__ __forceinline__ uint32_t pack2h(float a, float b) { return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, h2)); }
+
+__device__ __forceinline__ uint32_t pack2b(float a, float b) { return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, bf2)); }
 
 // Two FP16 values from two bytes of E4M3 (exact).
 template <bool kHigh>
@@ -71,21 +70,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return m * 0xFFFFu;
 }
 
-// Two values' kinds as BF16 numbers: 1 for infinity, 64 for -infinity, 4096 for
-// NaN, 0 for all others; sums of 32 of them tell the kinds apart.
+// A value's kind as a BF16 number: 1 for infinity, 64 for -infinity, 4096 for NaN,
+// 0 for all others; sums of 32 of them tell the kinds apart.
 __device__ __forceinline__ uint32_t kind_of(uint32_t bf16) {
     const uint32_t a = bf16 & 0x7FFFu;
     return a < 0x7F80u ? 0u : a > 0x7F80u ? 0x4580u : bf16 & 0x8000u ? 0x4280u : 0x3F80u;
 }
 
-template <bool kE4M3, class Row>
-__device__ __forceinline__ uint32_t kind2(const Row &row, int j) {
-    if (kE4M3) {
-        const uint32_t w = row[j / 4] >> (8 * (j & 3));
-        return ((w & 0x7Fu) == 0x7Fu ? 0x4580u : 0u) | ((w & 0x7F00u) == 0x7F00u ? 0x45800000u : 0u);
-    }
-    const uint32_t w = row[kE4M3 ? 0 : j / 2];
-    return kind_of(w & 0xFFFFu) | kind_of(w >> 16) << 16;
+template <bool kE4M3>
+__device__ __forceinline__ uint32_t kind_at(const uint8_t *row, uint32_t d) {
+    if (kE4M3) return (row[d] & 0x7Fu) == 0x7Fu ? 0x4580u : 0u;
+    return kind_of(reinterpret_cast<const uint16_t *>(row)[d]);
 }
 
 __device__ __forceinline__ float of_counts(float sum) {
@@ -93,49 +88,367 @@ __device__ __forceinline__ float of_counts(float sum) {
     return n >> 12 || (plus && minus) ? NAN : plus ? INFINITY : minus ? -INFINITY : 0.0f;
 }
 
-constexpr int waves_for(int dim, int tiles) { return dim * tiles <= 64 ? 3 : dim * tiles <= 256 && dim < 256 ? 2 : 1; }
+// Four values of a row's output, or of its part in a chunk: `there` where the row has a node.
+template <int kDim>
+__device__ __forceinline__ void write_out(const TreeParams &p, uint32_t split, uint64_t row, uint32_t d, bool there, float top, float total, f4 o) {
+    if (!there) {
+        top = -INFINITY;
+        total = 0;
+        o = f4{};
+    }
+    if (p.splits == 1) {
+        if (total == 0) o = f4{};
+        const float inv = total == 0 ? 0.0f : 1.0f / total;
+        v2u to;
+        to.x = pack2b(o[0] * inv, o[1] * inv);
+        to.y = pack2b(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<v2u *>(p.out + row * kDim + d) = to;
+        if (d == 0 && p.lse) p.lse[row] = ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(total)) * kLn2;
+    } else {
+        const uint64_t at = row * p.splits + split;
+        *reinterpret_cast<f4 *>(p.part + at * kDim + d) = o;
+        if (d == 0) {
+            p.stats[2 * at] = top;
+            p.stats[2 * at + 1] = total;
+        }
+    }
+}
 
+// What a workgroup works on: a tile of the rows (row n: node n / group, head n %
+// group) of a cache head of a sequence, and a chunk of its positions.
+struct Work {
+    uint32_t tile, b, h, split;
+    bool none;
+};
+
+__device__ __forceinline__ Work work_of(const TreeParams &p) {
+    // workgroups go round the 8 XCDs: those of one chunk's tiles, which read the
+    // same keys and values, stay on one
+    const uint32_t turn = blockIdx.x / (8 * p.tiles), in = blockIdx.x - turn * 8 * p.tiles;
+    Work w;
+    w.tile = in / 8;
+    uint32_t unit = turn * 8 + (in & 7u);
+    w.none = unit >= p.units;
+    w.h = unit % p.kv_heads;
+    unit /= p.kv_heads;
+    w.b = unit % p.batch;
+    w.split = unit / p.batch;
+    return w;
+}
+
+struct Rows {
+    uint32_t row0, rows;  // of the tile
+    int32_t count, len;   // of the sequence
+};
+
+__device__ __forceinline__ Rows rows_of(const TreeParams &p, const Work &w, uint32_t per_tile) {
+    Rows r;
+    r.row0 = w.tile * per_tile;
+    r.rows = min(per_tile, p.nodes * p.group - r.row0);
+    r.count = min(max(p.counts ? p.counts[w.b] : INT32_MAX, 0), static_cast<int32_t>(p.nodes));
+    r.len = static_cast<int32_t>(min(static_cast<uint32_t>(max(p.lens[w.b], 0)), p.positions));
+    return r;
+}
+
+// Where row i of a tile lies among the outputs' rows.
+__device__ __forceinline__ uint64_t out_row(const TreeParams &p, const Work &w, const Rows &rows, uint32_t i) {
+    const uint32_t n = rows.row0 + i, node = n / p.group;
+    return (uint64_t{w.b} * p.nodes + node) * p.q_heads + w.h * p.group + (n - node * p.group);
+}
+
+// A lane's row in a tile of 16: its node, the first position that it reads, and whether there is such a node.
+struct Row {
+    int32_t node, start;
+    bool have;
+    uint64_t first;  // its mask's first word
+};
+
+__device__ __forceinline__ Row row_of(const TreeParams &p, const Work &w, const Rows &rows, uint32_t i) {
+    Row r;
+    r.node = static_cast<int32_t>(min(rows.row0 + i, p.nodes * p.group - 1) / p.group);
+    r.have = i < rows.rows && r.node < rows.count;
+    r.start = 0;
+    if (p.starts)
+        r.start = min(max(p.starts[w.b * p.starts_batch + static_cast<uint32_t>(r.node) * p.starts_node], 0), rows.len);
+    r.first = p.mask ? static_cast<uint64_t>(p.mask[w.b * p.mask_batch + static_cast<uint32_t>(r.node) * p.mask_node]) : 0;
+    return r;
+}
+
+// The chunk: positions c0..c1 - 1 of those (from lo on) that any row of the tile
+// reads; all rows read those from lo_max to all_hi - 1.
+struct Chunk {
+    int32_t lo, lo_max, all_hi, c0, c1;
+    bool none;
+};
+
+__device__ __forceinline__ Chunk chunk_of(const TreeParams &p, const Work &w, const Rows &rows, int32_t lo, int32_t lo_max) {
+    const int32_t node_first = static_cast<int32_t>(rows.row0 / p.group), node_last = static_cast<int32_t>((rows.row0 + rows.rows - 1) / p.group);
+    const int32_t reach = min(rows.count, p.mask ? rows.count : node_last + 1);
+    const int32_t hi = node_first < rows.count ? static_cast<int32_t>(min(static_cast<uint32_t>(rows.len + reach), p.positions)) : 0;
+    const int32_t base = lo & ~static_cast<int32_t>(kStep - 1);
+    const uint32_t steps = hi > base ? (hi - base + kStep - 1) / kStep : 0;
+    const uint32_t chunks = min(p.splits, (steps + kMinChunk / kStep - 1) / (kMinChunk / kStep));
+    const uint32_t parts = max(chunks, 1u), each = steps / parts, more = steps - each * parts;
+    Chunk c;
+    c.lo = lo;
+    c.lo_max = lo_max;
+    c.all_hi = p.mask ? rows.len : min(rows.len + min(node_first + 1, rows.count), hi);
+    c.none = p.splits > 1 && w.split >= chunks;
+    c.c0 = base + static_cast<int32_t>((w.split * each + min(w.split, more)) * kStep);
+    c.c1 = max(c.c0, min(c.c0 + static_cast<int32_t>((each + (w.split < more)) * kStep), hi));
+    return c;
+}
+
+// Without a chunk: the join gives these rows no weight.
+__device__ __forceinline__ void no_chunk(const TreeParams &p, const Work &w, const Rows &rows) {
+    for (uint32_t i = threadIdx.x; i < rows.rows; i += blockDim.x) {
+        float *to = p.stats + 2 * (out_row(p, w, rows, i) * p.splits + w.split);
+        to[0] = -INFINITY;
+        to[1] = 0;
+    }
+}
+
+__device__ __forceinline__ uint32_t pages_of(const TreeParams &p, const Chunk &c) {
+    return c.c1 > c.c0 ? (static_cast<uint32_t>(c.c1 - 1) >> p.page_shift) - (static_cast<uint32_t>(c.c0) >> p.page_shift) + 1 : 0;
+}
+
+// The chunk's pages into LDS, -1 for those that mask; whether there is one.
+__device__ __forceinline__ int32_t load_pages(const TreeParams &p, const Work &w, const Chunk &c, int32_t *s_page) {
+    const uint32_t n = pages_of(p, c);
+    const int32_t *table = p.table + w.b * p.table_stride + (static_cast<uint32_t>(c.c0) >> p.page_shift);
+    int32_t masked = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+        const int32_t e = table[i];
+        const bool ok = e >= 0 && static_cast<uint64_t>(e) < p.n_pages;
+        s_page[i] = ok ? e : -1;
+        masked |= !ok;
+    }
+    return masked;
+}
+
+// Whether positions p0..p0 + n - 1 have to be looked at one by one.
+__device__ __forceinline__ bool masked_at(const Chunk &c, bool holes, int32_t p0, uint32_t n) {
+    return holes || p0 < c.lo_max || p0 + static_cast<int32_t>(n) > min(c.all_hi, c.c1);
+}
+
+// Of a lane's eight positions, 4 q + 0..3 of each half of a step, those that lie
+// in the chunk, past every start and in pages of the cache.
+__device__ __forceinline__ uint32_t positions_there(const TreeParams &p, const Chunk &c, const int32_t *s_page, int32_t p0, uint32_t q) {
+    const uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift;
+    uint32_t there = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int32_t pos0 = p0 + 16 * t + 4 * static_cast<int32_t>(q);
+        const bool page = s_page[(static_cast<uint32_t>(min(pos0, c.c1 - 1)) >> p.page_shift) - first] >= 0;
+        there |= page ? (bits_between(c.lo - pos0, c.c1 - pos0) & 15u) << (4 * t) : 0u;
+    }
+    return there;
+}
+
+// Those that a row reads.
+__device__ __forceinline__ uint32_t positions_read(const TreeParams &p, const Work &w, const Rows &rows, const Row &row, int32_t p0, uint32_t q) {
+    uint32_t live = bits_between(row.start - p0, rows.len - p0);
+    const int32_t a0 = p0 - rows.len;  // the node at p0
+    if (a0 + static_cast<int32_t>(kStep) > 0) {
+        if (!p.mask) {
+            live |= bits_between(-a0, min(row.node + 1, rows.count) - a0);
+        } else if (a0 < rows.count) {
+            const uint32_t from = static_cast<uint32_t>(max(a0, 0));
+            const uint32_t at = from / 64, shift = from % 64;
+            uint64_t m = row.first;
+            if (p.nodes > 64) {
+                const int64_t *words = p.mask + w.b * p.mask_batch + static_cast<uint32_t>(row.node) * p.mask_node;
+                m = static_cast<uint64_t>(words[at]) >> shift;
+                if (shift > 32 && 64 * (at + 1) < p.nodes) m |= static_cast<uint64_t>(words[at + 1]) << (64 - shift);
+            } else {
+                m >>= shift;
+            }
+            live |= static_cast<uint32_t>(a0 < 0 ? m << -a0 : m) & bits_between(-a0, rows.count - a0);
+        }
+    }
+    return ((live >> (4 * q)) & 15u) | (((live >> (16 + 4 * q)) & 15u) << 4);
+}
+
+// V rows of a step, a lane's piece of each of its eight positions (of one page
+// for each half: pages hold multiples of 8).
+template <int kWords>
+struct Piece {
+    typedef uint32_t Value __attribute__((ext_vector_type(kWords)));
+    typedef Value InMemory __attribute__((aligned(4)));
+};
+
+template <int kWords, class Values>
+__device__ __forceinline__ void load_v_rows(const TreeParams &p, const Chunk &c, const int32_t *s_page, const uint8_t *vb, int32_t p0,
+                                            uint32_t r, uint32_t q, Values &vr) {
+    const uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift, in_page = (1u << p.page_shift) - 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int32_t pos0 = p0 + 16 * t + 4 * static_cast<int32_t>(q);
+        const int32_t page = s_page[(static_cast<uint32_t>(min(pos0, c.c1 - 1)) >> p.page_shift) - first];
+        const uint8_t *at_page = vb + static_cast<uint64_t>(max(page, 0)) * p.v.page + r * (kWords * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = static_cast<uint32_t>(min(pos0 + i, c.c1 - 1));
+            vr[4 * t + i] = *reinterpret_cast<const typename Piece<kWords>::InMemory *>(at_page + uint64_t{at & in_page} * p.v.row);
+        }
+    }
+}
+
+// The running softmax of a lane's row over its wave's positions: weights are
+// exp2(s scale - ref), where ref follows the maximum as soon as it is left more
+// than kSlack behind.
+template <int kPiece>
+struct Running {
+    float ref = -INFINITY, sum = 0;  // sum: over this lane's positions
+    f4 acc[kPiece] = {};
+
+    // Turns a step's scores, -infinity where a position is masked, into weights.  scale > 0.
+    __device__ __forceinline__ void weights(const f4 (&s)[2], float scale, float (&w)[8]) {
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i & 3]);
+        const bool behind = top > -INFINITY && !(top * scale <= ref + kSlack);
+        if (__builtin_expect(__any(behind), 0)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float to = top > -INFINITY ? fmaxf(ref, top * scale) : ref;
+            const float fade = to == ref ? 1.0f : exp2_(ref - to);
+            ref = to;
+            sum *= fade;
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[j][c] *= fade;
+        }
+        const float from = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = exp2_(fmaf(s[i / 4][i & 3], scale, -from));
+            sum += w[i];
+        }
+    }
+};
+
+// Scores of positions that are not read become -infinity.
+__device__ __forceinline__ void mask_scores(f4 (&s)[2], uint32_t live) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i / 4][i & 3] = live >> i & 1u ? s[i / 4][i & 3] : -INFINITY;
+}
+
+// Weights as the product with V takes them: FP16 beside FP16 values (from E4M3),
+// or two parts of BF16, the second of which is held to at least `least`: where
+// nothing is masked, above zero, so that an infinity in V stays what it is.
+template <bool kE4M3>
+__device__ __forceinline__ void pack_weights(const float (&w)[8], uint32_t least, v4u &high, v4u &low) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kE4M3) {
+            high[i] = pack2h(w[2 * i], w[2 * i + 1]);
+        } else {
+            high[i] = cut2(w[2 * i], w[2 * i + 1]);
+            low[i] = at_least2(pack2b(w[2 * i] - __builtin_bit_cast(float, high[i] << 16),
+                                      w[2 * i + 1] - __builtin_bit_cast(float, high[i] & 0xFFFF0000u)),
+                               least);
+        }
+    }
+}
+
+template <bool kE4M3>
+__device__ __forceinline__ f4 product(const v4u &vt, const v4u &high, const v4u &low, f4 o) {
+    if (kE4M3) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, vt), __builtin_bit_cast(h8, high), o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, vt), __builtin_bit_cast(bf8, high), o, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, vt), __builtin_bit_cast(bf8, low), o, 0, 0, 0);
+}
+
+// Four 16-bit values of a row from each of four lanes in four: lane r of 16 gives
+// those of row r / 4 at `at`, and gets value r % 4 of the rows r / 4 gave, of all four.
+__device__ __forceinline__ v2u read_transposed(const uint8_t *at) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4 Lds;
+    return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at)));
+}
+
+// Values j and j + 1 of a lane's eight rows, each as an operand: V^T's rows.
+__device__ __forceinline__ void transpose(const uint32_t (&pair)[8], v4u (&vt)[2]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+        vt[e] = v4u{__builtin_amdgcn_perm(pair[1], pair[0], sel), __builtin_amdgcn_perm(pair[3], pair[2], sel),
+                    __builtin_amdgcn_perm(pair[5], pair[4], sel), __builtin_amdgcn_perm(pair[7], pair[6], sel)};
+    }
+}
+
+// What is no finite number in V is left out of a masked step's product, as 0
+// times it would reach rows that do not read it.  If there was any it is added
+// after all steps: a product of ones counts for each row how many of those that it
+// reads are infinities of either sign or NaN.  kStrided: a lane's values of V^T's
+// tile j are those of d = 16 j + r, otherwise of d = r kDim / 16 + j.
+template <int kDim, bool kE4M3, int kTiles, bool kStrided>
+__device__ __forceinline__ void add_counts(const TreeParams &p, const Work &work, const Rows &rows, const Row (&row)[kTiles], const uint8_t *vb,
+                                           const int32_t *s_page, const Chunk &c, int32_t p0, Running<kDim / 16> (&run)[kTiles]) {
+    constexpr int kPiece = kDim / 16;
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
+    const uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift, in_page = (1u << p.page_shift) - 1;
+    const uint32_t there = positions_there(p, c, s_page, p0, q);
+    v4u ones[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const uint32_t live = positions_read(p, work, rows, row[t], p0, q) & there;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ones[t][i] = (live >> (2 * i) & 1u ? 0x3F80u : 0u) | (live >> (2 * i + 1) & 1u ? 0x3F800000u : 0u);
+    }
+    const uint8_t *at[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t pos = static_cast<uint32_t>(min(p0 + 16 * (i / 4) + 4 * static_cast<int32_t>(q) + (i & 3), c.c1 - 1));
+        at[i] = vb + static_cast<uint64_t>(max(s_page[(pos >> p.page_shift) - first], 0)) * p.v.page + uint64_t{pos & in_page} * p.v.row;
+    }
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+        const uint32_t d = kStrided ? 16 * j + r : r * kPiece + j;
+        v4u kinds;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            kinds[i] = (there >> (2 * i) & 1u ? kind_at<kE4M3>(at[2 * i], d) : 0u) | (there >> (2 * i + 1) & 1u ? kind_at<kE4M3>(at[2 * i + 1], d) : 0u) << 16;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const f4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kinds), __builtin_bit_cast(bf8, ones[t]), f4{}, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) run[t].acc[j][k] += of_counts(n[k]);
+        }
+    }
+}
+
+constexpr int waves_for(int dim) { return dim == 64 ? 3 : dim == 128 ? 2 : 1; }
+
+// Few rows: the waves of a workgroup have all of a tile's rows (up to 32) each
+// and take the chunk's steps in turn, keys and values coming straight from
+// memory; they join in LDS.
 template <int kDim, bool kE4M3, int kTiles>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim, kTiles))))
-tree_kernel(TreeParams p) {
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim))))
+tree_few_kernel(TreeParams p) {
     constexpr int kPiece = kDim / 16;              // values of a V row in a lane; tiles of out^T
     constexpr int kKChunks = kDim / 32;            // matrix instructions over d
     constexpr int kKLoads = kE4M3 ? kDim / 64 : kKChunks;  // 16-byte loads of a K row in a lane
     constexpr int kVWords = kPiece * (kE4M3 ? 1 : 2) / 4;  // dwords of a V piece
     constexpr uint32_t kRows = 16 * kTiles;
-    __shared__ int32_t s_page[kMaxChunk / kMinPage + 1];
+    __shared__ int32_t s_page[kChunkPages];
     __shared__ float s_stat[kWaves][2][16];
     __shared__ __attribute__((aligned(16))) float s_out[kWaves][16][kDim + kPad];
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // workgroups go round the 8 XCDs: those of one chunk's tiles, which read the
-    // same keys and values, stay on one
-    const uint32_t turn = blockIdx.x / (8 * p.tiles), in = blockIdx.x - turn * 8 * p.tiles;
-    const uint32_t tile = in / 8;
-    uint32_t unit = turn * 8 + (in & 7u);
-    if (unit >= p.units) return;
-    const uint32_t h = unit % p.kv_heads;
-    unit /= p.kv_heads;
-    const uint32_t b = unit % p.batch, split = unit / p.batch;
-
-    // this tile's rows: row n is node n / group, head n % group
-    const uint32_t row0 = tile * kRows, rows = min(kRows, p.nodes * p.group - row0);
-    const int32_t count = min(max(p.counts ? p.counts[b] : INT32_MAX, 0), static_cast<int32_t>(p.nodes));
-    const int32_t len = static_cast<int32_t>(min(static_cast<uint32_t>(max(p.lens[b], 0)), p.positions));
-    const int32_t node_first = static_cast<int32_t>(row0 / p.group), node_last = static_cast<int32_t>((row0 + rows - 1) / p.group);
-    int32_t node[kTiles], start[kTiles];
-    bool have[kTiles];
-    int32_t lo = len, lo_max = 0;
+    const Work work = work_of(p);
+    if (work.none) return;
+    const Rows rows = rows_of(p, work, kRows);
+    Row row[kTiles];
+    int32_t lo = rows.len, lo_max = 0;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        const uint32_t n = row0 + 16 * t + r;
-        node[t] = static_cast<int32_t>(min(n, p.nodes * p.group - 1) / p.group);
-        have[t] = 16 * t + r < rows && node[t] < count;
-        start[t] = 0;
-        if (p.starts) start[t] = min(max(p.starts[b * p.starts_batch + static_cast<uint32_t>(node[t]) * p.starts_node], 0), len);
-        lo = have[t] ? min(lo, start[t]) : lo;
-        lo_max = have[t] ? max(lo_max, start[t]) : lo_max;
+        row[t] = row_of(p, work, rows, 16 * t + r);
+        lo = row[t].have ? min(lo, row[t].start) : lo;
+        lo_max = row[t].have ? max(lo_max, row[t].start) : lo_max;
     }
     if (p.starts) {
 #pragma unroll
@@ -148,135 +461,58 @@ tree_kernel(TreeParams p) {
     } else {
         lo = lo_max = 0;
     }
-    // the positions that any of these rows reads, and those that all read
-    const int32_t reach = min(count, p.mask ? count : node_last + 1);
-    const int32_t hi = node_first < count ? static_cast<int32_t>(min(static_cast<uint32_t>(len) + reach, p.positions)) : 0;
-    const int32_t all_hi = p.mask ? len : min(len + min(node_first + 1, count), hi);
-    const int32_t base = lo & ~static_cast<int32_t>(kStep - 1);
-    const uint32_t steps = hi > base ? (hi - base + kStep - 1) / kStep : 0;
-    const bool single = p.splits == 1;
-    const uint32_t chunks = min(p.splits, (steps + kWaves - 1) / kWaves);
-    const auto out_row = [&](uint32_t i) {  // of the tile's row i
-        const uint32_t n = row0 + i, nd = n / p.group;
-        return (uint64_t{b} * p.nodes + nd) * p.q_heads + h * p.group + (n - nd * p.group);
-    };
-    if (!single && split >= chunks) {  // nothing here: the join gives it no weight
-        for (uint32_t i = threadIdx.x; i < rows; i += 64 * kWaves) {
-            float *to = p.stats + 2 * (out_row(i) * p.splits + split);
-            to[0] = -INFINITY;
-            to[1] = 0;
-        }
+    Chunk c = chunk_of(p, work, rows, lo, lo_max);
+    if (c.none) {
+        no_chunk(p, work, rows);
         return;
     }
-    const uint32_t parts = max(chunks, 1u), each = steps / parts, more = steps - each * parts;
-    const int32_t c0 = base + static_cast<int32_t>((split * each + min(split, more)) * kStep);
-    const int32_t c1 = max(c0, min(c0 + static_cast<int32_t>((each + (split < more)) * kStep), hi));
-
-    // the chunk's pages; -1 masks
-    const uint32_t first = static_cast<uint32_t>(c0) >> p.page_shift;
-    const uint32_t n_pages = c1 > c0 ? (static_cast<uint32_t>(c1 - 1) >> p.page_shift) - first + 1 : 0;
-    const int32_t *table = p.table + b * p.table_stride + first;
-    int32_t masked_pages = 0;
-    for (uint32_t i = threadIdx.x; i < n_pages; i += 64 * kWaves) {
-        const int32_t e = table[i];
-        const bool ok = e >= 0 && static_cast<uint64_t>(e) < p.n_pages;
-        s_page[i] = ok ? e : -1;
-        masked_pages |= !ok;
-    }
+    const int32_t end = c.c1;
+    c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
+    const int32_t masked_pages = load_pages(p, work, c, s_page);
 
     // Q^T: row r of each tile, d in the order in which K's loads give them.  A
-    // negative scale turns q around, so that the largest product is the largest score.
-    const float signed_scale = kE4M3 ? p.scale * p.k.scale[h] : p.scale;
-    const float scale = fabsf(signed_scale);
+    // negative scale turns q around, so that the largest product is the largest
+    // score, and one of zero makes q zero.
+    const float signed_scale = kE4M3 ? p.scale * p.k.scale[work.h] : p.scale;
+    const float scale = signed_scale == 0 ? 1.0f : fabsf(signed_scale);
     const uint32_t turned = signed_scale < 0 ? 0x80008000u : 0;
     bf8 qf[kTiles][kKChunks];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        const uint32_t n = min(row0 + 16 * t + r, p.nodes * p.group - 1);
-        const uint16_t *qp = p.q + b * p.q_batch + static_cast<uint32_t>(node[t]) * p.q_node +
-                             (h * p.group + (n - static_cast<uint32_t>(node[t]) * p.group)) * p.q_head;
+        const uint32_t n = min(rows.row0 + 16 * t + r, p.nodes * p.group - 1);
+        const uint16_t *qp = p.q + work.b * p.q_batch + static_cast<uint32_t>(row[t].node) * p.q_node +
+                             (work.h * p.group + (n - static_cast<uint32_t>(row[t].node) * p.group)) * p.q_head;
 #pragma unroll
         for (int i = 0; i < kKChunks; ++i) {
             const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
-            v4u w = have[t] ? load8(qp + d) : v4u{0, 0, 0, 0};
+            v4u w = row[t].have && signed_scale != 0 ? load8(qp + d) : v4u{0, 0, 0, 0};
             w ^= turned;
             qf[t][i] = __builtin_bit_cast(bf8, w);
         }
     }
-    const uint8_t *kb = p.k.base + h * p.k.head, *vb = p.v.base + h * p.v.head;
+    const uint8_t *kb = p.k.base + work.h * p.k.head, *vb = p.v.base + work.h * p.v.head;
     const uint32_t in_page = (1u << p.page_shift) - 1;
-    const bool holes = __syncthreads_or(masked_pages);  // and the pages are there
+    uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift;
+    bool holes = __syncthreads_or(masked_pages);  // and the pages are there
 
     // K rows of a step: lane r has position r of each half
     v4u kr[2][kKLoads];
     auto load_k = [&](int32_t p0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t pos = static_cast<uint32_t>(min(p0 + 16 * t + static_cast<int32_t>(r), c1 - 1));
+            const uint32_t pos = static_cast<uint32_t>(min(p0 + 16 * t + static_cast<int32_t>(r), c.c1 - 1));
             const int32_t page = max(s_page[(pos >> p.page_shift) - first], 0);
-            const uint8_t *row = kb + static_cast<uint64_t>(page) * p.k.page + uint64_t{pos & in_page} * p.k.row + 16 * q;
+            const uint8_t *at = kb + static_cast<uint64_t>(page) * p.k.page + uint64_t{pos & in_page} * p.k.row + 16 * q;
 #pragma unroll
-            for (int i = 0; i < kKLoads; ++i) kr[t][i] = *reinterpret_cast<const v4u *>(row + 64 * i);
+            for (int i = 0; i < kKLoads; ++i) kr[t][i] = *reinterpret_cast<const v4u *>(at + 64 * i);
         }
     };
-    // V rows of a step: positions 4 q + 0..3 of each half (of one page: pages
-    // hold multiples of 8)
-    typedef uint32_t VRow __attribute__((ext_vector_type(kVWords)));
-    typedef VRow VRowInMemory __attribute__((aligned(4)));
-    VRow vr[8];
-    auto load_v = [&](int32_t p0) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int32_t pos0 = p0 + 16 * t + 4 * static_cast<int32_t>(q);
-            const int32_t page = s_page[(static_cast<uint32_t>(min(pos0, c1 - 1)) >> p.page_shift) - first];
-            const uint8_t *at_page = vb + static_cast<uint64_t>(max(page, 0)) * p.v.page + r * (kVWords * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t at = static_cast<uint32_t>(min(pos0 + i, c1 - 1));
-                vr[4 * t + i] = *reinterpret_cast<const VRowInMemory *>(at_page + uint64_t{at & in_page} * p.v.row);
-            }
-        }
-    };
-    // Which of a lane's eight positions lie in the chunk, past every start and in pages of the cache.
-    auto positions_there = [&](int32_t p0) {
-        uint32_t there = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int32_t pos0 = p0 + 16 * t + 4 * static_cast<int32_t>(q);
-            const bool page = s_page[(static_cast<uint32_t>(min(pos0, c1 - 1)) >> p.page_shift) - first] >= 0;
-            there |= page ? (bits_between(lo - pos0, c1 - pos0) & 15u) << (4 * t) : 0u;
-        }
-        return there;
-    };
-    // Which of them row r of a tile reads.
-    auto positions_read = [&](int t, int32_t p0) {
-        uint32_t live = bits_between(start[t] - p0, len - p0);
-        const int32_t a0 = p0 - len;  // the node at p0
-        if (a0 + static_cast<int32_t>(kStep) > 0) {
-            if (!p.mask) {
-                live |= bits_between(-a0, min(node[t] + 1, count) - a0);
-            } else if (a0 < count) {
-                const int64_t *words = p.mask + b * p.mask_batch + static_cast<uint32_t>(node[t]) * p.mask_node;
-                const uint32_t from = static_cast<uint32_t>(max(a0, 0));
-                const uint32_t w = from / 64, shift = from % 64;
-                uint64_t m = static_cast<uint64_t>(words[w]) >> shift;
-                if (shift > 32 && 64 * (w + 1) < p.nodes) m |= static_cast<uint64_t>(words[w + 1]) << (64 - shift);
-                live |= static_cast<uint32_t>(a0 < 0 ? m << -a0 : m) & bits_between(-a0, count - a0);
-            }
-        }
-        return ((live >> (4 * q)) & 15u) | (((live >> (16 + 4 * q)) & 15u) << 4);
-    };
+    typename Piece<kVWords>::Value vr[8];
+    auto load_v = [&](int32_t p0) { load_v_rows<kVWords>(p, c, s_page, vb, p0, r, q, vr); };
 
-    float ref[kTiles], l[kTiles];  // reference of a row's weights in log2 units, their sum over this lane's positions
-    f4 acc[kTiles][kPiece] = {};
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-        ref[t] = -INFINITY;
-        l[t] = 0;
-    }
-
-    auto step = [&](int32_t p0, int32_t next, auto masked_) {
-        constexpr bool kMasked = decltype(masked_)::value;
+    Running<kPiece> run[kTiles];
+    uint32_t odd = 0;  // whether some value of V was left out of masked steps
+    auto step = [&](int32_t p0, int32_t next) {
         f4 s[kTiles][2] = {};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -293,12 +529,14 @@ tree_kernel(TreeParams p) {
             }
         load_k(next);
 
-        uint32_t there = 0xFF, odd = 0;  // odd: some value of V is no finite number
-        if (kMasked) {
-            there = positions_there(p0);
+        const bool masked = masked_at(c, holes, p0, kStep);
+        if (__builtin_expect(masked, false)) {
+            const uint32_t there = positions_there(p, c, s_page, p0, q);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) mask_scores(s[t], positions_read(p, work, rows, row[t], p0, q) & there);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                vr[i] = there >> i & 1u ? vr[i] : VRow(0);
+                if (!(there >> i & 1u)) vr[i] = 0;
 #pragma unroll
                 for (int w = 0; w < kVWords; ++w) {
                     const uint32_t n = not_finite<kE4M3>(vr[i][w]);
@@ -306,57 +544,16 @@ tree_kernel(TreeParams p) {
                     vr[i][w] &= ~n;
                 }
             }
-            odd = __any(odd != 0);
         }
-        v4u high[kTiles], low[kTiles];  // the weights as the product takes them
+        v4u high[kTiles], low[kTiles];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-            uint32_t live = 0xFF;
-            if (kMasked) {
-                live = positions_read(t, p0) & there;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[t][i / 4][i & 3] = live >> i & 1u ? s[t][i / 4][i & 3] : -INFINITY;
-            }
-            float top = s[t][0][0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[t][i / 4][i & 3]);
-            // the reference follows a maximum that has left it behind
-            const bool behind = top > -INFINITY && !(top * scale <= ref[t] + kSlack);
-            if (__any(behind)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float to = top > -INFINITY ? fmaxf(ref[t], top * scale) : ref[t];
-                const float fade = to == ref[t] ? 1.0f : exp2_(ref[t] - to);
-                ref[t] = to;
-                l[t] *= fade;
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[t][j][c] *= fade;
-            }
-            const float from = ref[t] == -INFINITY ? 0.0f : ref[t];
             float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = exp2_(fmaf(s[t][i / 4][i & 3], scale, -from));
-                if (kMasked) w[i] = live >> i & 1u ? w[i] : 0.0f;
-                l[t] += w[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (kE4M3) {
-                    high[t][i] = pack2h(w[2 * i], w[2 * i + 1]);
-                } else {
-                    high[t][i] = cut2(w[2 * i], w[2 * i + 1]);
-                    low[t][i] = pack2(w[2 * i] - __builtin_bit_cast(float, high[t][i] << 16),
-                                      w[2 * i + 1] - __builtin_bit_cast(float, high[t][i] & 0xFFFF0000u));
-                    if (!kMasked) low[t][i] = at_least2(low[t][i], kLeastPart);
-                }
-            }
+            run[t].weights(s[t], scale, w);
+            pack_weights<kE4M3>(w, masked ? 0u : kLeastPart, high[t], low[t]);
         }
 #pragma unroll
         for (int j = 0; j < kPiece; j += 2) {
-            // values j and j + 1 of the eight rows
             uint32_t pair[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -365,103 +562,63 @@ tree_kernel(TreeParams p) {
                 else
                     pair[i] = vr[i][kE4M3 ? 0 : j / 2];
             }
+            v4u vt[2];
+            transpose(pair, vt);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t sel = e ? 0x07060302u : 0x05040100u;
-                const v4u a = {__builtin_amdgcn_perm(pair[1], pair[0], sel), __builtin_amdgcn_perm(pair[3], pair[2], sel),
-                               __builtin_amdgcn_perm(pair[5], pair[4], sel), __builtin_amdgcn_perm(pair[7], pair[6], sel)};
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    f4 o = acc[t][j + e];
-                    if (kE4M3) {
-                        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, high[t]), o, 0, 0, 0);
-                    } else {
-                        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, high[t]), o, 0, 0, 0);
-                        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, low[t]), o, 0, 0, 0);
-                    }
-                    acc[t][j + e] = o;
-                }
-            }
-        }
-        if (kMasked && odd) {
-            // What is no finite number was left out above, as 0 times it would reach
-            // rows that do not read it.  A product of ones counts for each row how many
-            // of those that it reads are infinities of either sign or NaN.
-            load_v(p0);
-            uint32_t ones[kTiles][4];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const uint32_t live = positions_read(t, p0) & there;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ones[t][i] = (live >> (2 * i) & 1u ? 0x3F80u : 0u) | (live >> (2 * i + 1) & 1u ? 0x3F800000u : 0u);
-            }
-#pragma unroll
-            for (int j = 0; j < kPiece; j += 2) {
-                uint32_t pair[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) pair[i] = there >> i & 1u ? kind2<kE4M3>(vr[i], j) : 0u;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t sel = e ? 0x07060302u : 0x05040100u;
-                    const bf8 a = __builtin_bit_cast(
-                        bf8, v4u{__builtin_amdgcn_perm(pair[1], pair[0], sel), __builtin_amdgcn_perm(pair[3], pair[2], sel),
-                                 __builtin_amdgcn_perm(pair[5], pair[4], sel), __builtin_amdgcn_perm(pair[7], pair[6], sel)});
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        const bf8 w = __builtin_bit_cast(bf8, v4u{ones[t][0], ones[t][1], ones[t][2], ones[t][3]});
-                        const f4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, f4{}, 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[t][j + e][c] += of_counts(n[c]);
-                    }
-                }
-            }
+                for (int t = 0; t < kTiles; ++t) run[t].acc[j + e] = product<kE4M3>(vt[e], high[t], low[t], run[t].acc[j + e]);
         }
         load_v(next);
     };
-    const auto masked_at = [&](int32_t p0) { return holes || p0 < lo_max || p0 + static_cast<int32_t>(kStep) > min(all_hi, c1); };
-    int32_t p0 = c0 + static_cast<int32_t>(wave * kStep);
-    if (p0 < c1) {
-        load_k(p0);
-        load_v(p0);
-        // the last step loads its chunk's last row in vain
-        for (; p0 < c1; p0 += kWaves * kStep) {
-            if (masked_at(p0))
-                step(p0, p0 + kWaves * kStep, std::true_type());
-            else
-                step(p0, p0 + kWaves * kStep, std::false_type());
+    for (;;) {  // once for the pages that LDS holds
+        const int32_t wave0 = c.c0 + static_cast<int32_t>(wave * kStep);
+        if (wave0 < c.c1) {
+            load_k(wave0);
+            load_v(wave0);
+            // the last step loads its chunk's last row in vain
+            for (int32_t p0 = wave0; p0 < c.c1; p0 += kWaves * kStep) step(p0, p0 + kWaves * kStep);
+            if (__builtin_expect(__any(odd != 0), 0))
+                for (int32_t p0 = wave0; p0 < c.c1; p0 += kWaves * kStep)
+                    if (masked_at(c, holes, p0, kStep)) add_counts<kDim, kE4M3, kTiles, false>(p, work, rows, row, vb, s_page, c, p0, run);
+            odd = 0;
         }
+        if (c.c1 >= end) break;
+        __syncthreads();
+        c.c0 = c.c1;
+        c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
+        first = static_cast<uint32_t>(c.c0) >> p.page_shift;
+        holes = __syncthreads_or(load_pages(p, work, c, s_page));
     }
 
     // join the waves, a tile at a time
-    const float v_scale = kE4M3 ? p.v.scale[h] : 1.0f;
+    const float v_scale = kE4M3 ? p.v.scale[work.h] : 1.0f;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        if (16u * t >= rows) break;
-        float sum = l[t];
+        if (16u * t >= rows.rows) break;
+        float sum = run[t].sum;
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (t) __syncthreads();  // the last tile has been read
         if (q == 0) {
-            s_stat[wave][0][r] = ref[t];
+            s_stat[wave][0][r] = run[t].ref;
             s_stat[wave][1][r] = sum;
         }
         // acc[j][c]: d = (4 q + c) * kPiece + j
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int j = 0; j < kPiece; j += 4)
-                *reinterpret_cast<f4 *>(&s_out[wave][r][(4 * q + c) * kPiece + j]) =
-                    f4{acc[t][j][c], acc[t][j + 1][c], acc[t][j + 2][c], acc[t][j + 3][c]};
+                *reinterpret_cast<f4 *>(&s_out[wave][r][(4 * q + k) * kPiece + j]) =
+                    f4{run[t].acc[j][k], run[t].acc[j + 1][k], run[t].acc[j + 2][k], run[t].acc[j + 3][k]};
         __syncthreads();
         constexpr uint32_t kQuads = kDim / 4;
-        for (uint32_t i = threadIdx.x; i < min(16u, rows - 16 * t) * kQuads; i += 64 * kWaves) {
+        for (uint32_t i = threadIdx.x; i < min(16u, rows.rows - 16 * t) * kQuads; i += 64 * kWaves) {
             const uint32_t g = i / kQuads, d = i % kQuads * 4;
-            const bool there = static_cast<int32_t>((row0 + 16 * t + g) / p.group) < count;
+            const bool there = static_cast<int32_t>((rows.row0 + 16 * t + g) / p.group) < rows.count;
             float top = -INFINITY;
 #pragma unroll
             for (uint32_t k = 0; k < kWaves; ++k) top = fmaxf(top, s_stat[k][0][g]);
-            if (!there) top = -INFINITY;
             const float from = top == -INFINITY ? 0.0f : top;
             float total = 0;
             f4 o = {};
@@ -471,28 +628,295 @@ tree_kernel(TreeParams p) {
                 total += s_stat[k][1][g] * f;
                 o += *reinterpret_cast<const f4 *>(&s_out[k][g][d]) * f;
             }
-            if (!there) {
-                total = 0;
-                o = f4{};
-            }
-            o *= v_scale;
-            const uint64_t row = out_row(16 * t + g);
-            if (single) {
-                if (total == 0) o = f4{};
-                const float inv = total == 0 ? 0.0f : 1.0f / total;
-                v2u to;
-                to.x = pack2(o[0] * inv, o[1] * inv);
-                to.y = pack2(o[2] * inv, o[3] * inv);
-                *reinterpret_cast<v2u *>(p.out + row * kDim + d) = to;
-                if (d == 0 && p.lse) p.lse[row] = (from + __builtin_amdgcn_logf(total)) * kLn2;
-            } else {
-                const uint64_t at = row * p.splits + split;
-                *reinterpret_cast<f4 *>(p.part + at * kDim + d) = o;
-                if (d == 0) {
-                    p.stats[2 * at] = top;
-                    p.stats[2 * at + 1] = total;
+            write_out<kDim>(p, work.split, out_row(p, work, rows, 16 * t + g), d, there, top, total, o * v_scale);
+        }
+    }
+}
+
+// Many rows: keys and values go through LDS, once for a workgroup,
+// two stages in turn.  kGroups of the waves share a wave's 16 kTiles rows and take
+// a stage's steps in turn; they join in LDS.  E4M3 becomes BF16 (keys) and FP16
+// (values) on its way to LDS.  A row's 16-byte pieces lie there in an order of its
+// own, so that lanes that read a piece of different rows do not meet in a bank: K
+// is read row by row, V across four rows and two pieces, which the hardware's
+// transposing reads turn into V^T.
+constexpr uint32_t kManyWaves = 4;
+
+template <int kDim>
+constexpr uint32_t kStagePositions = kDim == 256 ? 32 : 64;
+
+template <int kDim>
+__device__ __forceinline__ uint32_t k_place(uint32_t row, uint32_t piece) {
+    return row * 2 * kDim + 16 * (piece ^ (kDim == 64 ? row & 7u : row & 15u));
+}
+
+template <int kDim>
+__device__ __forceinline__ uint32_t v_place(uint32_t row, uint32_t piece) {
+    return row * 2 * kDim + 16 * (piece ^ (kDim == 64 ? row & 6u : 2 * (row & 7u)));
+}
+
+template <int kDim, bool kE4M3, int kTiles, uint32_t kGroups>
+__global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParams p) {
+    constexpr int kPiece = kDim / 16, kKChunks = kDim / 32;
+    constexpr uint32_t kThreads = 64 * kManyWaves, kRows = 16 * kTiles * kManyWaves / kGroups, kStage = kStagePositions<kDim>;
+    constexpr uint32_t kRowLoads = kDim * (kE4M3 ? 1 : 2) / 16;   // 16-byte loads of a row
+    constexpr int kLoads = kStage * kRowLoads / kThreads;         // of a lane for a stage's K, and V
+    constexpr uint32_t kBytes = kStage * 2 * kDim;                // of a stage's K, and V
+    static_assert(kStage % (kStep * kGroups) == 0 && kManyWaves * kTiles * kPiece * 1024 <= 4 * kBytes, "stages hold what the waves join");
+    __shared__ int32_t s_page[kChunkPages];
+    __shared__ uint64_t s_k_at[kChunkPages], s_v_at[kChunkPages];  // the pages' offsets
+    __shared__ int32_t s_reads[2][kManyWaves];
+    __shared__ float s_stat[kManyWaves][kTiles][2][16];
+    __shared__ __attribute__((aligned(16))) uint8_t s_stage[4 * kBytes];  // K and V of two stages
+
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t group = wave % kGroups;
+    const Work work = work_of(p);
+    if (work.none) return;
+    const Rows rows = rows_of(p, work, kRows);
+    const uint32_t wave_row = wave / kGroups * 16 * kTiles;
+    const bool active = wave_row < rows.rows;  // others fetch and wait
+    Row row[kTiles];
+    int32_t lo = rows.len, lo_max = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        row[t] = row_of(p, work, rows, wave_row + 16 * t + r);
+        lo = row[t].have ? min(lo, row[t].start) : lo;
+        lo_max = row[t].have ? max(lo_max, row[t].start) : lo_max;
+    }
+    if (p.starts) {
+#pragma unroll
+        for (int i = 1; i < 16; i <<= 1) {
+            lo = min(lo, __shfl_xor(lo, i));
+            lo_max = max(lo_max, __shfl_xor(lo_max, i));
+        }
+        if (lane == 0) {
+            s_reads[0][wave] = lo;
+            s_reads[1][wave] = lo_max;
+        }
+        __syncthreads();
+        lo = rows.len;
+        lo_max = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < kManyWaves; ++w) {
+            lo = min(lo, s_reads[0][w]);
+            lo_max = max(lo_max, s_reads[1][w]);
+        }
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+    } else {
+        lo = lo_max = 0;
+    }
+    Chunk c = chunk_of(p, work, rows, lo, lo_max);
+    if (c.none) {
+        no_chunk(p, work, rows);
+        return;
+    }
+    const int32_t end = c.c1;
+    c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
+    auto load_offsets = [&] {
+        const int32_t masked = load_pages(p, work, c, s_page);
+        for (uint32_t i = threadIdx.x; i < pages_of(p, c); i += kThreads) {  // as in load_pages: the same lane
+            const uint64_t page = static_cast<uint64_t>(max(s_page[i], 0));
+            s_k_at[i] = page * p.k.page;
+            s_v_at[i] = page * p.v.page;
+        }
+        return masked;
+    };
+    const int32_t masked_pages = load_offsets();
+
+    const float signed_scale = kE4M3 ? p.scale * p.k.scale[work.h] : p.scale;
+    const float scale = signed_scale == 0 ? 1.0f : fabsf(signed_scale);
+    const uint32_t turned = signed_scale < 0 ? 0x80008000u : 0;
+    bf8 qf[kTiles][kKChunks];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const uint32_t n = min(rows.row0 + wave_row + 16 * t + r, p.nodes * p.group - 1);
+        const uint16_t *qp = p.q + work.b * p.q_batch + static_cast<uint32_t>(row[t].node) * p.q_node +
+                             (work.h * p.group + (n - static_cast<uint32_t>(row[t].node) * p.group)) * p.q_head;
+#pragma unroll
+        for (int i = 0; i < kKChunks; ++i) {
+            v4u w = row[t].have && signed_scale != 0 ? load8(qp + 32 * i + 8 * q) : v4u{0, 0, 0, 0};
+            w ^= turned;
+            qf[t][i] = __builtin_bit_cast(bf8, w);
+        }
+    }
+    const uint8_t *kb = p.k.base + work.h * p.k.head, *vb = p.v.base + work.h * p.v.head;
+    const uint32_t in_page = (1u << p.page_shift) - 1;
+    uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift;
+    bool holes = __syncthreads_or(masked_pages);  // and the pages are there
+
+    // a stage's pieces, a lane's in registers on their way
+    const uint32_t load_row = threadIdx.x / kRowLoads, load_piece = threadIdx.x % kRowLoads;
+    constexpr uint32_t kRowStep = kThreads / kRowLoads;
+    const uint8_t *k_piece = kb + 16 * load_piece, *v_piece = vb + 16 * load_piece;
+    const uint32_t k_row = static_cast<uint32_t>(p.k.row), v_row = static_cast<uint32_t>(p.v.row);
+    v4u kr[kLoads], vr[kLoads];
+    auto load = [&](int32_t p0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t pos = static_cast<uint32_t>(min(p0 + static_cast<int32_t>(load_row + i * kRowStep), c.c1 - 1));
+            const uint32_t page = (pos >> p.page_shift) - first, at = pos & in_page;
+            kr[i] = *reinterpret_cast<const v4u *>(k_piece + s_k_at[page] + uint64_t{at} * k_row);
+            vr[i] = *reinterpret_cast<const v4u *>(v_piece + s_v_at[page] + uint64_t{at} * v_row);
+        }
+    };
+    uint32_t odd = 0;  // whether some value of V was left out of masked stages
+    auto store = [&](int32_t p0, uint8_t *to) {
+        if (__builtin_expect(masked_at(c, holes, p0, kStage), false)) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int32_t pos = p0 + static_cast<int32_t>(load_row + i * kRowStep);
+                const bool there = pos >= c.lo && pos < c.c1 && s_page[(static_cast<uint32_t>(min(pos, c.c1 - 1)) >> p.page_shift) - first] >= 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    if (!there) vr[i][w] = 0;
+                    const uint32_t n = not_finite<kE4M3>(vr[i][w]);
+                    odd |= n;
+                    vr[i][w] &= ~n;
                 }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = load_row + i * kRowStep;
+            if (kE4M3) {
+#pragma unroll
+                for (uint32_t e = 0; e < 2; ++e) {
+                    const uint32_t a = kr[i][2 * e], b = kr[i][2 * e + 1], x = vr[i][2 * e], y = vr[i][2 * e + 1];
+                    *reinterpret_cast<v4u *>(to + k_place<kDim>(at, 2 * load_piece + e)) = from_e4m3x8(a, b);
+                    *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, 2 * load_piece + e)) =
+                        v4u{half_from_e4m3<false>(x), half_from_e4m3<true>(x), half_from_e4m3<false>(y), half_from_e4m3<true>(y)};
+                }
+            } else {
+                *reinterpret_cast<v4u *>(to + k_place<kDim>(at, load_piece)) = kr[i];
+                *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, load_piece)) = vr[i];
+            }
+        }
+    };
+
+    Running<kPiece> run[kTiles];
+    auto step = [&](int32_t p0, const uint8_t *stage, uint32_t row0, bool masked) {  // positions p0.., rows row0.. of the stage
+        f4 s[kTiles][2] = {};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < kKChunks; ++i) {
+                const v4u kw = *reinterpret_cast<const v4u *>(stage + row0 * 2 * kDim + k_place<kDim>(16 * u + r, 4 * i + q));
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+                    s[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[t][i], s[t][u], 0, 0, 0);
+            }
+        if (__builtin_expect(masked, false)) {
+            const uint32_t there = positions_there(p, c, s_page, p0, q);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) mask_scores(s[t], positions_read(p, work, rows, row[t], p0, q) & there);
+        }
+        v4u high[kTiles], low[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            float w[8];
+            run[t].weights(s[t], scale, w);
+            pack_weights<kE4M3>(w, masked ? 0u : kLeastPart, high[t], low[t]);
+        }
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+            // lane r of four rows gives four values of row r / 4 and gets value r of all four
+            v2u half[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                half[u] = read_transposed(stage + kBytes + row0 * 2 * kDim + v_place<kDim>(16 * u + 4 * q + r / 4, 2 * j + (r & 3u) / 2) + 8 * (r & 1u));
+            const v4u vt = {half[0].x, half[0].y, half[1].x, half[1].y};
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) run[t].acc[j] = product<kE4M3>(vt, high[t], low[t], run[t].acc[j]);
+        }
+    };
+    while (c.c0 < c.c1) {  // once for the pages that LDS holds
+        load(c.c0);
+        store(c.c0, s_stage);
+        load(c.c0 + static_cast<int32_t>(kStage));  // past the end the last row again
+        __syncthreads();
+        uint32_t stage = 0;
+        for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage, stage ^= 2 * kBytes) {
+            if (active) {
+                const bool masked = masked_at(c, holes, p0, kStage);
+#pragma unroll
+                for (uint32_t at = 0; at < kStage; at += kStep * kGroups) {
+                    const int32_t from = p0 + static_cast<int32_t>(at + kStep * group);
+                    if (from >= c.c1) break;
+                    step(from, s_stage + stage, at + kStep * group, masked);
+                }
+            }
+            store(p0 + static_cast<int32_t>(kStage), s_stage + (stage ^ 2 * kBytes));
+            load(p0 + static_cast<int32_t>(2 * kStage));
+            __syncthreads();
+        }
+        if (__builtin_expect(__syncthreads_or(odd != 0), 0))
+            for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage)
+                if (masked_at(c, holes, p0, kStage))
+                    for (uint32_t at = kStep * group; at < kStage && p0 + static_cast<int32_t>(at) < c.c1; at += kStep * kGroups)
+                        add_counts<kDim, kE4M3, kTiles, true>(p, work, rows, row, vb, s_page, c, p0 + static_cast<int32_t>(at), run);
+        if (c.c1 >= end) break;
+        __syncthreads();
+        odd = 0;
+        c.c0 = c.c1;
+        c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
+        first = static_cast<uint32_t>(c.c0) >> p.page_shift;
+        holes = __syncthreads_or(load_offsets());
+    }
+
+    const float v_scale = kE4M3 ? p.v.scale[work.h] : 1.0f;
+    f4 *parts = reinterpret_cast<f4 *>(s_stage) + wave / kGroups * kGroups * kTiles * kPiece * 64 + lane;
+    if (kGroups > 1) {
+        // every wave of a row group puts what it has side by side, and takes a share of all
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            float sum = run[t].sum;
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (q == 0) {
+                s_stat[wave][t][0][r] = run[t].ref;
+                s_stat[wave][t][1][r] = sum;
+            }
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) parts[((group * kTiles + t) * kPiece + j) * 64] = run[t].acc[j];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const uint32_t i = wave_row + 16 * t + r;
+        if (i >= rows.rows) continue;
+        const uint64_t to = out_row(p, work, rows, i);
+        float top = run[t].ref, total = 0, fade[kGroups];
+        if (kGroups == 1) {
+            total = run[t].sum;
+            total += __shfl_xor(total, 16);
+            total += __shfl_xor(total, 32);
+        } else {
+            const uint32_t wave0 = wave / kGroups * kGroups;
+            top = -INFINITY;
+#pragma unroll
+            for (uint32_t g = 0; g < kGroups; ++g) top = fmaxf(top, s_stat[wave0 + g][t][0][r]);
+            const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (uint32_t g = 0; g < kGroups; ++g) {
+                fade[g] = exp2_(s_stat[wave0 + g][t][0][r] - from);
+                total += s_stat[wave0 + g][t][1][r] * fade[g];
+            }
+        }
+        // acc[j][k]: d = 16 j + 4 q + k
+#pragma unroll
+        for (int n = 0; n < kPiece / static_cast<int>(kGroups); ++n) {
+            const int j = n * kGroups;
+            f4 o = run[t].acc[j];
+            if (kGroups > 1) {
+                o = f4{};
+#pragma unroll
+                for (uint32_t g = 0; g < kGroups; ++g) o += parts[((g * kTiles + t) * kPiece + j + group) * 64] * fade[g];
+            }
+            write_out<kDim>(p, work.split, to, 16 * (j + (kGroups > 1 ? group : 0)) + 4 * q, row[t].have, top, total, o * v_scale);
         }
     }
 }
@@ -523,8 +947,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
     if (total == 0) o = f4{};
     const float inv = total == 0 ? 0.0f : 1.0f / total;
     v2u to;
-    to.x = pack2(o[0] * inv, o[1] * inv);
-    to.y = pack2(o[2] * inv, o[3] * inv);
+    to.x = pack2b(o[0] * inv, o[1] * inv);
+    to.y = pack2b(o[2] * inv, o[3] * inv);
     *reinterpret_cast<v2u *>(p.out + row * kDim + 4 * d) = to;
     if (d == 0 && p.lse) p.lse[row] = (from + __builtin_amdgcn_logf(total)) * kLn2;
 }
@@ -532,21 +956,20 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
 // ---- Host ------------------------------------------------------------------
 
 struct Shape {
-    uint32_t row_tiles;  // of 16 rows in a workgroup
+    uint32_t rows;  // of a workgroup: 16 and 32 in tree_few_kernel, more in tree_many_kernel
     uint32_t tiles, splits;
 };
-
-constexpr uint64_t kWantGroups = 2 * kComputeUnits;
 
 Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads, uint32_t dim, uint64_t positions) {
     const uint64_t rows = nodes * group;
     Shape s;
-    s.row_tiles = rows <= 16 ? 1 : rows <= 32 || dim == 256 ? 2 : 4;
-    s.tiles = static_cast<uint32_t>((rows + 16 * s.row_tiles - 1) / (16 * s.row_tiles));
-    const uint64_t units = batch * kv_heads * s.tiles;
-    const uint64_t want = (kWantGroups + units - 1) / std::max<uint64_t>(units, 1);
-    const uint64_t most = (positions + kMinChunk - 1) / kMinChunk, least = (positions + kMaxChunk - 1) / kMaxChunk;
-    s.splits = static_cast<uint32_t>(positions <= 2 * kMinChunk ? 1 : std::max(std::min(want, most), least));
+    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (s.rows == 64 && dim < 256 && batch * kv_heads * ((rows + 127) / 128) >= kComputeUnits) s.rows = 128;
+    s.tiles = static_cast<uint32_t>((rows + s.rows - 1) / s.rows);
+    const uint64_t units = batch * kv_heads * s.tiles, wanted = 2 * kComputeUnits;
+    const uint64_t want = (wanted + units - 1) / std::max<uint64_t>(units, 1);
+    const uint64_t most = (positions + kMinChunk - 1) / kMinChunk;
+    s.splits = static_cast<uint32_t>(positions <= 2 * kMinChunk ? 1 : std::min(want, most));
     return s;
 }
 
@@ -570,11 +993,15 @@ uint64_t workspace_of(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t
 }
 
 template <int kDim>
-auto kernel_of(bool e4m3, uint32_t row_tiles) {
-    if constexpr (kDim < 256)
-        if (row_tiles == 4) return e4m3 ? tree_kernel<kDim, true, 4> : tree_kernel<kDim, false, 4>;
-    if (row_tiles == 1) return e4m3 ? tree_kernel<kDim, true, 1> : tree_kernel<kDim, false, 1>;
-    return e4m3 ? tree_kernel<kDim, true, 2> : tree_kernel<kDim, false, 2>;
+auto kernel_of(bool e4m3, uint32_t rows) {
+    if constexpr (kDim == 256) {
+        if (rows == 64) return e4m3 ? tree_many_kernel<kDim, true, 1, 1> : tree_many_kernel<kDim, false, 1, 1>;
+    } else {
+        if (rows == 128) return e4m3 ? tree_many_kernel<kDim, true, 2, 1> : tree_many_kernel<kDim, false, 2, 1>;
+        if (rows == 64) return e4m3 ? tree_many_kernel<kDim, true, 2, 2> : tree_many_kernel<kDim, false, 2, 2>;
+    }
+    if (rows == 32) return e4m3 ? tree_few_kernel<kDim, true, 2> : tree_few_kernel<kDim, false, 2>;
+    return e4m3 ? tree_few_kernel<kDim, true, 1> : tree_few_kernel<kDim, false, 1>;
 }
 
 df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const int32_t *table, uint64_t table_stride,
@@ -600,6 +1027,7 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     TreeParams p;
     p.k = k_of(c);
     p.v = v_of(c);
+    if (p.k.row > 0xFFFFFFFFu || p.v.row > 0xFFFFFFFFu) return DF11_E_INVALID_ARG;  // the kernels multiply by them in 32 bits
     p.q = t->q;
     p.table = table;
     p.lens = lens;
@@ -637,10 +1065,10 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     p.stats = s.splits > 1 ? p.part + rows * s.splits * c->head_dim : nullptr;
     const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    auto fn = c->head_dim == 64    ? kernel_of<64>(e4m3, s.row_tiles)
-              : c->head_dim == 128 ? kernel_of<128>(e4m3, s.row_tiles)
-                                   : kernel_of<256>(e4m3, s.row_tiles);
-    hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(t->batch, c->kv_heads, s)), 64 * kWaves, 0, st, p);
+    auto fn = c->head_dim == 64    ? kernel_of<64>(e4m3, s.rows)
+              : c->head_dim == 128 ? kernel_of<128>(e4m3, s.rows)
+                                   : kernel_of<256>(e4m3, s.rows);
+    hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(t->batch, c->kv_heads, s)), 64 * (s.rows > 32 ? kManyWaves : kWaves), 0, st, p);
     if (err == hipSuccess && s.splits > 1) {
         const uint64_t per = kJoinThreads / (c->head_dim / 4);
         err = launch(c->head_dim == 64    ? tree_join_kernel<64>
