@@ -302,11 +302,8 @@ struct Running {
     float ref = -INFINITY, sum = 0;  // sum: over this lane's positions
     f4 acc[kPiece] = {};
 
-    // Turns a step's scores, -infinity where a position is masked, into weights.  scale > 0.
-    __device__ __forceinline__ void weights(const f4 (&s)[2], float scale, float (&w)[8]) {
-        float top = s[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i & 3]);
+    // Takes the largest of some scores (of this lane's; scale > 0) into the reference.
+    __device__ __forceinline__ void follow(float top, float scale) {
         const bool behind = top > -INFINITY && !(top * scale <= ref + kSlack);
         if (__builtin_expect(__any(behind), 0)) {
             top = fmaxf(top, __shfl_xor(top, 16));
@@ -320,6 +317,10 @@ struct Running {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[j][c] *= fade;
         }
+    }
+
+    // Turns a step's scores, -infinity where a position is masked, into weights.
+    __device__ __forceinline__ void weights(const f4 (&s)[2], float scale, float (&w)[8]) {
         const float from = ref == -INFINITY ? 0.0f : ref;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -328,6 +329,12 @@ struct Running {
         }
     }
 };
+
+__device__ __forceinline__ float largest(const f4 (&s)[2], float top) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i / 4][i & 3]);
+    return top;
+}
 
 // Scores of positions that are not read become -infinity.
 __device__ __forceinline__ void mask_scores(f4 (&s)[2], uint32_t live) {
@@ -549,6 +556,7 @@ tree_few_kernel(TreeParams p) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             float w[8];
+            run[t].follow(largest(s[t], -INFINITY), scale);
             run[t].weights(s[t], scale, w);
             pack_weights<kE4M3>(w, masked ? 0u : kLeastPart, high[t], low[t]);
         }
@@ -643,31 +651,52 @@ tree_few_kernel(TreeParams p) {
 constexpr uint32_t kManyWaves = 4;
 
 template <int kDim>
-constexpr uint32_t kStagePositions = kDim == 256 ? 32 : 64;
+constexpr uint32_t kStagePositions = 8192 / kDim;  // 16 KiB of K, and of V
+
+template <int kDim>
+__device__ __forceinline__ uint32_t k_turn(uint32_t row) {
+    return kDim == 64 ? row & 7u : row & 15u;
+}
+
+template <int kDim>
+__device__ __forceinline__ uint32_t v_turn(uint32_t row) {
+    return kDim == 64 ? row & 6u : 2 * (row & 7u);
+}
 
 template <int kDim>
 __device__ __forceinline__ uint32_t k_place(uint32_t row, uint32_t piece) {
-    return row * 2 * kDim + 16 * (piece ^ (kDim == 64 ? row & 7u : row & 15u));
+    return row * 2 * kDim + 16 * (piece ^ k_turn<kDim>(row));
 }
 
 template <int kDim>
 __device__ __forceinline__ uint32_t v_place(uint32_t row, uint32_t piece) {
-    return row * 2 * kDim + 16 * (piece ^ (kDim == 64 ? row & 6u : 2 * (row & 7u)));
+    return row * 2 * kDim + 16 * (piece ^ v_turn<kDim>(row));
 }
+
+// 16 bytes for each lane, from its offset, into LDS next to each other from `to` on
+// (both pointers uniform).
+__device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint8_t *to) {
+    typedef const __attribute__((address_space(1))) void *Global;
+    typedef __attribute__((address_space(3))) void *Lds;
+    __builtin_amdgcn_global_load_lds((Global)(from + offset), (Lds)(to), 16, 0, 0);
+}
+
+// Waits for this wave's loads, those into LDS among them: a barrier alone does not
+// (vmcnt 0; the other counters as they are).
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 template <int kDim, bool kE4M3, int kTiles, uint32_t kGroups>
 __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParams p) {
     constexpr int kPiece = kDim / 16, kKChunks = kDim / 32;
     constexpr uint32_t kThreads = 64 * kManyWaves, kRows = 16 * kTiles * kManyWaves / kGroups, kStage = kStagePositions<kDim>;
-    constexpr uint32_t kRowLoads = kDim * (kE4M3 ? 1 : 2) / 16;   // 16-byte loads of a row
-    constexpr int kLoads = kStage * kRowLoads / kThreads;         // of a lane for a stage's K, and V
-    constexpr uint32_t kBytes = kStage * 2 * kDim;                // of a stage's K, and V
-    static_assert(kStage % (kStep * kGroups) == 0 && kManyWaves * kTiles * kPiece * 1024 <= 4 * kBytes, "stages hold what the waves join");
+    constexpr uint32_t kBytes = kStage * 2 * kDim;  // of a stage's K, and V
+    static_assert(kStage % (kStep * kGroups) == 0 && kManyWaves / 2 * kTiles * kPiece * 1024 <= 2 * kBytes, "stages hold what the waves join");
     __shared__ int32_t s_page[kChunkPages];
-    __shared__ uint64_t s_k_at[kChunkPages], s_v_at[kChunkPages];  // the pages' offsets
     __shared__ int32_t s_reads[2][kManyWaves];
     __shared__ float s_stat[kManyWaves][kTiles][2][16];
-    __shared__ __attribute__((aligned(16))) uint8_t s_stage[4 * kBytes];  // K and V of two stages
+    // K and V of two stages: two arrays, as the compiler waits for loads into one
+    // before it reads from it
+    __shared__ __attribute__((aligned(16))) uint8_t s_even[2 * kBytes], s_odd[2 * kBytes];
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -715,16 +744,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     }
     const int32_t end = c.c1;
     c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
-    auto load_offsets = [&] {
-        const int32_t masked = load_pages(p, work, c, s_page);
-        for (uint32_t i = threadIdx.x; i < pages_of(p, c); i += kThreads) {  // as in load_pages: the same lane
-            const uint64_t page = static_cast<uint64_t>(max(s_page[i], 0));
-            s_k_at[i] = page * p.k.page;
-            s_v_at[i] = page * p.v.page;
-        }
-        return masked;
-    };
-    const int32_t masked_pages = load_offsets();
+    const int32_t masked_pages = load_pages(p, work, c, s_page);
 
     const float signed_scale = kE4M3 ? p.scale * p.k.scale[work.h] : p.scale;
     const float scale = signed_scale == 0 ? 1.0f : fabsf(signed_scale);
@@ -747,110 +767,198 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift;
     bool holes = __syncthreads_or(masked_pages);  // and the pages are there
 
-    // a stage's pieces, a lane's in registers on their way
+    // Rows of one load lie in one page each eight: where such a row begins is the
+    // same for all lanes, and a lane's own part of an address stays what it is.
+    const auto begin = [&](const Pages &x, const uint8_t *base, int32_t pos) {
+        const uint32_t at = static_cast<uint32_t>(min(pos, (c.c1 - 1) & ~7));  // past the end the last rows again
+        const uint32_t page = static_cast<uint32_t>(max(__builtin_amdgcn_readfirstlane(s_page[(at >> p.page_shift) - first]), 0));
+        return base + page * x.page + (at & in_page) * x.row;
+    };
+    uint32_t odd = 0;  // whether some value of V was left out of masked stages
+    auto clean = [&](int32_t pos, v4u &v) {  // nothing of V where no row reads, nothing that is no finite number
+        const bool there = pos >= c.lo && pos < c.c1 && s_page[(static_cast<uint32_t>(min(pos, c.c1 - 1)) >> p.page_shift) - first] >= 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (!there) v[w] = 0;
+            const uint32_t n = not_finite<kE4M3>(v[w]);
+            odd |= n;
+            v[w] &= ~n;
+        }
+    };
+    // E4M3: a lane's pieces of a stage, in registers on their way
+    constexpr uint32_t kRowLoads = kDim / 16;             // 16-byte loads of a row
+    constexpr int kLoads = kStage * kRowLoads / kThreads;  // of a lane for a stage's K, and V
+    constexpr uint32_t kRowStep = kThreads / kRowLoads, kRowsAtOnce = 64 / kRowLoads;
     const uint32_t load_row = threadIdx.x / kRowLoads, load_piece = threadIdx.x % kRowLoads;
-    constexpr uint32_t kRowStep = kThreads / kRowLoads;
-    const uint8_t *k_piece = kb + 16 * load_piece, *v_piece = vb + 16 * load_piece;
-    const uint32_t k_row = static_cast<uint32_t>(p.k.row), v_row = static_cast<uint32_t>(p.v.row);
+    const uint32_t k_lane = load_row % 8 * static_cast<uint32_t>(p.k.row) + 16 * load_piece;
+    const uint32_t v_lane = load_row % 8 * static_cast<uint32_t>(p.v.row) + 16 * load_piece;
     v4u kr[kLoads], vr[kLoads];
     auto load = [&](int32_t p0) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t pos = static_cast<uint32_t>(min(p0 + static_cast<int32_t>(load_row + i * kRowStep), c.c1 - 1));
-            const uint32_t page = (pos >> p.page_shift) - first, at = pos & in_page;
-            kr[i] = *reinterpret_cast<const v4u *>(k_piece + s_k_at[page] + uint64_t{at} * k_row);
-            vr[i] = *reinterpret_cast<const v4u *>(v_piece + s_v_at[page] + uint64_t{at} * v_row);
+            const int32_t pos = p0 + static_cast<int32_t>((wave * kRowsAtOnce + i * kRowStep) & ~7u);
+            const uint8_t *k = begin(p.k, kb, pos), *v = begin(p.v, vb, pos);
+            if (kRowsAtOnce > 8 && load_row % kRowsAtOnce >= 8) {
+                k = begin(p.k, kb, pos + 8);
+                v = begin(p.v, vb, pos + 8);
+            }
+            kr[i] = *reinterpret_cast<const v4u *>(k + k_lane);
+            vr[i] = *reinterpret_cast<const v4u *>(v + v_lane);
         }
     };
-    uint32_t odd = 0;  // whether some value of V was left out of masked stages
     auto store = [&](int32_t p0, uint8_t *to) {
         if (__builtin_expect(masked_at(c, holes, p0, kStage), false)) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int32_t pos = p0 + static_cast<int32_t>(load_row + i * kRowStep);
-                const bool there = pos >= c.lo && pos < c.c1 && s_page[(static_cast<uint32_t>(min(pos, c.c1 - 1)) >> p.page_shift) - first] >= 0;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    if (!there) vr[i][w] = 0;
-                    const uint32_t n = not_finite<kE4M3>(vr[i][w]);
-                    odd |= n;
-                    vr[i][w] &= ~n;
-                }
-            }
+            for (int i = 0; i < kLoads; ++i) clean(p0 + static_cast<int32_t>(load_row + i * kRowStep), vr[i]);
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t at = load_row + i * kRowStep;
-            if (kE4M3) {
 #pragma unroll
-                for (uint32_t e = 0; e < 2; ++e) {
-                    const uint32_t a = kr[i][2 * e], b = kr[i][2 * e + 1], x = vr[i][2 * e], y = vr[i][2 * e + 1];
-                    *reinterpret_cast<v4u *>(to + k_place<kDim>(at, 2 * load_piece + e)) = from_e4m3x8(a, b);
-                    *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, 2 * load_piece + e)) =
-                        v4u{half_from_e4m3<false>(x), half_from_e4m3<true>(x), half_from_e4m3<false>(y), half_from_e4m3<true>(y)};
-                }
-            } else {
-                *reinterpret_cast<v4u *>(to + k_place<kDim>(at, load_piece)) = kr[i];
-                *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, load_piece)) = vr[i];
+            for (uint32_t e = 0; e < 2; ++e) {
+                const uint32_t a = kr[i][2 * e], b = kr[i][2 * e + 1];
+                *reinterpret_cast<v4u *>(to + k_place<kDim>(at, 2 * load_piece + e)) = from_e4m3x8(a, b);
+                // rows in turn write their first and their second pieces: V's turn keeps those apart
+                const bool second = (e ^ at) & 1u;
+                const uint32_t x = second ? vr[i][2] : vr[i][0], y = second ? vr[i][3] : vr[i][1];
+                *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, 2 * load_piece + second)) =
+                    v4u{half_from_e4m3<false>(x), half_from_e4m3<true>(x), half_from_e4m3<false>(y), half_from_e4m3<true>(y)};
             }
+        }
+    };
+    // BF16: loads into LDS, a wave's next to each other: lane i's piece goes to place i
+    constexpr uint32_t kPieces = kDim / 8, kWaveRows = 64 / kPieces, kFetches = kStage / (kWaveRows * kManyWaves);
+    auto fetch = [&](int32_t p0, uint8_t *to) {
+#pragma unroll
+        for (uint32_t i = 0; i < kFetches; ++i) {
+            const uint32_t row0 = (i * kManyWaves + wave) * kWaveRows, row = row0 + lane / kPieces, place = lane % kPieces;
+            const int32_t pos = p0 + static_cast<int32_t>(row0 & ~7u);
+            load_lds(begin(p.k, kb, pos), row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim>(row)), to + row0 * 2 * kDim);
+            load_lds(begin(p.v, vb, pos), row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim>(row)), to + kBytes + row0 * 2 * kDim);
+        }
+    };
+    auto clean_stage = [&](int32_t p0, uint8_t *stage) {  // what has arrived
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < kStage * kPieces; i += kThreads) {
+            v4u *at = reinterpret_cast<v4u *>(stage + kBytes + 16 * i);
+            v4u v = *at;
+            clean(p0 + static_cast<int32_t>(i / kPieces), v);
+            *at = v;
         }
     };
 
     Running<kPiece> run[kTiles];
-    auto step = [&](int32_t p0, const uint8_t *stage, uint32_t row0, bool masked) {  // positions p0.., rows row0.. of the stage
-        f4 s[kTiles][2] = {};
+    constexpr int kSteps = kStage / (kStep * kGroups);  // of a wave in a stage
+    // A wave's steps of a stage, positions p0 and on, and the way of the next stage:
+    // all scores first, then a step's weights beside the product of those before.
+    auto steps = [&](int32_t p0, const uint8_t *stage, bool masked) {
+        f4 s[kSteps][kTiles][2] = {};
+        // reads from LDS stay a group ahead of what takes them: nothing of them is
+        // moved over these places, all else is
+        const auto keep_reads = [] { __builtin_amdgcn_sched_barrier(0x7F); };
+        v4u kf[2][kKChunks];
+        const auto read_k = [&](int n) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < kKChunks; ++i)
+                kf[n & 1][i] = *reinterpret_cast<const v4u *>(stage + (n / 2 * kGroups + group) * kStep * 2 * kDim + k_place<kDim>(16 * (n & 1) + r, 4 * i + q));
+        };
+        read_k(0);
 #pragma unroll
-            for (int i = 0; i < kKChunks; ++i) {
-                const v4u kw = *reinterpret_cast<const v4u *>(stage + row0 * 2 * kDim + k_place<kDim>(16 * u + r, 4 * i + q));
+        for (int n = 0; n < 2 * kSteps; ++n) {
+            if (n + 1 < 2 * kSteps) read_k(n + 1);
+            keep_reads();
+#pragma unroll
+            for (int i = 0; i < kKChunks; ++i)
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
-                    s[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[t][i], s[t][u], 0, 0, 0);
-            }
-        if (__builtin_expect(masked, false)) {
-            const uint32_t there = positions_there(p, c, s_page, p0, q);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) mask_scores(s[t], positions_read(p, work, rows, row[t], p0, q) & there);
+                    s[n / 2][t][n & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kf[n & 1][i]), qf[t][i], s[n / 2][t][n & 1], 0, 0, 0);
         }
-        v4u high[kTiles], low[kTiles];
+        constexpr int kBlock = 4, kBlocks = kPiece / kBlock;  // of V^T's tiles
+        v4u vt[2][kBlock];
+        const auto read_v = [&](int n) {
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                // lane r of four rows gives four values of row r / 4 and gets value r of all four
+                v2u half[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    half[u] = read_transposed(stage + kBytes + (n / kBlocks * kGroups + group) * kStep * 2 * kDim +
+                                              v_place<kDim>(16 * u + 4 * q + r / 4, 2 * (n % kBlocks * kBlock + j) + (r & 3u) / 2) + 8 * (r & 1u));
+                vt[n & 1][j] = v4u{half[0].x, half[0].y, half[1].x, half[1].y};
+            }
+        };
+        read_v(0);
+        keep_reads();
+        if (__builtin_expect(masked, false)) {
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n) {
+                const int32_t at = p0 + static_cast<int32_t>((n * kGroups + group) * kStep);
+                const uint32_t there = positions_there(p, c, s_page, at, q);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) mask_scores(s[n][t], positions_read(p, work, rows, row[t], at, q) & there);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-            float w[8];
-            run[t].weights(s[t], scale, w);
-            pack_weights<kE4M3>(w, masked ? 0u : kLeastPart, high[t], low[t]);
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n) top = largest(s[n][t], top);
+            run[t].follow(top, scale);
         }
+        const uint32_t least = masked ? 0u : kLeastPart;
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-            // lane r of four rows gives four values of row r / 4 and gets value r of all four
-            v2u half[2];
+        for (int n = 0; n < kSteps; ++n) {
+            v4u high[kTiles], low[kTiles];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                half[u] = read_transposed(stage + kBytes + row0 * 2 * kDim + v_place<kDim>(16 * u + 4 * q + r / 4, 2 * j + (r & 3u) / 2) + 8 * (r & 1u));
-            const v4u vt = {half[0].x, half[0].y, half[1].x, half[1].y};
+            for (int t = 0; t < kTiles; ++t) {
+                float w[8];
+                run[t].weights(s[n][t], scale, w);
+                pack_weights<kE4M3>(w, least, high[t], low[t]);
+            }
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) run[t].acc[j] = product<kE4M3>(vt, high[t], low[t], run[t].acc[j]);
+            for (int b = 0; b < kBlocks; ++b) {
+                const int at = n * kBlocks + b;
+                if (at + 1 < kSteps * kBlocks) read_v(at + 1);
+                keep_reads();
+#pragma unroll
+                for (int j = 0; j < kBlock; ++j)
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        run[t].acc[b * kBlock + j] = product<kE4M3>(vt[at & 1][j], high[t], low[t], run[t].acc[b * kBlock + j]);
+            }
         }
     };
     while (c.c0 < c.c1) {  // once for the pages that LDS holds
-        load(c.c0);
-        store(c.c0, s_stage);
-        load(c.c0 + static_cast<int32_t>(kStage));  // past the end the last row again
+        if (kE4M3) {
+            load(c.c0);
+            store(c.c0, s_even);
+            load(c.c0 + static_cast<int32_t>(kStage));  // past the end the last row again
+        } else {
+            fetch(c.c0, s_even);
+            arrived();
+        }
         __syncthreads();
-        uint32_t stage = 0;
-        for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage, stage ^= 2 * kBytes) {
-            if (active) {
-                const bool masked = masked_at(c, holes, p0, kStage);
-#pragma unroll
-                for (uint32_t at = 0; at < kStage; at += kStep * kGroups) {
-                    const int32_t from = p0 + static_cast<int32_t>(at + kStep * group);
-                    if (from >= c.c1) break;
-                    step(from, s_stage + stage, at + kStep * group, masked);
+        const auto turn = [&](int32_t p0, uint8_t *stage, uint8_t *other) {
+            const bool masked = masked_at(c, holes, p0, kStage);
+            const int32_t next = p0 + static_cast<int32_t>(kStage);
+            if (kE4M3) {
+                store(next, other);
+                load(next + static_cast<int32_t>(kStage));
+            } else {
+                if (__builtin_expect(masked, false)) {
+                    clean_stage(p0, stage);
+                    __syncthreads();
                 }
+                fetch(next, other);
             }
-            store(p0 + static_cast<int32_t>(kStage), s_stage + (stage ^ 2 * kBytes));
-            load(p0 + static_cast<int32_t>(2 * kStage));
+            if (active) steps(p0, stage, masked);
+            if (!kE4M3) arrived();
             __syncthreads();
+        };
+        for (int32_t p0 = c.c0; p0 < c.c1; p0 += 2 * kStage) {
+            turn(p0, s_even, s_odd);
+            if (p0 + static_cast<int32_t>(kStage) >= c.c1) break;
+            turn(p0 + static_cast<int32_t>(kStage), s_odd, s_even);
         }
         if (__builtin_expect(__syncthreads_or(odd != 0), 0))
             for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage)
@@ -863,11 +971,15 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         c.c0 = c.c1;
         c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
         first = static_cast<uint32_t>(c.c0) >> p.page_shift;
-        holes = __syncthreads_or(load_offsets());
+        holes = __syncthreads_or(load_pages(p, work, c, s_page));
     }
 
     const float v_scale = kE4M3 ? p.v.scale[work.h] : 1.0f;
-    f4 *parts = reinterpret_cast<f4 *>(s_stage) + wave / kGroups * kGroups * kTiles * kPiece * 64 + lane;
+    // a wave's part is as large as half of a stage
+    const auto part = [&](uint32_t g, int t, int j) -> f4 & {
+        const uint32_t w = wave / kGroups * kGroups + g;
+        return reinterpret_cast<f4 *>(w < kManyWaves / 2 ? s_even : s_odd)[((w % (kManyWaves / 2) * kTiles + t) * kPiece + j) * 64 + lane];
+    };
     if (kGroups > 1) {
         // every wave of a row group puts what it has side by side, and takes a share of all
 #pragma unroll
@@ -880,7 +992,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 s_stat[wave][t][1][r] = sum;
             }
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) parts[((group * kTiles + t) * kPiece + j) * 64] = run[t].acc[j];
+            for (int j = 0; j < kPiece; ++j) part(group, t, j) = run[t].acc[j];
         }
         __syncthreads();
     }
@@ -914,7 +1026,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             if (kGroups > 1) {
                 o = f4{};
 #pragma unroll
-                for (uint32_t g = 0; g < kGroups; ++g) o += parts[((g * kTiles + t) * kPiece + j + group) * 64] * fade[g];
+                for (uint32_t g = 0; g < kGroups; ++g) o += part(g, t, j + static_cast<int>(group)) * fade[g];
             }
             write_out<kDim>(p, work.split, to, 16 * (j + (kGroups > 1 ? group : 0)) + 4 * q, row[t].have, top, total, o * v_scale);
         }
@@ -955,6 +1067,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
 
 // ---- Host ------------------------------------------------------------------
 
+constexpr uint64_t kLargeChunk = 1024;
+
 struct Shape {
     uint32_t rows;  // of a workgroup: 16 and 32 in tree_few_kernel, more in tree_many_kernel
     uint32_t tiles, splits;
@@ -964,7 +1078,8 @@ Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads
     const uint64_t rows = nodes * group;
     Shape s;
     s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    if (s.rows == 64 && dim < 256 && batch * kv_heads * ((rows + 127) / 128) >= kComputeUnits) s.rows = 128;
+    const uint64_t large = batch * kv_heads * ((rows + 127) / 128);  // workgroups with all positions
+    if (rows > 64 && dim < 256 && large * positions >= 2 * kComputeUnits * kLargeChunk) s.rows = 128;
     s.tiles = static_cast<uint32_t>((rows + s.rows - 1) / s.rows);
     const uint64_t units = batch * kv_heads * s.tiles, wanted = 2 * kComputeUnits;
     const uint64_t want = (wanted + units - 1) / std::max<uint64_t>(units, 1);
@@ -1004,6 +1119,8 @@ auto kernel_of(bool e4m3, uint32_t rows) {
     return e4m3 ? tree_few_kernel<kDim, true, 1> : tree_few_kernel<kDim, false, 1>;
 }
 
+constexpr uint64_t kMaxRow = uint64_t{1} << 28;  // bytes; eight of them are an offset in 32 bits
+
 df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const int32_t *table, uint64_t table_stride,
                            uint64_t width, const int32_t *lens, uint16_t *out, float *lse, void *workspace,
                            uint64_t workspace_bytes, void *hip_stream) {
@@ -1027,7 +1144,7 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     TreeParams p;
     p.k = k_of(c);
     p.v = v_of(c);
-    if (p.k.row > 0xFFFFFFFFu || p.v.row > 0xFFFFFFFFu) return DF11_E_INVALID_ARG;  // the kernels multiply by them in 32 bits
+    if (p.k.row >= kMaxRow || p.v.row >= kMaxRow) return DF11_E_INVALID_ARG;
     p.q = t->q;
     p.table = table;
     p.lens = lens;

@@ -68,7 +68,7 @@ typedef struct df11_tree {
  * between calls; calls that run at the same time need one each.  batch = 0 or
  * nodes = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null or misaligned
  * pointers; sizes and strides as for df11_paged_attention, but 2^30 positions
- * or more in a table, or positions 4 GiB apart in a page; mask_node_stride below ceil(nodes / 64); over 2^20 nodes; more workgroups than a launch holds,
+ * or more in a table, or positions of a page 256 MiB apart; mask_node_stride below ceil(nodes / 64); over 2^20 nodes; more workgroups than a launch holds,
  * 2^24: batch x kv_heads x tiles of 16 to 64 rows of nodes x heads, times the
  * chunks of a sequence, or rows of the output past 2^31),
  * DF11_E_UNSUPPORTED, DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
