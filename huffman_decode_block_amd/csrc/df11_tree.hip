@@ -375,6 +375,13 @@ __device__ __forceinline__ v2u read_transposed(const uint8_t *at) {
     return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at)));
 }
 
+// The same of 8-bit values: eight of a row from each of two lanes, of eight rows.
+__device__ __forceinline__ v2u read_transposed8(const uint8_t *at) {
+    typedef int i2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) i2 Lds;
+    return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32((Lds *)(at)));
+}
+
 // Values j and j + 1 of a lane's eight rows, each as an operand: V^T's rows.
 __device__ __forceinline__ void transpose(const uint32_t (&pair)[8], v4u (&vt)[2]) {
 #pragma unroll
@@ -641,62 +648,61 @@ tree_few_kernel(TreeParams p) {
     }
 }
 
-// Many rows: keys and values go through LDS, once for a workgroup,
-// two stages in turn.  kGroups of the waves share a wave's 16 kTiles rows and take
-// a stage's steps in turn; they join in LDS.  E4M3 becomes BF16 (keys) and FP16
-// (values) on its way to LDS.  A row's 16-byte pieces lie there in an order of its
-// own, so that lanes that read a piece of different rows do not meet in a bank: K
-// is read row by row, V across four rows and two pieces, which the hardware's
-// transposing reads turn into V^T.
+// Many rows: keys and values go through LDS, once for a workgroup, as they are
+// stored, by loads that are stages ahead of their use.  kGroups of the waves share a
+// wave's 16 kTiles rows and take a stage's steps in turn; they join in LDS.  A row's
+// 16-byte pieces lie there in an order of its own, so that lanes that read a piece
+// of different rows do not meet in a bank: K is read piece by piece of 16 rows, V
+// across rows by the hardware's transposing reads, which give V^T.  E4M3 becomes
+// BF16 (keys) and FP16 (values) in registers.
 constexpr uint32_t kManyWaves = 4;
 
 template <int kDim>
-constexpr uint32_t kStagePositions = 8192 / kDim;  // 16 KiB of K, and of V
+constexpr uint32_t kStagePositions = 8192 / kDim;
 
-template <int kDim>
+template <int kDim, bool kE4M3>
 __device__ __forceinline__ uint32_t k_turn(uint32_t row) {
-    return kDim == 64 ? row & 7u : row & 15u;
+    constexpr uint32_t kPieces = kDim * (kE4M3 ? 1 : 2) / 16;
+    return kPieces >= 16 ? row & 15u : kPieces == 8 ? row >> (kE4M3 ? 1 : 0) & 7u : row >> 2 & 3u;
 }
 
-template <int kDim>
+template <int kDim, bool kE4M3>
 __device__ __forceinline__ uint32_t v_turn(uint32_t row) {
-    return kDim == 64 ? row & 6u : 2 * (row & 7u);
-}
-
-template <int kDim>
-__device__ __forceinline__ uint32_t k_place(uint32_t row, uint32_t piece) {
-    return row * 2 * kDim + 16 * (piece ^ k_turn<kDim>(row));
-}
-
-template <int kDim>
-__device__ __forceinline__ uint32_t v_place(uint32_t row, uint32_t piece) {
-    return row * 2 * kDim + 16 * (piece ^ v_turn<kDim>(row));
+    constexpr uint32_t kPieces = kDim * (kE4M3 ? 1 : 2) / 16;
+    if (!kE4M3) return kPieces == 8 ? row & 6u : 2 * (row & 7u);
+    return kPieces >= 16 ? (row & 7u) | (row >> 1 & 8u) : kPieces == 8 ? (row >> 1 & 3u) | (row >> 2 & 4u) : (row >> 2 & 1u) | (row >> 3 & 2u);
 }
 
 // 16 bytes for each lane, from its offset, into LDS next to each other from `to` on
-// (both pointers uniform).
+// (uniform).
 __device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint8_t *to) {
     typedef const __attribute__((address_space(1))) void *Global;
     typedef __attribute__((address_space(3))) void *Lds;
     __builtin_amdgcn_global_load_lds((Global)(from + offset), (Lds)(to), 16, 0, 0);
 }
 
-// Waits for this wave's loads, those into LDS among them: a barrier alone does not
-// (vmcnt 0; the other counters as they are).
-__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// Waits for this wave's loads but the last kAfter, those into LDS among them: a
+// barrier alone does not (vmcnt; the other counters as they are).
+template <int kAfter>
+__device__ __forceinline__ void arrived() {
+    static_assert(kAfter < 16, "four bits of the count");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | kAfter);
+}
 
 template <int kDim, bool kE4M3, int kTiles, uint32_t kGroups>
 __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParams p) {
     constexpr int kPiece = kDim / 16, kKChunks = kDim / 32;
     constexpr uint32_t kThreads = 64 * kManyWaves, kRows = 16 * kTiles * kManyWaves / kGroups, kStage = kStagePositions<kDim>;
-    constexpr uint32_t kBytes = kStage * 2 * kDim;  // of a stage's K, and V
-    static_assert(kStage % (kStep * kGroups) == 0 && kManyWaves / 2 * kTiles * kPiece * 1024 <= 2 * kBytes, "stages hold what the waves join");
+    constexpr uint32_t kRowBytes = kDim * (kE4M3 ? 1 : 2), kPieces = kRowBytes / 16, kBytes = kStage * kRowBytes;  // of a stage's K, and V
+    constexpr uint32_t kRing = kE4M3 ? 4 : 2;  // stages, 64 KiB
+    static_assert(kStage % (kStep * kGroups) == 0 && kTiles * kPiece * 1024 <= 2 * kBytes * kRing / kManyWaves, "stages hold what the waves join");
     __shared__ int32_t s_page[kChunkPages];
     __shared__ int32_t s_reads[2][kManyWaves];
     __shared__ float s_stat[kManyWaves][kTiles][2][16];
-    // K and V of two stages: two arrays, as the compiler waits for loads into one
-    // before it reads from it
-    __shared__ __attribute__((aligned(16))) uint8_t s_even[2 * kBytes], s_odd[2 * kBytes];
+    // K and V of each stage: arrays of their own, as the compiler waits for loads into
+    // one before it reads from it
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring0[2 * kBytes], s_ring1[2 * kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring2[kRing > 2 ? 2 * kBytes : 16], s_ring3[kRing > 2 ? 2 * kBytes : 16];
 
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -757,7 +763,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                              (work.h * p.group + (n - static_cast<uint32_t>(row[t].node) * p.group)) * p.q_head;
 #pragma unroll
         for (int i = 0; i < kKChunks; ++i) {
-            v4u w = row[t].have && signed_scale != 0 ? load8(qp + 32 * i + 8 * q) : v4u{0, 0, 0, 0};
+            const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
+            v4u w = row[t].have && signed_scale != 0 ? load8(qp + d) : v4u{0, 0, 0, 0};
             w ^= turned;
             qf[t][i] = __builtin_bit_cast(bf8, w);
         }
@@ -785,56 +792,20 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             v[w] &= ~n;
         }
     };
-    // E4M3: a lane's pieces of a stage, in registers on their way
-    constexpr uint32_t kRowLoads = kDim / 16;             // 16-byte loads of a row
-    constexpr int kLoads = kStage * kRowLoads / kThreads;  // of a lane for a stage's K, and V
-    constexpr uint32_t kRowStep = kThreads / kRowLoads, kRowsAtOnce = 64 / kRowLoads;
-    const uint32_t load_row = threadIdx.x / kRowLoads, load_piece = threadIdx.x % kRowLoads;
-    const uint32_t k_lane = load_row % 8 * static_cast<uint32_t>(p.k.row) + 16 * load_piece;
-    const uint32_t v_lane = load_row % 8 * static_cast<uint32_t>(p.v.row) + 16 * load_piece;
-    v4u kr[kLoads], vr[kLoads];
-    auto load = [&](int32_t p0) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int32_t pos = p0 + static_cast<int32_t>((wave * kRowsAtOnce + i * kRowStep) & ~7u);
-            const uint8_t *k = begin(p.k, kb, pos), *v = begin(p.v, vb, pos);
-            if (kRowsAtOnce > 8 && load_row % kRowsAtOnce >= 8) {
-                k = begin(p.k, kb, pos + 8);
-                v = begin(p.v, vb, pos + 8);
-            }
-            kr[i] = *reinterpret_cast<const v4u *>(k + k_lane);
-            vr[i] = *reinterpret_cast<const v4u *>(v + v_lane);
-        }
-    };
-    auto store = [&](int32_t p0, uint8_t *to) {
-        if (__builtin_expect(masked_at(c, holes, p0, kStage), false)) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) clean(p0 + static_cast<int32_t>(load_row + i * kRowStep), vr[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t at = load_row + i * kRowStep;
-#pragma unroll
-            for (uint32_t e = 0; e < 2; ++e) {
-                const uint32_t a = kr[i][2 * e], b = kr[i][2 * e + 1];
-                *reinterpret_cast<v4u *>(to + k_place<kDim>(at, 2 * load_piece + e)) = from_e4m3x8(a, b);
-                // rows in turn write their first and their second pieces: V's turn keeps those apart
-                const bool second = (e ^ at) & 1u;
-                const uint32_t x = second ? vr[i][2] : vr[i][0], y = second ? vr[i][3] : vr[i][1];
-                *reinterpret_cast<v4u *>(to + kBytes + v_place<kDim>(at, 2 * load_piece + second)) =
-                    v4u{half_from_e4m3<false>(x), half_from_e4m3<true>(x), half_from_e4m3<false>(y), half_from_e4m3<true>(y)};
-            }
-        }
-    };
-    // BF16: loads into LDS, a wave's next to each other: lane i's piece goes to place i
-    constexpr uint32_t kPieces = kDim / 8, kWaveRows = 64 / kPieces, kFetches = kStage / (kWaveRows * kManyWaves);
+    // Loads of a stage into LDS, a wave's next to each other: lane i's piece goes to place i.
+    constexpr uint32_t kLoadRows = 64 / kPieces, kFetches = kStage / (kLoadRows * kManyWaves);  // rows of a load; loads of K
     auto fetch = [&](int32_t p0, uint8_t *to) {
 #pragma unroll
         for (uint32_t i = 0; i < kFetches; ++i) {
-            const uint32_t row0 = (i * kManyWaves + wave) * kWaveRows, row = row0 + lane / kPieces, place = lane % kPieces;
+            const uint32_t row0 = (i * kManyWaves + wave) * kLoadRows, row = row0 + lane / kPieces, place = lane % kPieces;
             const int32_t pos = p0 + static_cast<int32_t>(row0 & ~7u);
-            load_lds(begin(p.k, kb, pos), row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim>(row)), to + row0 * 2 * kDim);
-            load_lds(begin(p.v, vb, pos), row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim>(row)), to + kBytes + row0 * 2 * kDim);
+            const uint8_t *k = begin(p.k, kb, pos), *v = begin(p.v, vb, pos);
+            if (kLoadRows > 8 && lane >= 8 * kPieces) {
+                k = begin(p.k, kb, pos + 8);
+                v = begin(p.v, vb, pos + 8);
+            }
+            load_lds(k, row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim, kE4M3>(row)), to + row0 * kRowBytes);
+            load_lds(v, row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim, kE4M3>(row)), to + kBytes + row0 * kRowBytes);
         }
     };
     auto clean_stage = [&](int32_t p0, uint8_t *stage) {  // what has arrived
@@ -856,11 +827,13 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         // reads from LDS stay a group ahead of what takes them: nothing of them is
         // moved over these places, all else is
         const auto keep_reads = [] { __builtin_amdgcn_sched_barrier(0x7F); };
-        v4u kf[2][kKChunks];
+        constexpr int kKReads = kE4M3 ? kKChunks / 2 : kKChunks;  // 16 bytes of a K row each
+        v4u kf[2][kKReads];
         const auto read_k = [&](int n) {
+            const uint32_t at = (n / 2 * kGroups + group) * kStep + 16 * (n & 1);
 #pragma unroll
-            for (int i = 0; i < kKChunks; ++i)
-                kf[n & 1][i] = *reinterpret_cast<const v4u *>(stage + (n / 2 * kGroups + group) * kStep * 2 * kDim + k_place<kDim>(16 * (n & 1) + r, 4 * i + q));
+            for (int i = 0; i < kKReads; ++i)
+                kf[n & 1][i] = *reinterpret_cast<const v4u *>(stage + (at + r) * kRowBytes + 16 * ((4 * i + q) ^ k_turn<kDim, kE4M3>(16 * (n & 1) + r)));
         };
         read_k(0);
 #pragma unroll
@@ -868,23 +841,31 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             if (n + 1 < 2 * kSteps) read_k(n + 1);
             keep_reads();
 #pragma unroll
-            for (int i = 0; i < kKChunks; ++i)
+            for (int i = 0; i < kKChunks; ++i) {
+                v4u kw = kf[n & 1][kE4M3 ? i / 2 : i];
+                if (kE4M3) kw = i & 1 ? from_e4m3x8(kw.z, kw.w) : from_e4m3x8(kw.x, kw.y);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
-                    s[n / 2][t][n & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kf[n & 1][i]), qf[t][i], s[n / 2][t][n & 1], 0, 0, 0);
+                    s[n / 2][t][n & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kw), qf[t][i], s[n / 2][t][n & 1], 0, 0, 0);
+            }
         }
         constexpr int kBlock = 4, kBlocks = kPiece / kBlock;  // of V^T's tiles
-        v4u vt[2][kBlock];
+        v2u vt[2][kBlock][kE4M3 ? 1 : 2];
         const auto read_v = [&](int n) {
+            const uint8_t *from = stage + kBytes + (n / kBlocks * kGroups + group) * kStep * kRowBytes;
 #pragma unroll
             for (int j = 0; j < kBlock; ++j) {
-                // lane r of four rows gives four values of row r / 4 and gets value r of all four
-                v2u half[2];
+                const uint32_t tile = n % kBlocks * kBlock + j;
+                if (kE4M3) {
+                    const uint32_t at = 16 * (r / 8) + 4 * q + (r / 2 & 3u);
+                    vt[n & 1][j][0] = read_transposed8(from + at * kRowBytes + 16 * (tile ^ v_turn<kDim, true>(at)) + 8 * (r & 1u));
+                } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    half[u] = read_transposed(stage + kBytes + (n / kBlocks * kGroups + group) * kStep * 2 * kDim +
-                                              v_place<kDim>(16 * u + 4 * q + r / 4, 2 * (n % kBlocks * kBlock + j) + (r & 3u) / 2) + 8 * (r & 1u));
-                vt[n & 1][j] = v4u{half[0].x, half[0].y, half[1].x, half[1].y};
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t at = 16 * u + 4 * q + r / 4;
+                        vt[n & 1][j][kE4M3 ? 0 : u] = read_transposed(from + at * kRowBytes + 16 * ((2 * tile + (r & 3u) / 2) ^ v_turn<kDim, false>(at)) + 8 * (r & 1u));
+                    }
+                }
             }
         };
         read_v(0);
@@ -921,45 +902,42 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 if (at + 1 < kSteps * kBlocks) read_v(at + 1);
                 keep_reads();
 #pragma unroll
-                for (int j = 0; j < kBlock; ++j)
+                for (int j = 0; j < kBlock; ++j) {
+                    const v2u x = vt[at & 1][j][0], y = vt[at & 1][j][kE4M3 ? 0 : 1];
+                    const v4u v = kE4M3 ? v4u{half_from_e4m3<false>(x.x), half_from_e4m3<true>(x.x), half_from_e4m3<false>(x.y), half_from_e4m3<true>(x.y)}
+                                        : v4u{x.x, x.y, y.x, y.y};
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
-                        run[t].acc[b * kBlock + j] = product<kE4M3>(vt[at & 1][j], high[t], low[t], run[t].acc[b * kBlock + j]);
+                        run[t].acc[b * kBlock + j] = product<kE4M3>(v, high[t], low[t], run[t].acc[b * kBlock + j]);
+                }
             }
         }
     };
     while (c.c0 < c.c1) {  // once for the pages that LDS holds
-        if (kE4M3) {
-            load(c.c0);
-            store(c.c0, s_even);
-            load(c.c0 + static_cast<int32_t>(kStage));  // past the end the last row again
-        } else {
-            fetch(c.c0, s_even);
-            arrived();
-        }
+        uint8_t *const ring[4] = {s_ring0, s_ring1, s_ring2, s_ring3};
+#pragma unroll
+        for (uint32_t i = 0; i + 1 < kRing; ++i) fetch(c.c0 + static_cast<int32_t>(i * kStage), ring[i]);
+        arrived<2 * kFetches * (kRing - 2)>();
         __syncthreads();
-        const auto turn = [&](int32_t p0, uint8_t *stage, uint8_t *other) {
+        const auto turn = [&](int32_t p0, uint32_t n) {  // a stage, number n of the ring
             const bool masked = masked_at(c, holes, p0, kStage);
-            const int32_t next = p0 + static_cast<int32_t>(kStage);
-            if (kE4M3) {
-                store(next, other);
-                load(next + static_cast<int32_t>(kStage));
-            } else {
-                if (__builtin_expect(masked, false)) {
-                    clean_stage(p0, stage);
-                    __syncthreads();
-                }
-                fetch(next, other);
+            if (__builtin_expect(masked, false)) {
+                clean_stage(p0, ring[n]);
+                __syncthreads();
             }
-            if (active) steps(p0, stage, masked);
-            if (!kE4M3) arrived();
+            fetch(p0 + static_cast<int32_t>((kRing - 1) * kStage), ring[(n + kRing - 1) % kRing]);
+            if (active) steps(p0, ring[n], masked);
+            arrived<2 * kFetches * (kRing - 2)>();
             __syncthreads();
         };
-        for (int32_t p0 = c.c0; p0 < c.c1; p0 += 2 * kStage) {
-            turn(p0, s_even, s_odd);
-            if (p0 + static_cast<int32_t>(kStage) >= c.c1) break;
-            turn(p0 + static_cast<int32_t>(kStage), s_odd, s_even);
+        for (int32_t p0 = c.c0; p0 < c.c1; p0 += kRing * kStage) {
+#pragma unroll
+            for (uint32_t n = 0; n < kRing; ++n) {
+                const int32_t at = p0 + static_cast<int32_t>(n * kStage);
+                if (at < c.c1) turn(at, n);
+            }
         }
+        arrived<0>();  // what was fetched past the end
         if (__builtin_expect(__syncthreads_or(odd != 0), 0))
             for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage)
                 if (masked_at(c, holes, p0, kStage))
@@ -975,10 +953,11 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     }
 
     const float v_scale = kE4M3 ? p.v.scale[work.h] : 1.0f;
-    // a wave's part is as large as half of a stage
+    // the stages hold the waves' parts
     const auto part = [&](uint32_t g, int t, int j) -> f4 & {
-        const uint32_t w = wave / kGroups * kGroups + g;
-        return reinterpret_cast<f4 *>(w < kManyWaves / 2 ? s_even : s_odd)[((w % (kManyWaves / 2) * kTiles + t) * kPiece + j) * 64 + lane];
+        constexpr uint32_t kPer = kManyWaves / kRing;  // waves to a stage
+        const uint32_t w = wave / kGroups * kGroups + g, n = w / kPer;
+        return reinterpret_cast<f4 *>(n == 0 ? s_ring0 : n == 1 ? s_ring1 : n == 2 ? s_ring2 : s_ring3)[((w % kPer * kTiles + t) * kPiece + j) * 64 + lane];
     };
     if (kGroups > 1) {
         // every wave of a row group puts what it has side by side, and takes a share of all
