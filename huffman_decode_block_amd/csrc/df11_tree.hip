@@ -1012,36 +1012,73 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     }
 }
 
-// Joins the chunks: kDim / 4 lanes for a row, four values each.
+// Joins the chunks: kDim / 4 lanes, four values each, for every `share`-th chunk of
+// a row (a power of two); LDS joins those.  Bound by latency: a lane has four
+// chunks' values on their way.
 constexpr uint32_t kJoinThreads = 256;
 
 template <int kDim>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, uint64_t rows) {
-    constexpr uint32_t kQuads = kDim / 4;
-    const uint64_t row = uint64_t{blockIdx.x} * (kJoinThreads / kQuads) + threadIdx.x / kQuads;
-    const uint32_t d = threadIdx.x % kQuads;
-    if (row >= rows) return;
-    const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row * p.splits;
-    const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
-    float top = -INFINITY;
-    for (uint32_t i = 0; i < p.splits; ++i) top = fmaxf(top, stats[i].x);
-    const float from = top == -INFINITY ? 0.0f : top;
-    float total = 0;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, uint64_t rows, uint32_t share) {
+    constexpr uint32_t kQuads = kDim / 4, kAhead = 4;
+    __shared__ f4 s_part[kJoinThreads];
+    __shared__ v2f s_stat[kJoinThreads];
+    const uint32_t d = threadIdx.x % kQuads, group = threadIdx.x / kQuads % share;
+    const uint64_t row = uint64_t{blockIdx.x} * (kJoinThreads / kQuads / share) + threadIdx.x / (kQuads * share);
+    float top = -INFINITY, total = 0;
     f4 o = {};
-    for (uint32_t i = 0; i < p.splits; ++i) {
-        const v2f s = stats[i];
-        if (s.x == -INFINITY && s.y == 0) continue;  // its values are not written
-        const float f = exp2_(s.x - from);
-        total += s.y * f;
-        o += part[uint64_t{i} * kQuads] * f;
+    if (row < rows) {
+        const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row * p.splits;
+        const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
+        for (uint32_t i0 = group; i0 < p.splits; i0 += kAhead * share) {
+            v2f s[kAhead];
+            f4 v[kAhead];
+            float most = top;
+#pragma unroll
+            for (uint32_t a = 0; a < kAhead; ++a) {
+                const uint32_t i = i0 + a * share;
+                s[a] = v2f{-INFINITY, 0};
+                v[a] = f4{};
+                if (i < p.splits) {
+                    s[a] = stats[i];
+                    v[a] = part[uint64_t{i} * kQuads];
+                }
+            }
+#pragma unroll
+            for (uint32_t a = 0; a < kAhead; ++a) most = fmaxf(most, s[a].x);
+            const float from = most == -INFINITY ? 0.0f : most, fade = exp2_(top - from);
+            top = most;
+            total *= fade;
+            o *= fade;
+#pragma unroll
+            for (uint32_t a = 0; a < kAhead; ++a) {
+                const float f = exp2_(s[a].x - from);
+                total += s[a].y * f;
+                // without positions a chunk's values are not written
+                if (s[a].x != -INFINITY || s[a].y != 0) o += v[a] * f;
+            }
+        }
     }
+    if (share > 1) {
+        s_part[threadIdx.x] = o;
+        s_stat[threadIdx.x] = v2f{top, total};
+        __syncthreads();
+        if (group) return;
+        for (uint32_t g = 1; g < share; ++g) {
+            const v2f s = s_stat[threadIdx.x + g * kQuads];
+            const float most = fmaxf(top, s.x), from = most == -INFINITY ? 0.0f : most, fade = exp2_(top - from), f = exp2_(s.x - from);
+            top = most;
+            total = total * fade + s.y * f;
+            o = o * fade + s_part[threadIdx.x + g * kQuads] * f;
+        }
+    }
+    if (row >= rows) return;
     if (total == 0) o = f4{};
     const float inv = total == 0 ? 0.0f : 1.0f / total;
     v2u to;
     to.x = pack2b(o[0] * inv, o[1] * inv);
     to.y = pack2b(o[2] * inv, o[3] * inv);
     *reinterpret_cast<v2u *>(p.out + row * kDim + 4 * d) = to;
-    if (d == 0 && p.lse) p.lse[row] = (from + __builtin_amdgcn_logf(total)) * kLn2;
+    if (d == 0 && p.lse) p.lse[row] = ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // ---- Host ------------------------------------------------------------------
@@ -1079,7 +1116,7 @@ uint64_t workgroups(uint64_t batch, uint32_t kv_heads, const Shape &s) {
 // Whether the kernels' work items fit a launch, which holds fewer than 2^32.
 bool launchable(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t kv_heads, const Shape &s) {
     return batch * kv_heads * s.splits < (uint64_t{1} << 32) && workgroups(batch, kv_heads, s) < (1u << 24) &&
-           nodes * q_heads < (uint64_t{1} << 31) && batch * nodes * q_heads < (uint64_t{1} << 31) / 64 * 16;
+           nodes * q_heads < (uint64_t{1} << 31) && batch * nodes * q_heads < (uint64_t{1} << 24);
 }
 
 uint64_t workspace_of(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t dim, const Shape &s) {
@@ -1166,11 +1203,13 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
                                    : kernel_of<256>(e4m3, s.rows);
     hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(t->batch, c->kv_heads, s)), 64 * (s.rows > 32 ? kManyWaves : kWaves), 0, st, p);
     if (err == hipSuccess && s.splits > 1) {
-        const uint64_t per = kJoinThreads / (c->head_dim / 4);
+        uint32_t share = 1;
+        while (share < kJoinThreads / (c->head_dim / 4) && 4 * share < s.splits) share *= 2;
+        const uint64_t per = kJoinThreads / (c->head_dim / 4) / share;
         err = launch(c->head_dim == 64    ? tree_join_kernel<64>
                      : c->head_dim == 128 ? tree_join_kernel<128>
                                           : tree_join_kernel<256>,
-                     static_cast<uint32_t>((rows + per - 1) / per), kJoinThreads, 0, st, p, rows);
+                     static_cast<uint32_t>((rows + per - 1) / per), kJoinThreads, 0, st, p, rows, share);
     }
     return launched(err);
 }

@@ -70,7 +70,7 @@ typedef struct df11_tree {
  * pointers; sizes and strides as for df11_paged_attention, but 2^30 positions
  * or more in a table, or positions of a page 256 MiB apart; mask_node_stride below ceil(nodes / 64); over 2^20 nodes; more workgroups than a launch holds,
  * 2^24: batch x kv_heads x tiles of 16 to 64 rows of nodes x heads, times the
- * chunks of a sequence, or rows of the output past 2^31),
+ * chunks of a sequence; or 2^24 rows of the output),
  * DF11_E_UNSUPPORTED, DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
 df11_status df11_paged_tree_attention(const df11_paged_cache *cache, const df11_tree *tree, const int32_t *page_table,
                                       uint64_t table_stride, uint64_t table_width, const int32_t *lens, uint16_t *out,
