@@ -21,6 +21,7 @@ constexpr uint32_t kMinChunk = kWaves * kStep;
 constexpr uint32_t kMaxChunk = 4096;  // positions whose pages LDS holds
 constexpr uint32_t kChunkPages = kMaxChunk / kMinPage + 1;
 constexpr uint32_t kPad = 4;  // floats between rows in LDS: they start in different banks
+constexpr uint32_t kMaskedSteps = 3;  // what looking at masks costs a chunk
 constexpr float kSlack = 8;   // powers of two that weights may grow to before their reference follows
 
 struct TreeParams {
@@ -188,7 +189,8 @@ __device__ __forceinline__ Chunk chunk_of(const TreeParams &p, const Work &w, co
     const int32_t base = lo & ~static_cast<int32_t>(kStep - 1);
     const uint32_t steps = hi > base ? (hi - base + kStep - 1) / kStep : 0;
     const uint32_t chunks = min(p.splits, (steps + kMinChunk / kStep - 1) / (kMinChunk / kStep));
-    const uint32_t parts = max(chunks, 1u), each = steps / parts, more = steps - each * parts;
+    // the last chunk has steps in which masks are looked at, and gets fewer
+    const uint32_t parts = max(chunks, 1u), full = steps + min(kMaskedSteps, steps / parts / 2), each = full / parts, more = full - each * parts;
     Chunk c;
     c.lo = lo;
     c.lo_max = lo_max;
@@ -674,11 +676,13 @@ __device__ __forceinline__ uint32_t v_turn(uint32_t row) {
 }
 
 // 16 bytes for each lane, from its offset, into LDS next to each other from `to` on
-// (uniform).
+// (uniform).  By hand: behind the builtin the compiler lets transposing
+// reads of other arrays wait for it, too.  Nothing is returned to a register, and
+// arrived() waits for what was loaded.
 __device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint8_t *to) {
-    typedef const __attribute__((address_space(1))) void *Global;
-    typedef __attribute__((address_space(3))) void *Lds;
-    __builtin_amdgcn_global_load_lds((Global)(from + offset), (Lds)(to), 16, 0, 0);
+    typedef __attribute__((address_space(3))) uint8_t *Lds;
+    const uint32_t place = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((Lds)(to))));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(place), "v"(from + offset) : "memory", "m0");
 }
 
 // Waits for this wave's loads but the last kAfter, those into LDS among them: a
@@ -754,33 +758,20 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
 
     const float signed_scale = kE4M3 ? p.scale * p.k.scale[work.h] : p.scale;
     const float scale = signed_scale == 0 ? 1.0f : fabsf(signed_scale);
-    const uint32_t turned = signed_scale < 0 ? 0x80008000u : 0;
-    bf8 qf[kTiles][kKChunks];
+    v4u qw[kTiles][kKChunks];  // on its way until the first stage is
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         const uint32_t n = min(rows.row0 + wave_row + 16 * t + r, p.nodes * p.group - 1);
         const uint16_t *qp = p.q + work.b * p.q_batch + static_cast<uint32_t>(row[t].node) * p.q_node +
                              (work.h * p.group + (n - static_cast<uint32_t>(row[t].node) * p.group)) * p.q_head;
 #pragma unroll
-        for (int i = 0; i < kKChunks; ++i) {
-            const uint32_t d = kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
-            v4u w = row[t].have && signed_scale != 0 ? load8(qp + d) : v4u{0, 0, 0, 0};
-            w ^= turned;
-            qf[t][i] = __builtin_bit_cast(bf8, w);
-        }
+        for (int i = 0; i < kKChunks; ++i) qw[t][i] = load8(qp + (kE4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q));
     }
     const uint8_t *kb = p.k.base + work.h * p.k.head, *vb = p.v.base + work.h * p.v.head;
     const uint32_t in_page = (1u << p.page_shift) - 1;
     uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift;
     bool holes = __syncthreads_or(masked_pages);  // and the pages are there
 
-    // Rows of one load lie in one page each eight: where such a row begins is the
-    // same for all lanes, and a lane's own part of an address stays what it is.
-    const auto begin = [&](const Pages &x, const uint8_t *base, int32_t pos) {
-        const uint32_t at = static_cast<uint32_t>(min(pos, (c.c1 - 1) & ~7));  // past the end the last rows again
-        const uint32_t page = static_cast<uint32_t>(max(__builtin_amdgcn_readfirstlane(s_page[(at >> p.page_shift) - first]), 0));
-        return base + page * x.page + (at & in_page) * x.row;
-    };
     uint32_t odd = 0;  // whether some value of V was left out of masked stages
     auto clean = [&](int32_t pos, v4u &v) {  // nothing of V where no row reads, nothing that is no finite number
         const bool there = pos >= c.lo && pos < c.c1 && s_page[(static_cast<uint32_t>(min(pos, c.c1 - 1)) >> p.page_shift) - first] >= 0;
@@ -792,37 +783,91 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             v[w] &= ~n;
         }
     };
-    // Loads of a stage into LDS, a wave's next to each other: lane i's piece goes to place i.
+    // Loads of a stage into LDS, a wave's next to each other: lane i's piece goes to
+    // place i.  Rows of one load lie in one page each eight: where such eight begin
+    // is the same for all lanes, and a lane's own part of an address stays what it is.
     constexpr uint32_t kLoadRows = 64 / kPieces, kFetches = kStage / (kLoadRows * kManyWaves);  // rows of a load; loads of K
-    auto fetch = [&](int32_t p0, uint8_t *to) {
+    constexpr uint32_t kEights = kLoadRows > 8 ? 2 : 1;
+    struct Fetch {
+        const uint8_t *k[kFetches][kEights], *v[kFetches][kEights];
+        uint8_t *to;
+    };
+    auto find = [&](int32_t p0, uint8_t *to) {
+        uint32_t at[kFetches][kEights];
+        int32_t page[kFetches][kEights];
 #pragma unroll
-        for (uint32_t i = 0; i < kFetches; ++i) {
-            const uint32_t row0 = (i * kManyWaves + wave) * kLoadRows, row = row0 + lane / kPieces, place = lane % kPieces;
-            const int32_t pos = p0 + static_cast<int32_t>(row0 & ~7u);
-            const uint8_t *k = begin(p.k, kb, pos), *v = begin(p.v, vb, pos);
-            if (kLoadRows > 8 && lane >= 8 * kPieces) {
-                k = begin(p.k, kb, pos + 8);
-                v = begin(p.v, vb, pos + 8);
+        for (uint32_t i = 0; i < kFetches; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < kEights; ++e) {
+                // past the end the last rows again
+                at[i][e] = static_cast<uint32_t>(min(p0 + static_cast<int32_t>(((i * kManyWaves + wave) * kLoadRows & ~7u) + 8 * e), (c.c1 - 1) & ~7));
+                page[i][e] = s_page[(at[i][e] >> p.page_shift) - first];
             }
-            load_lds(k, row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim, kE4M3>(row)), to + row0 * kRowBytes);
-            load_lds(v, row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim, kE4M3>(row)), to + kBytes + row0 * kRowBytes);
-        }
+        __builtin_amdgcn_sched_barrier(0);  // all of them on their way before the first is waited for
+        Fetch f;
+        f.to = to;
+#pragma unroll
+        for (uint32_t i = 0; i < kFetches; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < kEights; ++e) {
+                const uint32_t n = static_cast<uint32_t>(max(__builtin_amdgcn_readfirstlane(page[i][e]), 0)), in = at[i][e] & in_page;
+                f.k[i][e] = kb + n * p.k.page + in * p.k.row;
+                f.v[i][e] = vb + n * p.v.page + in * p.v.row;
+            }
+        return f;
+    };
+    auto fetch = [&](const Fetch &f, uint32_t i) {
+        const uint32_t row0 = (i * kManyWaves + wave) * kLoadRows, row = row0 + lane / kPieces, place = lane % kPieces;
+        const bool second = kEights > 1 && lane >= 8 * kPieces;
+        const uint8_t *k = second ? f.k[i][kEights - 1] : f.k[i][0], *v = second ? f.v[i][kEights - 1] : f.v[i][0];
+        load_lds(k, row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim, kE4M3>(row)), f.to + row0 * kRowBytes);
+        load_lds(v, row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim, kE4M3>(row)), f.to + kBytes + row0 * kRowBytes);
+    };
+    auto fetch_all = [&](const Fetch &f) {
+#pragma unroll
+        for (uint32_t i = 0; i < kFetches; ++i) fetch(f, i);
+    };
+    uint8_t *const ring[4] = {s_ring0, s_ring1, s_ring2, s_ring3};
+    auto fetch_first = [&] {
+#pragma unroll
+        for (uint32_t i = 0; i + 1 < kRing; ++i) fetch_all(find(c.c0 + static_cast<int32_t>(i * kStage), ring[i]));
     };
     auto clean_stage = [&](int32_t p0, uint8_t *stage) {  // what has arrived
-#pragma unroll 1
-        for (uint32_t i = threadIdx.x; i < kStage * kPieces; i += kThreads) {
-            v4u *at = reinterpret_cast<v4u *>(stage + kBytes + 16 * i);
-            v4u v = *at;
-            clean(p0 + static_cast<int32_t>(i / kPieces), v);
-            *at = v;
+        constexpr uint32_t kEach = kStage * kPieces / kThreads;
+        v4u *at = reinterpret_cast<v4u *>(stage + kBytes) + threadIdx.x;
+        v4u v[kEach];
+#pragma unroll
+        for (uint32_t i = 0; i < kEach; ++i) v[i] = at[i * kThreads];
+#pragma unroll
+        for (uint32_t i = 0; i < kEach; ++i) {
+            clean(p0 + static_cast<int32_t>((i * kThreads + threadIdx.x) / kPieces), v[i]);
+            at[i * kThreads] = v[i];
         }
     };
 
+    if (c.c0 < c.c1) fetch_first();
+    bf8 qf[kTiles][kKChunks];
+    const uint32_t turned = signed_scale < 0 ? 0x80008000u : 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < kKChunks; ++i) {
+            const v4u w = row[t].have && signed_scale != 0 ? qw[t][i] : v4u{0, 0, 0, 0};
+            qf[t][i] = __builtin_bit_cast(bf8, w ^ turned);
+        }
+
     Running<kPiece> run[kTiles];
     constexpr int kSteps = kStage / (kStep * kGroups);  // of a wave in a stage
-    // A wave's steps of a stage, positions p0 and on, and the way of the next stage:
-    // all scores first, then a step's weights beside the product of those before.
-    auto steps = [&](int32_t p0, const uint8_t *stage, bool masked) {
+    // A wave's steps of a stage, positions p0 and on: all scores first, then a step's
+    // weights beside the product of those before.  Loads of a later stage go out
+    // between them, as a compute unit takes 64 bytes of them in a cycle.
+    auto steps = [&](int32_t p0, const uint8_t *stage, bool masked, const Fetch &later) {
+        constexpr int kPlaces = 2 * kSteps + kSteps * (kPiece / 4);
+        const auto go_on = [&](int place) {
+#pragma unroll
+            for (uint32_t i = 0; i < kFetches; ++i)
+                if (place == static_cast<int>(i * kPlaces / kFetches)) fetch(later, i);
+        };
         f4 s[kSteps][kTiles][2] = {};
         // reads from LDS stay a group ahead of what takes them: nothing of them is
         // moved over these places, all else is
@@ -840,6 +885,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         for (int n = 0; n < 2 * kSteps; ++n) {
             if (n + 1 < 2 * kSteps) read_k(n + 1);
             keep_reads();
+            go_on(n);
 #pragma unroll
             for (int i = 0; i < kKChunks; ++i) {
                 v4u kw = kf[n & 1][kE4M3 ? i / 2 : i];
@@ -901,6 +947,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 const int at = n * kBlocks + b;
                 if (at + 1 < kSteps * kBlocks) read_v(at + 1);
                 keep_reads();
+                go_on(2 * kSteps + at);
 #pragma unroll
                 for (int j = 0; j < kBlock; ++j) {
                     const v2u x = vt[at & 1][j][0], y = vt[at & 1][j][kE4M3 ? 0 : 1];
@@ -914,9 +961,6 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         }
     };
     while (c.c0 < c.c1) {  // once for the pages that LDS holds
-        uint8_t *const ring[4] = {s_ring0, s_ring1, s_ring2, s_ring3};
-#pragma unroll
-        for (uint32_t i = 0; i + 1 < kRing; ++i) fetch(c.c0 + static_cast<int32_t>(i * kStage), ring[i]);
         arrived<2 * kFetches * (kRing - 2)>();
         __syncthreads();
         const auto turn = [&](int32_t p0, uint32_t n) {  // a stage, number n of the ring
@@ -925,8 +969,11 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 clean_stage(p0, ring[n]);
                 __syncthreads();
             }
-            fetch(p0 + static_cast<int32_t>((kRing - 1) * kStage), ring[(n + kRing - 1) % kRing]);
-            if (active) steps(p0, ring[n], masked);
+            const Fetch later = find(p0 + static_cast<int32_t>((kRing - 1) * kStage), ring[(n + kRing - 1) % kRing]);
+            if (active)
+                steps(p0, ring[n], masked, later);
+            else
+                fetch_all(later);
             arrived<2 * kFetches * (kRing - 2)>();
             __syncthreads();
         };
@@ -950,6 +997,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         c.c1 = min(end, c.c0 + static_cast<int32_t>(kMaxChunk));
         first = static_cast<uint32_t>(c.c0) >> p.page_shift;
         holes = __syncthreads_or(load_pages(p, work, c, s_page));
+        fetch_first();
     }
 
     const float v_scale = kE4M3 ? p.v.scale[work.h] : 1.0f;
