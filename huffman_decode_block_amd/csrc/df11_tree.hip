@@ -21,6 +21,7 @@ constexpr uint32_t kMinChunk = kWaves * kStep;
 constexpr uint32_t kMaxChunk = 4096;  // positions whose pages LDS holds
 constexpr uint32_t kChunkPages = kMaxChunk / kMinPage + 1;
 constexpr uint32_t kPad = 4;  // floats between rows in LDS: they start in different banks
+constexpr uint32_t kSlots = 2 * kComputeUnits;  // workgroups that run at once
 constexpr uint32_t kMaskedSteps = 3;  // what looking at masks costs a chunk
 constexpr float kSlack = 8;   // powers of two that weights may grow to before their reference follows
 
@@ -161,17 +162,17 @@ __device__ __forceinline__ uint64_t out_row(const TreeParams &p, const Work &w, 
 struct Row {
     int32_t node, start;
     bool have;
-    uint64_t first;  // its mask's first word
 };
 
-__device__ __forceinline__ Row row_of(const TreeParams &p, const Work &w, const Rows &rows, uint32_t i) {
+__device__ __forceinline__ Row row_of(const TreeParams &p, const Work &w, const Rows &rows, uint32_t i, uint64_t *first) {
     Row r;
     r.node = static_cast<int32_t>(min(rows.row0 + i, p.nodes * p.group - 1) / p.group);
     r.have = i < rows.rows && r.node < rows.count;
     r.start = 0;
     if (p.starts)
         r.start = min(max(p.starts[w.b * p.starts_batch + static_cast<uint32_t>(r.node) * p.starts_node], 0), rows.len);
-    r.first = p.mask ? static_cast<uint64_t>(p.mask[w.b * p.mask_batch + static_cast<uint32_t>(r.node) * p.mask_node]) : 0;
+    // its mask's first word is looked at seldom: LDS keeps it
+    if (p.mask) *first = static_cast<uint64_t>(p.mask[w.b * p.mask_batch + static_cast<uint32_t>(r.node) * p.mask_node]);
     return r;
 }
 
@@ -248,7 +249,8 @@ __device__ __forceinline__ uint32_t positions_there(const TreeParams &p, const C
 }
 
 // Those that a row reads.
-__device__ __forceinline__ uint32_t positions_read(const TreeParams &p, const Work &w, const Rows &rows, const Row &row, int32_t p0, uint32_t q) {
+__device__ __forceinline__ uint32_t positions_read(const TreeParams &p, const Work &w, const Rows &rows, const Row &row, const uint64_t *first, int32_t p0,
+                                                   uint32_t q) {
     uint32_t live = bits_between(row.start - p0, rows.len - p0);
     const int32_t a0 = p0 - rows.len;  // the node at p0
     if (a0 + static_cast<int32_t>(kStep) > 0) {
@@ -257,7 +259,7 @@ __device__ __forceinline__ uint32_t positions_read(const TreeParams &p, const Wo
         } else if (a0 < rows.count) {
             const uint32_t from = static_cast<uint32_t>(max(a0, 0));
             const uint32_t at = from / 64, shift = from % 64;
-            uint64_t m = row.first;
+            uint64_t m = *first;
             if (p.nodes > 64) {
                 const int64_t *words = p.mask + w.b * p.mask_batch + static_cast<uint32_t>(row.node) * p.mask_node;
                 m = static_cast<uint64_t>(words[at]) >> shift;
@@ -400,8 +402,8 @@ __device__ __forceinline__ void transpose(const uint32_t (&pair)[8], v4u (&vt)[2
 // reads are infinities of either sign or NaN.  kStrided: a lane's values of V^T's
 // tile j are those of d = 16 j + r, otherwise of d = r kDim / 16 + j.
 template <int kDim, bool kE4M3, int kTiles, bool kStrided>
-__device__ __forceinline__ void add_counts(const TreeParams &p, const Work &work, const Rows &rows, const Row (&row)[kTiles], const uint8_t *vb,
-                                           const int32_t *s_page, const Chunk &c, int32_t p0, Running<kDim / 16> (&run)[kTiles]) {
+__device__ __forceinline__ void add_counts(const TreeParams &p, const Work &work, const Rows &rows, const Row (&row)[kTiles], const uint64_t *s_first,
+                                           const uint8_t *vb, const int32_t *s_page, const Chunk &c, int32_t p0, Running<kDim / 16> (&run)[kTiles]) {
     constexpr int kPiece = kDim / 16;
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift, in_page = (1u << p.page_shift) - 1;
@@ -409,7 +411,7 @@ __device__ __forceinline__ void add_counts(const TreeParams &p, const Work &work
     v4u ones[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        const uint32_t live = positions_read(p, work, rows, row[t], p0, q) & there;
+        const uint32_t live = positions_read(p, work, rows, row[t], &s_first[16 * t + r], p0, q) & there;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             ones[t][i] = (live >> (2 * i) & 1u ? 0x3F80u : 0u) | (live >> (2 * i + 1) & 1u ? 0x3F800000u : 0u);
@@ -450,6 +452,7 @@ tree_few_kernel(TreeParams p) {
     constexpr int kVWords = kPiece * (kE4M3 ? 1 : 2) / 4;  // dwords of a V piece
     constexpr uint32_t kRows = 16 * kTiles;
     __shared__ int32_t s_page[kChunkPages];
+    __shared__ uint64_t s_first[kRows];
     __shared__ float s_stat[kWaves][2][16];
     __shared__ __attribute__((aligned(16))) float s_out[kWaves][16][kDim + kPad];
 
@@ -462,7 +465,7 @@ tree_few_kernel(TreeParams p) {
     int32_t lo = rows.len, lo_max = 0;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        row[t] = row_of(p, work, rows, 16 * t + r);
+        row[t] = row_of(p, work, rows, 16 * t + r, &s_first[16 * t + r]);
         lo = row[t].have ? min(lo, row[t].start) : lo;
         lo_max = row[t].have ? max(lo_max, row[t].start) : lo_max;
     }
@@ -549,7 +552,7 @@ tree_few_kernel(TreeParams p) {
         if (__builtin_expect(masked, false)) {
             const uint32_t there = positions_there(p, c, s_page, p0, q);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) mask_scores(s[t], positions_read(p, work, rows, row[t], p0, q) & there);
+            for (int t = 0; t < kTiles; ++t) mask_scores(s[t], positions_read(p, work, rows, row[t], &s_first[16 * t + r], p0, q) & there);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (!(there >> i & 1u)) vr[i] = 0;
@@ -597,7 +600,7 @@ tree_few_kernel(TreeParams p) {
             for (int32_t p0 = wave0; p0 < c.c1; p0 += kWaves * kStep) step(p0, p0 + kWaves * kStep);
             if (__builtin_expect(__any(odd != 0), 0))
                 for (int32_t p0 = wave0; p0 < c.c1; p0 += kWaves * kStep)
-                    if (masked_at(c, holes, p0, kStep)) add_counts<kDim, kE4M3, kTiles, false>(p, work, rows, row, vb, s_page, c, p0, run);
+                    if (masked_at(c, holes, p0, kStep)) add_counts<kDim, kE4M3, kTiles, false>(p, work, rows, row, s_first, vb, s_page, c, p0, run);
             odd = 0;
         }
         if (c.c1 >= end) break;
@@ -676,13 +679,21 @@ __device__ __forceinline__ uint32_t v_turn(uint32_t row) {
 }
 
 // 16 bytes for each lane, from its offset, into LDS next to each other from `to` on
-// (uniform).  By hand: behind the builtin the compiler lets transposing
+// (uniform, like the base).  By hand: behind the builtin the compiler lets transposing
 // reads of other arrays wait for it, too.  Nothing is returned to a register, and
-// arrived() waits for what was loaded.
-__device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint8_t *to) {
-    typedef __attribute__((address_space(3))) uint8_t *Lds;
-    const uint32_t place = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((Lds)(to))));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(place), "v"(from + offset) : "memory", "m0");
+// arrived() waits for what was loaded.  A scalar register that the vector unit wrote
+// is there for memory's instructions five cycles later.  Nothing else here uses m0.
+__device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(from) : "memory");
+}
+
+// The same from two bases.
+__device__ __forceinline__ void load_lds(const uint8_t *from, const uint8_t *from2, bool second, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"((second ? from2 : from) + offset) : "memory");
+}
+
+__device__ __forceinline__ uint32_t place_of(uint8_t *stage) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)(stage)));
 }
 
 // Waits for this wave's loads but the last kAfter, those into LDS among them: a
@@ -701,6 +712,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     constexpr uint32_t kRing = kE4M3 ? 4 : 2;  // stages, 64 KiB
     static_assert(kStage % (kStep * kGroups) == 0 && kTiles * kPiece * 1024 <= 2 * kBytes * kRing / kManyWaves, "stages hold what the waves join");
     __shared__ int32_t s_page[kChunkPages];
+    __shared__ uint64_t s_first[kRows];
     __shared__ int32_t s_reads[2][kManyWaves];
     __shared__ float s_stat[kManyWaves][kTiles][2][16];
     // K and V of each stage: arrays of their own, as the compiler waits for loads into
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     int32_t lo = rows.len, lo_max = 0;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        row[t] = row_of(p, work, rows, wave_row + 16 * t + r);
+        row[t] = row_of(p, work, rows, wave_row + 16 * t + r, &s_first[wave_row + 16 * t + r]);
         lo = row[t].have ? min(lo, row[t].start) : lo;
         lo_max = row[t].have ? max(lo_max, row[t].start) : lo_max;
     }
@@ -790,9 +802,9 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
     constexpr uint32_t kEights = kLoadRows > 8 ? 2 : 1;
     struct Fetch {
         const uint8_t *k[kFetches][kEights], *v[kFetches][kEights];
-        uint8_t *to;
+        uint32_t to;
     };
-    auto find = [&](int32_t p0, uint8_t *to) {
+    auto find = [&](int32_t p0, uint32_t to) {
         uint32_t at[kFetches][kEights];
         int32_t page[kFetches][kEights];
 #pragma unroll
@@ -816,21 +828,33 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             }
         return f;
     };
+    uint32_t from_k[kFetches], from_v[kFetches];  // of a lane, from where its eight rows begin
+#pragma unroll
+    for (uint32_t i = 0; i < kFetches; ++i) {
+        const uint32_t row = (i * kManyWaves + wave) * kLoadRows + lane / kPieces, place = lane % kPieces;
+        from_k[i] = row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim, kE4M3>(row));
+        from_v[i] = row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim, kE4M3>(row));
+    }
     auto fetch = [&](const Fetch &f, uint32_t i) {
-        const uint32_t row0 = (i * kManyWaves + wave) * kLoadRows, row = row0 + lane / kPieces, place = lane % kPieces;
-        const bool second = kEights > 1 && lane >= 8 * kPieces;
-        const uint8_t *k = second ? f.k[i][kEights - 1] : f.k[i][0], *v = second ? f.v[i][kEights - 1] : f.v[i][0];
-        load_lds(k, row % 8 * static_cast<uint32_t>(p.k.row) + 16 * (place ^ k_turn<kDim, kE4M3>(row)), f.to + row0 * kRowBytes);
-        load_lds(v, row % 8 * static_cast<uint32_t>(p.v.row) + 16 * (place ^ v_turn<kDim, kE4M3>(row)), f.to + kBytes + row0 * kRowBytes);
+        const uint32_t to = f.to + (i * kManyWaves + wave) * kLoadRows * kRowBytes;
+        if constexpr (kEights > 1) {
+            const bool second = lane >= 8 * kPieces;
+            load_lds(f.k[i][0], f.k[i][1], second, from_k[i], to);
+            load_lds(f.v[i][0], f.v[i][1], second, from_v[i], to + kBytes);
+        } else {
+            load_lds(f.k[i][0], from_k[i], to);
+            load_lds(f.v[i][0], from_v[i], to + kBytes);
+        }
     };
     auto fetch_all = [&](const Fetch &f) {
 #pragma unroll
         for (uint32_t i = 0; i < kFetches; ++i) fetch(f, i);
     };
     uint8_t *const ring[4] = {s_ring0, s_ring1, s_ring2, s_ring3};
+    const uint32_t places[4] = {place_of(s_ring0), place_of(s_ring1), place_of(s_ring2), place_of(s_ring3)};
     auto fetch_first = [&] {
 #pragma unroll
-        for (uint32_t i = 0; i + 1 < kRing; ++i) fetch_all(find(c.c0 + static_cast<int32_t>(i * kStage), ring[i]));
+        for (uint32_t i = 0; i + 1 < kRing; ++i) fetch_all(find(c.c0 + static_cast<int32_t>(i * kStage), places[i]));
     };
     auto clean_stage = [&](int32_t p0, uint8_t *stage) {  // what has arrived
         constexpr uint32_t kEach = kStage * kPieces / kThreads;
@@ -858,6 +882,23 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
 
     Running<kPiece> run[kTiles];
     constexpr int kSteps = kStage / (kStep * kGroups);  // of a wave in a stage
+    // Where a lane reads in a stage: rows 16 and 32 further on take their pieces in the
+    // same order, so that steps and stages are constants of the instructions.  Unknown
+    // to the compiler, which would keep these places for each stage.
+    constexpr int kKReads = kE4M3 ? kKChunks / 2 : kKChunks;  // 16 bytes of a K row each
+    uint32_t k_at[kKReads], v_at[kPiece];
+#pragma unroll
+    for (int i = 0; i < kKReads; ++i) {
+        k_at[i] = (group * kStep + r) * kRowBytes + 16 * ((4 * i + q) ^ k_turn<kDim, kE4M3>(r));
+        asm("" : "+v"(k_at[i]));
+    }
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+        const uint32_t at = kE4M3 ? 16 * (r / 8) + 4 * q + (r / 2 & 3u) : 4 * q + r / 4;
+        v_at[j] = kBytes + (group * kStep + at) * kRowBytes + 8 * (r & 1u) +
+                  16 * ((kE4M3 ? j : 2 * j + (r & 3u) / 2) ^ v_turn<kDim, kE4M3>(at));
+        asm("" : "+v"(v_at[j]));
+    }
     // A wave's steps of a stage, positions p0 and on: all scores first, then a step's
     // weights beside the product of those before.  Loads of a later stage go out
     // between them, as a compute unit takes 64 bytes of them in a cycle.
@@ -872,13 +913,11 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         // reads from LDS stay a group ahead of what takes them: nothing of them is
         // moved over these places, all else is
         const auto keep_reads = [] { __builtin_amdgcn_sched_barrier(0x7F); };
-        constexpr int kKReads = kE4M3 ? kKChunks / 2 : kKChunks;  // 16 bytes of a K row each
         v4u kf[2][kKReads];
         const auto read_k = [&](int n) {
-            const uint32_t at = (n / 2 * kGroups + group) * kStep + 16 * (n & 1);
 #pragma unroll
             for (int i = 0; i < kKReads; ++i)
-                kf[n & 1][i] = *reinterpret_cast<const v4u *>(stage + (at + r) * kRowBytes + 16 * ((4 * i + q) ^ k_turn<kDim, kE4M3>(16 * (n & 1) + r)));
+                kf[n & 1][i] = *reinterpret_cast<const v4u *>(stage + k_at[i] + (n / 2 * kGroups * kStep + 16 * (n & 1)) * kRowBytes);
         };
         read_k(0);
 #pragma unroll
@@ -898,19 +937,15 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
         constexpr int kBlock = 4, kBlocks = kPiece / kBlock;  // of V^T's tiles
         v2u vt[2][kBlock][kE4M3 ? 1 : 2];
         const auto read_v = [&](int n) {
-            const uint8_t *from = stage + kBytes + (n / kBlocks * kGroups + group) * kStep * kRowBytes;
+            const uint8_t *from = stage + n / kBlocks * kGroups * kStep * kRowBytes;
 #pragma unroll
             for (int j = 0; j < kBlock; ++j) {
-                const uint32_t tile = n % kBlocks * kBlock + j;
+                const uint32_t at = v_at[n % kBlocks * kBlock + j];
                 if (kE4M3) {
-                    const uint32_t at = 16 * (r / 8) + 4 * q + (r / 2 & 3u);
-                    vt[n & 1][j][0] = read_transposed8(from + at * kRowBytes + 16 * (tile ^ v_turn<kDim, true>(at)) + 8 * (r & 1u));
+                    vt[n & 1][j][0] = read_transposed8(from + at);
                 } else {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t at = 16 * u + 4 * q + r / 4;
-                        vt[n & 1][j][kE4M3 ? 0 : u] = read_transposed(from + at * kRowBytes + 16 * ((2 * tile + (r & 3u) / 2) ^ v_turn<kDim, false>(at)) + 8 * (r & 1u));
-                    }
+                    for (int u = 0; u < 2; ++u) vt[n & 1][j][kE4M3 ? 0 : u] = read_transposed(from + at + 16 * u * kRowBytes);
                 }
             }
         };
@@ -922,7 +957,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 const int32_t at = p0 + static_cast<int32_t>((n * kGroups + group) * kStep);
                 const uint32_t there = positions_there(p, c, s_page, at, q);
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) mask_scores(s[n][t], positions_read(p, work, rows, row[t], at, q) & there);
+                for (int t = 0; t < kTiles; ++t) mask_scores(s[n][t], positions_read(p, work, rows, row[t], &s_first[wave_row + 16 * t + r], at, q) & there);
             }
         }
 #pragma unroll
@@ -969,7 +1004,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
                 clean_stage(p0, ring[n]);
                 __syncthreads();
             }
-            const Fetch later = find(p0 + static_cast<int32_t>((kRing - 1) * kStage), ring[(n + kRing - 1) % kRing]);
+            const Fetch later = find(p0 + static_cast<int32_t>((kRing - 1) * kStage), places[(n + kRing - 1) % kRing]);
             if (active)
                 steps(p0, ring[n], masked, later);
             else
@@ -989,7 +1024,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             for (int32_t p0 = c.c0; p0 < c.c1; p0 += kStage)
                 if (masked_at(c, holes, p0, kStage))
                     for (uint32_t at = kStep * group; at < kStage && p0 + static_cast<int32_t>(at) < c.c1; at += kStep * kGroups)
-                        add_counts<kDim, kE4M3, kTiles, true>(p, work, rows, row, vb, s_page, c, p0 + static_cast<int32_t>(at), run);
+                        add_counts<kDim, kE4M3, kTiles, true>(p, work, rows, row, s_first + wave_row, vb, s_page, c, p0 + static_cast<int32_t>(at), run);
         if (c.c1 >= end) break;
         __syncthreads();
         odd = 0;
@@ -1141,12 +1176,12 @@ struct Shape {
 Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads, uint32_t dim, uint64_t positions) {
     const uint64_t rows = nodes * group;
     Shape s;
-    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    s.rows = rows <= 16 ? 16 : rows <= 32 && dim < 256 ? 32 : 64;
     const uint64_t large = batch * kv_heads * ((rows + 127) / 128);  // workgroups with all positions
     if (rows > 64 && dim < 256 && large * positions >= 2 * kComputeUnits * kLargeChunk) s.rows = 128;
     s.tiles = static_cast<uint32_t>((rows + s.rows - 1) / s.rows);
-    const uint64_t units = batch * kv_heads * s.tiles, wanted = 2 * kComputeUnits;
-    const uint64_t want = (wanted + units - 1) / std::max<uint64_t>(units, 1);
+    const uint64_t units = batch * kv_heads * s.tiles;
+    const uint64_t want = (kSlots + units - 1) / std::max<uint64_t>(units, 1);
     const uint64_t most = (positions + kMinChunk - 1) / kMinChunk;
     s.splits = static_cast<uint32_t>(positions <= 2 * kMinChunk ? 1 : std::min(want, most));
     return s;
@@ -1176,10 +1211,10 @@ auto kernel_of(bool e4m3, uint32_t rows) {
     if constexpr (kDim == 256) {
         if (rows == 64) return e4m3 ? tree_many_kernel<kDim, true, 1, 1> : tree_many_kernel<kDim, false, 1, 1>;
     } else {
+        if (rows == 32) return e4m3 ? tree_few_kernel<kDim, true, 2> : tree_few_kernel<kDim, false, 2>;
         if (rows == 128) return e4m3 ? tree_many_kernel<kDim, true, 2, 1> : tree_many_kernel<kDim, false, 2, 1>;
         if (rows == 64) return e4m3 ? tree_many_kernel<kDim, true, 2, 2> : tree_many_kernel<kDim, false, 2, 2>;
     }
-    if (rows == 32) return e4m3 ? tree_few_kernel<kDim, true, 2> : tree_few_kernel<kDim, false, 2>;
     return e4m3 ? tree_few_kernel<kDim, true, 1> : tree_few_kernel<kDim, false, 1>;
 }
 
