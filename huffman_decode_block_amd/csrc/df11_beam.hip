@@ -26,6 +26,7 @@ constexpr uint32_t kThreads = 256, kWaves = kThreads / 64;
 constexpr uint32_t kMaxK = 64;
 constexpr uint32_t kRoom = 1024;  // values that may reach t before they are sought one by one
 constexpr uint32_t kEach = 8;     // values of a load
+constexpr uint32_t kAtOnce = 8;   // values compared with one: their reads from LDS overlap
 
 struct BeamParams {
     const void *logits;
@@ -77,57 +78,72 @@ struct __attribute__((packed, aligned(4))) EightFloats {
     float x[8];
 };
 
-// Eight tokens' logits from `at` on; -infinity from `end` on.
+// Eight tokens' logits as they are in memory: BF16 takes half of the registers.
 template <bool kF32>
-__device__ __forceinline__ void load_logits(const void *row, uint32_t at, uint32_t end, float (&x)[kEach]) {
+struct Eight {
+    uint32_t w[kF32 ? 8 : 4];
+    __device__ __forceinline__ float operator[](int j) const {
+        if (kF32) return __builtin_bit_cast(float, w[j % (kF32 ? 8 : 4)]);
+        return __builtin_bit_cast(float, j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    }
+};
+
+// Those from `at` on; -infinity from `end` on.
+template <bool kF32>
+__device__ __forceinline__ Eight<kF32> load_logits(const void *row, uint32_t at, uint32_t end) {
+    Eight<kF32> x;
     if (at + kEach <= end) {
         if (kF32) {
             const EightFloats w = *reinterpret_cast<const EightFloats *>(static_cast<const float *>(row) + at);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = w.x[i];
+            for (int i = 0; i < (kF32 ? 8 : 4); ++i) x.w[i] = __builtin_bit_cast(uint32_t, w.x[i]);
         } else {
             const v4u w = load8(static_cast<const uint16_t *>(row) + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-                x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
-            }
+            for (int i = 0; i < 4; ++i) x.w[i] = w[i];
         }
+    } else if (kF32) {
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 8 : 4); ++i)
+            x.w[i] = at + i < end ? static_cast<const uint32_t *>(row)[at + i] : 0xFF800000u;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = -INFINITY;
-            if (at + i < end)
-                x[i] = kF32 ? static_cast<const float *>(row)[at + i]
-                            : __builtin_bit_cast(float, uint32_t{static_cast<const uint16_t *>(row)[at + i]} << 16);
+        for (int i = 0; i < 4; ++i) {
+            const uint16_t *from = static_cast<const uint16_t *>(row) + at + 2 * i;
+            x.w[i] = (at + 2 * i < end ? from[0] : 0xFF80u) | (at + 2 * i + 1 < end ? from[1] : 0xFF80u) << 16;
         }
     }
+    return x;
 }
 
 template <bool kF32, int kLoads>
 __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
     __shared__ float s_max[kWaves], s_sum[kWaves], s_reach[kWaves];
-    __shared__ float s_x[kRoom];
-    __shared__ uint32_t s_at[kRoom];
+    __shared__ __attribute__((aligned(16))) float s_x[kRoom + kAtOnce];
+    __shared__ __attribute__((aligned(16))) uint32_t s_at[kRoom + kAtOnce];
     __shared__ uint32_t s_n;
     const uint32_t row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
-    if (p.done && p.done[row]) return;
-    if (!(fabsf(p.scores[row]) < INFINITY)) return;
+    const float score = p.scores[row];
+    const bool done = p.done && p.done[row];
+    if (done || !(fabsf(score) < INFINITY)) return;
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint32_t b = row / p.beams;
     const uint64_t first = b * p.batch_stride + (row - b * p.beams) * p.beam_stride;
     const void *logits = static_cast<const uint8_t *>(p.logits) + first * (kF32 ? 4 : 2);
     const uint32_t begin = part * p.part, end = min(begin + p.part, p.vocab);
 
-    float x[kLoads][kEach];
+    Eight<kF32> x[kLoads];
     const auto token = [&](int i, int j) { return begin + (i * kThreads + threadIdx.x) * kEach + j; };
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_logits<kF32>(logits, token(i, 0), end, x[i]);
-    float top = -INFINITY;  // NaN aside, which makes the sum NaN
+    for (int i = 0; i < kLoads; ++i) x[i] = load_logits<kF32>(logits, token(i, 0), end);
+    float top = -INFINITY, tops[kLoads];  // NaN aside, which makes the sum NaN
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
+    for (int i = 0; i < kLoads; ++i) {
+        tops[i] = x[i][0];
 #pragma unroll
-        for (int j = 0; j < static_cast<int>(kEach); ++j) top = fmaxf(top, x[i][j]);
+        for (int j = 1; j < static_cast<int>(kEach); ++j) tops[i] = fmaxf(tops[i], x[i][j]);
+        top = fmaxf(top, tops[i]);
+    }
     const float reach = reached_by(top, p.k), wave_top = wave_max(top);
     if (lane == 0) {
         s_max[wave] = wave_top;
@@ -141,6 +157,14 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
         m = fmaxf(m, s_max[w]);
         t = fmaxf(t, s_reach[w]);
     }
+    // unpacked anew each time: kept, the floats would take twice the registers
+    const auto as_loaded = [&] {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (uint32_t &w : x[i].w) asm volatile("" : "+v"(w));
+    };
+    as_loaded();
     const float from = m == -INFINITY ? 0.0f : m;
     float sum = 0;
 #pragma unroll
@@ -152,10 +176,12 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
     }
     sum = wave_sum(sum);
     if (lane == 0) s_sum[wave] = sum;
+    as_loaded();
 
-    // values that reach t
+    // values that reach t: most loads have none in a whole wave
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
+    for (int i = 0; i < kLoads; ++i) {
+        if (!__any(tops[i] >= t)) continue;
 #pragma unroll
         for (int j = 0; j < static_cast<int>(kEach); ++j)
             if (x[i][j] >= t && x[i][j] > -INFINITY) {
@@ -165,6 +191,7 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
                     s_at[n] = token(i, j);
                 }
             }
+    }
     __syncthreads();
     uint32_t n = s_n;
     const uint64_t out = (uint64_t{row} * p.parts + part) * p.k;
@@ -183,6 +210,7 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
         uint32_t last_at = 0;
         bool started = false;
         for (uint32_t i_out = 0; i_out < p.k; ++i_out) {
+            as_loaded();
             float best = -INFINITY;
             uint32_t best_at = UINT_MAX;
 #pragma unroll
@@ -225,11 +253,21 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
         }
         return;
     }
+    if (threadIdx.x < kAtOnce) s_x[n + threadIdx.x] = -INFINITY;
+    __syncthreads();
     for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
         const float v = s_x[i];
         const uint32_t at = s_at[i];
         uint32_t rank = 0;
-        for (uint32_t j = 0; j < n; ++j) rank += s_x[j] > v || (s_x[j] == v && s_at[j] < at);
+        for (uint32_t j = 0; j < n; j += kAtOnce) {
+#pragma unroll
+            for (uint32_t e = 0; e < kAtOnce; e += 4) {
+                const f4 o = *reinterpret_cast<const f4 *>(&s_x[j + e]);
+                const v4u o_at = *reinterpret_cast<const v4u *>(&s_at[j + e]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) rank += (o[k] > v) | ((o[k] == v) & (o_at[k] < at));
+            }
+        }
         if (rank < p.k) {
             p.best[out + rank] = v;
             p.at[out + rank] = static_cast<int32_t>(at);
@@ -247,70 +285,103 @@ struct Candidate {
 };
 
 __device__ __forceinline__ bool better(const Candidate &a, const Candidate &b) {
-    if (a.score != b.score) return a.score > b.score;
-    if (a.beam != b.beam) return a.beam < b.beam;
-    if (a.x != b.x) return a.x > b.x;
-    return a.token < b.token;
+    // without branches: ties are common among BF16 logits
+    const bool token = a.token < b.token, x = (a.x > b.x) | ((a.x == b.x) & token);
+    const bool beam = (a.beam < b.beam) | ((a.beam == b.beam) & x);
+    return (a.score > b.score) | ((a.score == b.score) & beam);
 }
 
 constexpr uint32_t kMaxBeams = 1024;
+constexpr uint32_t kHeld = 4;  // candidates that a thread holds in registers
 
 __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
     __shared__ double s_lse[kMaxBeams];  // NaN for a beam that offers no token
-    __shared__ double s_score[kRoom];
-    __shared__ float s_x[kRoom];
-    __shared__ uint32_t s_beam[kRoom], s_token[kRoom];
+    __shared__ float s_from[kMaxBeams];  // the beams' scores
+    __shared__ uint8_t s_done[kMaxBeams];
+    __shared__ __attribute__((aligned(16))) double s_score[kRoom + kAtOnce];
+    __shared__ __attribute__((aligned(16))) float s_x[kRoom + kAtOnce];
+    __shared__ __attribute__((aligned(16))) uint32_t s_beam[kRoom + kAtOnce], s_token[kRoom + kAtOnce];
     __shared__ float s_reach[kWaves];
     __shared__ uint32_t s_n;
     const uint32_t b = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint64_t row0 = uint64_t{b} * p.beams;
 
-    for (uint32_t i = wave; i < p.beams; i += kWaves) {
-        const uint64_t row = row0 + i;
-        const bool open = !(p.done && p.done[row]) && fabsf(p.scores[row]) < INFINITY;
-        double lse = NAN;
-        if (open) {
-            const v2f *sums = reinterpret_cast<const v2f *>(p.sums) + row * p.parts;
-            float m = -INFINITY;
-            for (uint32_t c = lane; c < p.parts; c += 64) m = fmaxf(m, sums[c].x);
-            m = wave_max(m);
-            double sum = 0;
-            for (uint32_t c = lane; c < p.parts; c += 64) {
-                const v2f s = sums[c];
-                sum += s.x == -INFINITY ? static_cast<double>(s.y != s.y ? NAN : 0.0f)
-                                        : static_cast<double>(s.y) * exp(static_cast<double>(s.x) - static_cast<double>(m));
-            }
-            for (int k = 32; k; k >>= 1) sum += __shfl_xor(sum, k);
-            lse = static_cast<double>(m) + log(sum);
+    // candidate c: place c % k of part c / k of a beam; a beam that has ended has one,
+    // its first.  A thread's first ones are on their way while the beams' sums are
+    // added; what a beam without tokens has there is not looked at.
+    const uint32_t per_beam = p.parts * p.k, all = per_beam * p.beams;
+    float held_x[kHeld];
+    int32_t held_at[kHeld];
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h) {
+        const uint32_t c = min(h * kThreads + threadIdx.x, all - 1);
+        held_x[h] = p.best[row0 * per_beam + c];
+        held_at[h] = p.at[row0 * per_beam + c];
+    }
+    // as many lanes for a beam as there are, a power of two
+    const uint32_t share = min(64u, kThreads >> (32 - __builtin_clz(min(p.beams, kThreads) * 2 - 1) - 1)), mine = threadIdx.x % share;
+    for (uint32_t i0 = 0; i0 < p.beams; i0 += kThreads / share) {
+        const uint32_t i = i0 + threadIdx.x / share;
+        const uint64_t row = row0 + min(i, p.beams - 1);
+        const v2f *sums = reinterpret_cast<const v2f *>(p.sums) + row * p.parts;
+        v2f s[2];  // the first of a lane's parts
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) s[h] = sums[min(mine + h * share, p.parts - 1)];
+        const float from = p.scores[row];
+        const bool done = p.done && p.done[row];
+        float m = -INFINITY;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            if (mine + h * share < p.parts) m = fmaxf(m, s[h].x);
+        for (uint32_t c = mine + 2 * share; c < p.parts; c += share) m = fmaxf(m, sums[c].x);
+        for (uint32_t k = share / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+        const auto part = [&](v2f x) {
+            return x.x == -INFINITY ? static_cast<double>(x.y != x.y ? NAN : 0.0f)
+                                    : static_cast<double>(x.y) * exp(static_cast<double>(x.x) - static_cast<double>(m));
+        };
+        double sum = 0;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            if (mine + h * share < p.parts) sum += part(s[h]);
+        for (uint32_t c = mine + 2 * share; c < p.parts; c += share) sum += part(sums[c]);
+        for (uint32_t k = share / 2; k; k >>= 1) sum += __shfl_xor(sum, k);
+        if (mine == 0 && i < p.beams) {
+            s_lse[i] = done || !(fabsf(from) < INFINITY) ? static_cast<double>(NAN) : static_cast<double>(m) + log(sum);
+            s_from[i] = from;
+            s_done[i] = done;
         }
-        if (lane == 0) s_lse[i] = lse;
     }
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
 
-    // candidate c: place c % k of part c / k of a beam; a beam that has ended has one, its first
-    const uint32_t per_beam = p.parts * p.k, all = per_beam * p.beams;
-    const auto candidate = [&](uint32_t c, Candidate &out) {
+    const auto of = [&](uint32_t c, float x, int32_t token, Candidate &out) {
         const uint32_t beam = c / per_beam;
-        const uint64_t row = row0 + beam;
         out.beam = beam;
-        if (p.done && p.done[row]) {
-            out.score = p.scores[row];
+        if (s_done[beam]) {
+            out.score = s_from[beam];
             out.x = 0;
             out.token = static_cast<uint32_t>(p.pad);
-            return c == beam * per_beam && fabsf(p.scores[row]) < INFINITY;
+            return c == beam * per_beam && fabsf(s_from[beam]) < INFINITY;
         }
         const double lse = s_lse[beam];
-        if (!(fabs(lse) < INFINITY)) return false;
-        const uint64_t at = row * per_beam + (c - beam * per_beam);
-        out.x = p.best[at];
-        if (!(out.x > -INFINITY)) return false;
-        out.token = static_cast<uint32_t>(p.at[at]);
-        out.score = static_cast<double>(p.scores[row]) + (static_cast<double>(out.x) - lse);
-        return true;
+        out.x = x;
+        out.token = static_cast<uint32_t>(token);
+        out.score = static_cast<double>(s_from[beam]) + (static_cast<double>(x) - lse);
+        return fabs(lse) < INFINITY && x > -INFINITY;
+    };
+    const auto candidate = [&](uint32_t c, Candidate &out) {
+        const uint64_t at = row0 * per_beam + c;
+        return of(c, p.best[at], p.at[at], out);
     };
     float top = -INFINITY;
-    for (uint32_t c = threadIdx.x; c < all; c += kThreads) {
+    Candidate held[kHeld];
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h) {
+        const uint32_t c = h * kThreads + threadIdx.x;
+        if (c >= all || !of(c, held_x[h], held_at[h], held[h])) held[h].score = -INFINITY;
+        top = fmaxf(top, static_cast<float>(held[h].score));
+    }
+    for (uint32_t c = kHeld * kThreads + threadIdx.x; c < all; c += kThreads) {
         Candidate x;
         if (candidate(c, x)) top = fmaxf(top, static_cast<float>(x.score));
     }
@@ -320,17 +391,21 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
     float t = s_reach[0];
 #pragma unroll
     for (uint32_t w = 1; w < kWaves; ++w) t = fmaxf(t, s_reach[w]);
-    for (uint32_t c = threadIdx.x; c < all; c += kThreads) {
-        Candidate x;
-        if (candidate(c, x) && static_cast<float>(x.score) >= t) {
-            const uint32_t n = atomicAdd(&s_n, 1u);
-            if (n < kRoom) {
-                s_score[n] = x.score;
-                s_beam[n] = x.beam;
-                s_x[n] = x.x;
-                s_token[n] = x.token;
-            }
+    const auto keep = [&](const Candidate &x) {
+        const uint32_t n = atomicAdd(&s_n, 1u);
+        if (n < kRoom) {
+            s_score[n] = x.score;
+            s_beam[n] = x.beam;
+            s_x[n] = x.x;
+            s_token[n] = x.token;
         }
+    };
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h)
+        if (held[h].score > -INFINITY && static_cast<float>(held[h].score) >= t) keep(held[h]);
+    for (uint32_t c = kHeld * kThreads + threadIdx.x; c < all; c += kThreads) {
+        Candidate x;
+        if (candidate(c, x) && static_cast<float>(x.score) >= t) keep(x);
     }
     __syncthreads();
     const uint32_t n = s_n;
@@ -373,10 +448,15 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
             last = best;
         }
     } else {
+        if (threadIdx.x < kAtOnce) s_score[n + threadIdx.x] = -INFINITY;
+        __syncthreads();
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
             const Candidate mine = {s_score[i], s_beam[i], s_x[i], s_token[i]};
             uint32_t rank = 0;
-            for (uint32_t j = 0; j < n; ++j) rank += better(Candidate{s_score[j], s_beam[j], s_x[j], s_token[j]}, mine);
+            for (uint32_t j = 0; j < n; j += kAtOnce)
+#pragma unroll
+                for (uint32_t e = 0; e < kAtOnce; ++e)
+                    rank += better(Candidate{s_score[j + e], s_beam[j + e], s_x[j + e], s_token[j + e]}, mine);
             if (rank < p.k) write(rank, mine);
         }
     }
