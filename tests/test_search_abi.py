@@ -176,3 +176,18 @@ def test_host_tensors_are_refused():
         hdb.df11_paged_fork(i, i.view(2, 1), i, i, 16)
     with pytest.raises(TypeError):
         hdb.df11_beam_select(torch.zeros(1, 2, 5), torch.zeros(1, 2), 2)
+
+
+def test_no_kernel_of_these_keeps_registers_in_memory():
+    """The compiler may store a vector register before the lanes that a loop left behind are on again, so that they
+    read back what was there before: seen where a kernel of these had more values than registers."""
+    built = open(hdb.LIB_PATH, "rb").read()
+    seen = set()
+    for m in re.finditer(rb"(_ZN12_GLOBAL__N_1\d+((?:tree|beam|fork)_\w+?_kernel|copy_kernel|compact_kernel)\w*)\.kd", built):
+        count = re.compile(rb"\.vgpr_spill_count(.)", re.S).search(built, m.end())
+        if count is None or count.start() - m.end() > 400:
+            continue  # a name elsewhere than in the kernel's description
+        seen.add(m.group(2).decode())
+        assert count.group(1) == b"\0", m.group(1)
+    assert {"tree_few_kernel", "tree_many_kernel", "tree_join_kernel", "beam_part_kernel", "beam_choose_kernel", "fork_plan_kernel",
+            "fork_table_kernel", "copy_kernel", "compact_kernel"} <= seen
