@@ -216,6 +216,46 @@ def test_many_sequences(torch, batch):
     check(torch, *build(torch, lens, 6, 2, 4, 64, 16, False, counts=[i % 7 for i in range(batch)]))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,nodes,chain", [([700], 65, False), ([900, 33, 0, 4200], 40, False), ([2500, 60, 1], 130, True)])
+def test_wide_tables(torch, fp8, dim, lens, nodes, chain):
+    """Tables for far more positions than there are: the largest tiles of rows, short chunks."""
+    say(f"tree in a wide table, lens {lens} nodes {nodes} dim {dim} chain={chain} fp8={fp8}")
+    a, reads = build(torch, lens, nodes, 2, 4, dim, 32, fp8, chain=chain)
+    table = torch.full((len(lens), 1 << 15), -1, dtype=torch.int32, device="cuda")
+    table[:, :a["page_table"].shape[1]] = a["page_table"]
+    a["page_table"] = table
+    check(torch, a, reads)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch,nodes,dim", [(2, 40, 128), (17, 3, 128), (64, 9, 64), (65, 9, 64), (24, 12, 256)])
+def test_ragged_batches(torch, batch, nodes, dim, fp8):
+    """One long sequence among short and empty ones, with and without windows."""
+    say(f"ragged batch of {batch}, nodes {nodes} dim {dim} fp8={fp8}")
+    lens = [(97 * i * i) % 160 for i in range(batch)]
+    lens[batch // 2] = 6000
+    a, reads = build(torch, lens, nodes, 1, 4, dim, 16, fp8, counts=[max(0, nodes - i % 5) for i in range(batch)])
+    check(torch, a, reads)
+    a["starts"] = (a["lens"].view(-1, 1) - torch.arange(nodes, device="cuda") * 7 - 50).int()
+    check(torch, a, reads)
+    a["lens"] = torch.zeros_like(a["lens"])
+    a["starts"] = None
+    a["nodes"] = torch.zeros_like(a["lens"])
+    out, lse = hdb.df11_paged_tree_attention(**a)
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("fp8,dim,nodes", [(False, 64, 3), (True, 64, 33), (True, 128, 2), (False, 256, 20)])
+def test_long_chunks(torch, fp8, dim, nodes):
+    """More positions for a workgroup than it keeps the pages of at a time."""
+    heads = 520 if dim == 64 else 260
+    say(f"{heads} heads behind 4,700 positions, nodes {nodes} dim {dim} fp8={fp8}")
+    batch = 520 // heads
+    check(torch, *build(torch, [4700] * batch, nodes, heads, 1, dim, 64, fp8))
+
+
 @pytest.mark.parametrize("chain", [False, True])
 @pytest.mark.parametrize("dim,fp8", [(64, False), (128, True), (256, False)])
 def test_starts(torch, dim, fp8, chain):
