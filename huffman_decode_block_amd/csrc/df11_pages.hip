@@ -150,15 +150,17 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactParams p) {
 // count: one that changes takes a holder from the old page and gives one to the
 // new.  Counts are whole numbers, so that the order of the atomics does not matter.
 // One workgroup for the plan, as a row's pages depend on what the rows before it
-// took; it looks at 16 pages of the pool in each lane at a time.  Bound by latency:
-// 6.3 + 3.2 us for 32 rows, 13.8 + 10.3 for 512 rows of up to 8,100 positions over
-// 513 columns, most of the plan's in its sums over the rows and the search for free
-// pages, of the other's in the changed entries' atomics.
+// took; it looks at 16 pages of the pool in each lane at a time, and at four entries.
+// Bound by latency, chains of parent, table, count: 6.9 + 3.7 us for 32 rows, 12.2 +
+// 7.4 for 512 rows of up to 8,100 positions over 513 columns (an entry at a time for
+// each lane: 6.4 + 3.3 and 13.8 + 10.5).
 
 constexpr uint32_t kMaxBatch = 4096;
 constexpr uint32_t kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanAhead = 16;  // pages that a lane looks at together
 constexpr uint32_t kColumns = 4;
+constexpr uint32_t kRowsAhead = 4;   // entries that a lane of the plan looks at together
+constexpr uint32_t kTableAhead = 2;  // rows that one of the table does
 
 struct ForkParams {
     const int32_t *parents;
@@ -203,38 +205,51 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
     // own pages, in order: kept ones, and -2 - n for the n-th that is wanted
     uint32_t wants = 0;
     const uint32_t entries = p.batch * p.columns;
-    for (uint32_t e0 = 0; e0 < entries; e0 += kPlanThreads) {
-        const uint32_t e = e0 + threadIdx.x;
-        int32_t own = -1;
-        bool want = false;
-        if (e < entries) {
-            const uint32_t b = e / p.columns, c = e - b * p.columns;
-            const int32_t a = parent_of(p, b);
-            if (a >= 0) {
-                const uint32_t len = s_len[a], col = (len >> p.page_shift) + c;
+    for (uint32_t e0 = 0; e0 < entries; e0 += kRowsAhead * kPlanThreads) {
+        int32_t a[kRowsAhead], page[kRowsAhead], holders[kRowsAhead];
+        uint32_t want = 0, keep = 0;  // a bit for each
+        uint64_t mask[kRowsAhead];
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            a[h] = -1;
+            if (e0 + h * kPlanThreads < entries) a[h] = parent_of(p, min(e0 + h * kPlanThreads + threadIdx.x, entries - 1) / p.columns);
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            const uint32_t e = e0 + h * kPlanThreads + threadIdx.x, b = e / p.columns;
+            page[h] = -1;
+            if (e0 + h * kPlanThreads >= entries) continue;
+            if (e < entries && a[h] >= 0) {
+                const uint32_t len = s_len[a[h]], col = (len >> p.page_shift) + (e - b * p.columns);
                 if (col < columns_of(p, len)) {
-                    want = true;
-                    if (s_first[a] == static_cast<int32_t>(b)) {
-                        const int32_t page = p.table[a * p.table_stride + col];
-                        if (is_page(p, page) && p.refs[page] <= 1) {
-                            own = page;
-                            want = false;
-                        }
-                    }
+                    want |= 1u << h;
+                    if (s_first[a[h]] == static_cast<int32_t>(b)) page[h] = p.table[a[h] * p.table_stride + col];
                 }
             }
         }
-        const uint64_t mask = __ballot(want);
-        if (lane == 0) s_count[wave] = __popcll(mask);
-        __syncthreads();
-        uint32_t at = wants;
-        for (uint32_t w = 0; w < kPlanWaves; ++w) {
-            const uint32_t n = s_count[w];
-            at += w < wave ? n : 0;
-            wants += n;
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            holders[h] = 2;
+            if (e0 + h * kPlanThreads < entries && is_page(p, page[h])) holders[h] = p.refs[page[h]];
         }
-        if (want) own = -2 - static_cast<int32_t>(at + before(mask));
-        if (e < entries) p.own[e] = own;
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            keep |= (holders[h] <= 1) << h;
+            want &= ~keep;
+            mask[h] = __ballot(want >> h & 1u);
+            if (lane == 0) s_count[h * kPlanWaves + wave] = __popcll(mask[h]);
+        }
+        __syncthreads();
+        // what comes before each of the 64 counts, a lane's each
+        static_assert(kRowsAhead * kPlanWaves == 64, "a lane for each count");
+        const uint32_t mine = s_count[lane], upto = df11w::wave_inclusive_scan(mine);
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            const uint32_t e = e0 + h * kPlanThreads + threadIdx.x;
+            const uint32_t at = wants + __builtin_amdgcn_readlane(upto - mine, h * kPlanWaves + wave) + before(mask[h]);
+            if (e < entries) p.own[e] = want >> h & 1u ? -2 - static_cast<int32_t>(at) : keep >> h & 1u ? page[h] : -1;
+        }
+        wants += __builtin_amdgcn_readlane(upto, 63);
         __syncthreads();
     }
 
@@ -285,11 +300,21 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
     found = min(found, wants);
     __syncthreads();
 
-    for (uint32_t e = threadIdx.x; e < entries; e += kPlanThreads) {
-        const int32_t own = p.own[e];
-        if (own > -2) continue;
-        const uint32_t n = static_cast<uint32_t>(-2 - own);
-        p.own[e] = n < found ? p.fresh[n] : -1;
+    for (uint32_t e0 = threadIdx.x; e0 < entries; e0 += kRowsAhead * kPlanThreads) {
+        int32_t own[kRowsAhead], page[kRowsAhead];
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            own[h] = -1;
+            if (e0 + h * kPlanThreads < entries) own[h] = p.own[e0 + h * kPlanThreads];
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h) {
+            const uint32_t n = static_cast<uint32_t>(-2 - own[h]);
+            page[h] = own[h] <= -2 && n < found ? p.fresh[n] : -1;
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < kRowsAhead; ++h)
+            if (e0 + h * kPlanThreads < entries && own[h] <= -2) p.own[e0 + h * kPlanThreads] = page[h];
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < p.batch; b += kPlanThreads) {
@@ -319,30 +344,65 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
 __global__ void __launch_bounds__(kThreads) fork_table_kernel(ForkParams p) {
     extern __shared__ int32_t s_table[];  // [batch][kColumns]
     const uint32_t col0 = blockIdx.x * kColumns;
-    const uint32_t n = p.batch * kColumns;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t b = i / kColumns, col = col0 + i % kColumns;
-        s_table[i] = col < p.width ? p.table[b * p.table_stride + col] : -1;
+    const uint32_t there = min(kColumns, p.width - col0);
+    // a thread's rows, all their columns at a time: loads of two rows are on their way together
+    for (uint32_t b0 = threadIdx.x; b0 < p.batch; b0 += kTableAhead * kThreads) {
+        int32_t e[kTableAhead][kColumns];
+#pragma unroll
+        for (uint32_t h = 0; h < kTableAhead; ++h) {
+            if (h * kThreads >= p.batch) break;
+#pragma unroll
+            for (uint32_t c = 0; c < kColumns; ++c)
+                e[h][c] = p.table[min(b0 + h * kThreads, p.batch - 1) * p.table_stride + col0 + min(c, there - 1)];
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < kTableAhead; ++h)
+#pragma unroll
+            for (uint32_t c = 0; c < kColumns; ++c)
+                if (b0 + h * kThreads < p.batch) s_table[(b0 + h * kThreads) * kColumns + c] = e[h][c];
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t b = i / kColumns, col = col0 + i % kColumns;
-        if (col >= p.width) continue;
-        const int32_t a = parent_of(p, b), old = s_table[i];
-        int32_t now = -1;
-        if (a >= 0) {
-            const uint32_t len = static_cast<uint32_t>(p.lens[b]), full = len >> p.page_shift;
-            if (col < full) {
-                now = s_table[static_cast<uint32_t>(a) * kColumns + i % kColumns];
-                if (!is_page(p, now)) now = -1;
-            } else if (col < columns_of(p, len)) {
-                now = p.own[uint64_t{b} * p.columns + (col - full)];
+    for (uint32_t b0 = threadIdx.x; b0 < p.batch; b0 += kTableAhead * kThreads) {
+        int32_t a[kTableAhead], own[kTableAhead][kColumns];
+        uint32_t len[kTableAhead];
+#pragma unroll
+        for (uint32_t h = 0; h < kTableAhead; ++h) {
+            a[h] = -1;
+            len[h] = 0;
+            if (h * kThreads >= p.batch) continue;
+            const uint32_t b = min(b0 + h * kThreads, p.batch - 1);
+            a[h] = parent_of(p, b);
+            len[h] = static_cast<uint32_t>(p.lens[b]);
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < kTableAhead; ++h) {
+            const uint32_t b = min(b0 + h * kThreads, p.batch - 1), full = len[h] >> p.page_shift, ends = columns_of(p, len[h]);
+#pragma unroll
+            for (uint32_t c = 0; c < kColumns; ++c) {
+                const uint32_t col = col0 + c;
+                own[h][c] = -1;
+                if (a[h] >= 0 && col >= full && col < ends) own[h][c] = p.own[uint64_t{b} * p.columns + (col - full)];
             }
         }
-        if (now == old) continue;
-        p.table[b * p.table_stride + col] = now;
-        if (now >= 0) atomicAdd(&p.refs[now], 1);
-        if (is_page(p, old)) atomicSub(&p.refs[old], 1);
+#pragma unroll
+        for (uint32_t h = 0; h < kTableAhead; ++h) {
+            const uint32_t b = b0 + h * kThreads, full = len[h] >> p.page_shift;
+            if (b >= p.batch) break;
+#pragma unroll
+            for (uint32_t c = 0; c < kColumns; ++c) {
+                if (c >= there) break;
+                const int32_t old = s_table[b * kColumns + c];
+                int32_t now = own[h][c];
+                if (a[h] >= 0 && col0 + c < full) {
+                    now = s_table[static_cast<uint32_t>(a[h]) * kColumns + c];
+                    if (!is_page(p, now)) now = -1;
+                }
+                if (now == old) continue;
+                p.table[b * p.table_stride + col0 + c] = now;
+                if (now >= 0) atomicAdd(&p.refs[now], 1);
+                if (is_page(p, old)) atomicSub(&p.refs[old], 1);
+            }
+        }
     }
 }
 
