@@ -1269,11 +1269,16 @@ Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads
     if (rows > 64 && dim < 256 && large * positions >= 2 * kComputeUnits * kLargeChunk) s.rows = 128;
     s.tiles = static_cast<uint32_t>((rows + s.rows - 1) / s.rows);
     const uint64_t units = batch * kv_heads * s.tiles;
-    const uint64_t want = (kSlots + units - 1) / std::max<uint64_t>(units, 1);
+    s.share = 0;
+    if (units == 0) {  // no rows: nothing to cut
+        s.splits = 1;
+        s.chunks = 0;
+        return s;
+    }
+    const uint64_t want = (kSlots + units - 1) / units;
     const uint64_t most = (positions + kMinChunk - 1) / kMinChunk;
     s.splits = static_cast<uint32_t>(positions <= 2 * kMinChunk ? 1 : std::min(want, most));
     s.chunks = batch * s.splits;
-    s.share = 0;
     if (s.splits > 1 && batch > 1 && batch <= 64) {  // a lane for each sequence
         const uint64_t at_once = kSlots / (kv_heads * s.tiles);
         s.share = static_cast<uint32_t>(at_once - batch / 2);

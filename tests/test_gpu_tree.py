@@ -491,3 +491,16 @@ def test_refusals(torch):
     assert call(q=a["q"][:0], page_table=a["page_table"][:0], lens=a["lens"][:0], tree=a["tree"][:0])[0].shape == (0, 5, 4, 128)
     out, lse = call(q=a["q"][:, :0], tree=a["tree"][:, :0, :0])
     assert out.shape == (2, 0, 4, 128) and lse.shape == (2, 0, 4)
+
+
+@pytest.mark.parametrize("batch", [1, 2, 64])
+def test_no_nodes_behind_long_tables(torch, batch):
+    """A call without nodes returns empty tensors, also where a table's positions would be shared among workgroups."""
+    say(f"no nodes, {batch} sequences of wide tables")
+    kp = torch.zeros(3, 8, 16, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(batch, 64, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), 1000, dtype=torch.int32, device="cuda")
+    q = torch.zeros(batch, 0, 32, 128, dtype=torch.bfloat16, device="cuda")
+    for tree in (None, torch.zeros(batch, 0, 0, dtype=torch.int64, device="cuda")):
+        out, lse = hdb.df11_paged_tree_attention(q, kp, kp, table, lens, tree)
+        assert out.shape == (batch, 0, 32, 128) and lse.shape == (batch, 0, 32)

@@ -162,6 +162,15 @@ def test_workspace_sizes():
     assert hdb.df11_beam_select_workspace_bytes(2, 4, 1000, 65) == hdb.df11_beam_select_workspace_bytes(0, 4, 1000, 8) == 0
 
 
+@pytest.mark.parametrize("batch", [0, 1, 2, 3, 63, 64, 65, 1 << 24])
+def test_empty_trees_need_no_workspace(batch):
+    """Without nodes nothing is cut, however wide the table is."""
+    need = hdb.df11_paged_tree_attention_workspace_bytes
+    for width in (4, 16, 17, 64, 4096, (1 << 26) - 1):
+        assert need(batch, 0, 32, 8, 128, 16, width) == need(0, batch % 64, 32, 8, 128, 16, width) == 0
+        assert need(batch, 0, 8, 1, 64, 16, width) == need(batch, 0, 16, 8, 256, 16, width) == 0
+
+
 def test_host_tensors_are_refused():
     import torch
     i = torch.zeros(2, dtype=torch.int32)
