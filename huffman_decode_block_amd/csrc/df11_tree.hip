@@ -1287,19 +1287,19 @@ Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads
     return s;
 }
 
+// A cut is made only of sizes that pass: the tiles of fewer than 2^24 rows fit 32 bits.
 bool sizes_ok(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t kv_heads, uint32_t page_size, uint64_t width) {
     return batch <= (1u << 24) && nodes <= (1u << 20) && kv_heads > 0 && kv_heads <= 65536 && q_heads > 0 && q_heads <= (1u << 20) &&
-           q_heads % kv_heads == 0 && width > 0 && width < (1u << 30) / page_size;
+           q_heads % kv_heads == 0 && width > 0 && width < (1u << 30) / page_size && span(batch, nodes * q_heads) < (1u << 24);
 }
 
-uint64_t workgroups(uint64_t batch, uint32_t kv_heads, const Shape &s) {
+uint64_t workgroups(uint32_t kv_heads, const Shape &s) {
     return (kv_heads * s.chunks + 7) / 8 * 8 * s.tiles;
 }
 
 // Whether the kernels' work items fit a launch, which holds fewer than 2^32.
-bool launchable(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t kv_heads, const Shape &s) {
-    return kv_heads * s.chunks < (uint64_t{1} << 32) && workgroups(batch, kv_heads, s) < (1u << 24) &&
-           nodes * q_heads < (uint64_t{1} << 31) && batch * nodes * q_heads < (uint64_t{1} << 24);
+bool launchable(uint32_t kv_heads, const Shape &s) {
+    return kv_heads * s.chunks < (uint64_t{1} << 32) && workgroups(kv_heads, s) < (1u << 24);
 }
 
 uint64_t workspace_of(uint64_t batch, uint64_t nodes, uint32_t q_heads, uint32_t dim, const Shape &s) {
@@ -1370,7 +1370,7 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     p.positions = static_cast<uint32_t>(width * c->page_size);
     p.scale = t->scale * kLog2e;
     const Shape s = shape_of(t->batch, t->nodes, p.group, p.kv_heads, c->head_dim, p.positions);
-    if (!launchable(t->batch, t->nodes, t->q_heads, c->kv_heads, s)) return DF11_E_INVALID_ARG;
+    if (!launchable(c->kv_heads, s)) return DF11_E_INVALID_ARG;
     p.tiles = s.tiles;
     p.splits = s.splits;
     p.units = static_cast<uint32_t>(c->kv_heads * s.chunks);
@@ -1387,7 +1387,7 @@ df11_status tree_attention(const df11_paged_cache *c, const df11_tree *t, const 
     auto fn = c->head_dim == 64    ? kernel_of<64>(e4m3, s.rows)
               : c->head_dim == 128 ? kernel_of<128>(e4m3, s.rows)
                                    : kernel_of<256>(e4m3, s.rows);
-    hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(t->batch, c->kv_heads, s)), 64 * (s.rows > 32 ? kManyWaves : kWaves), 0, st, p);
+    hipError_t err = launch(fn, static_cast<uint32_t>(workgroups(c->kv_heads, s)), 64 * (s.rows > 32 ? kManyWaves : kWaves), 0, st, p);
     if (err == hipSuccess && s.splits > 1) {
         uint32_t share = 1;
         while (share < kJoinThreads / (c->head_dim / 4) && 4 * share < s.chunks / t->batch) share *= 2;
@@ -1407,7 +1407,7 @@ extern "C" uint64_t df11_paged_tree_attention_workspace_bytes(uint64_t batch, ui
                                                               uint64_t table_width) {
     if (!dim_ok(head_dim) || !page_ok(page_size) || !sizes_ok(batch, nodes, q_heads, kv_heads, page_size, table_width)) return 0;
     const Shape s = shape_of(batch, nodes, q_heads / kv_heads, kv_heads, head_dim, table_width * page_size);
-    return launchable(batch, nodes, q_heads, kv_heads, s) ? workspace_of(batch, nodes, q_heads, head_dim, s) : 0;
+    return launchable(kv_heads, s) ? workspace_of(batch, nodes, q_heads, head_dim, s) : 0;
 }
 
 extern "C" df11_status df11_paged_tree_attention(const df11_paged_cache *cache, const df11_tree *tree,

@@ -171,6 +171,16 @@ def test_empty_trees_need_no_workspace(batch):
         assert need(batch, 0, 8, 1, 64, 16, width) == need(batch, 0, 16, 8, 256, 16, width) == 0
 
 
+@pytest.mark.parametrize("batch,nodes,q_heads,dim", [(2, 1 << 20, 1 << 20, 128), (64, 1 << 20, 1 << 19, 128), (3, 1 << 19, 1 << 20, 256),
+                                                     (1, 1 << 20, 1 << 20, 64), (1 << 24, 1 << 20, 1 << 20, 64)])
+def test_more_rows_than_a_launch_holds(batch, nodes, q_heads, dim):
+    """Sizes in their limits one by one whose tiles pass 32 bits."""
+    c, t = cache(kv_heads=1, head_dim=dim), tree(batch=batch, nodes=nodes, q_heads=q_heads, mask=None, q_batch_stride=0, q_node_stride=0)
+    for width in (1, 4, 64, 4096):
+        assert hdb.df11_paged_tree_attention_workspace_bytes(batch, nodes, q_heads, 1, dim, 16, width) == 0
+        assert attend(c, t, ts=width, width=width, ws=P, size=1 << 62) == BAD
+
+
 def test_host_tensors_are_refused():
     import torch
     i = torch.zeros(2, dtype=torch.int32)
