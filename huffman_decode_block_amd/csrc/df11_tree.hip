@@ -756,15 +756,16 @@ __device__ __forceinline__ uint32_t v_turn(uint32_t row) {
 // 16 bytes for each lane, from its offset, into LDS next to each other from `to` on
 // (uniform, like the base).  By hand: behind the builtin the compiler lets transposing
 // reads of other arrays wait for it, too.  Nothing is returned to a register, and
-// arrived() waits for what was loaded.  A scalar register that the vector unit wrote
-// is there for memory's instructions five cycles later.  Nothing else here uses m0.
+// arrived() waits for what was loaded.  The place is an operand in m0, which the
+// compiler sets and so knows the contents of.  m0 is there for a load into LDS one
+// cycle after it is written, and a scalar register that the vector unit wrote five.
 __device__ __forceinline__ void load_lds(const uint8_t *from, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(from) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(from) : "memory");
 }
 
 // The same from two bases.
 __device__ __forceinline__ void load_lds(const uint8_t *from, const uint8_t *from2, bool second, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"((second ? from2 : from) + offset) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(to), "v"((second ? from2 : from) + offset) : "memory");
 }
 
 __device__ __forceinline__ uint32_t place_of(uint8_t *stage) {

@@ -197,6 +197,21 @@ def test_host_tensors_are_refused():
         hdb.df11_beam_select(torch.zeros(1, 2, 5), torch.zeros(1, 2), 2)
 
 
+def test_inline_assembly_does_not_set_m0():
+    """m0 cannot be named as changed (the compiler keeps it for itself): what reads it takes it as an operand."""
+    csrc = os.path.join(os.path.dirname(hdb.LIB_PATH), "csrc")
+    readers = 0
+    for name in sorted(os.listdir(csrc)):
+        src = open(os.path.join(csrc, name)).read()
+        for text in re.findall(r"\basm\b[^;(]*\((.*?)\);", src, flags=re.S):
+            code = "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', text.split("::")[0]))
+            assert not re.search(r"\bm0\b", code), (name, text)
+            if "_load_lds_" in code:
+                readers += 1
+                assert '"{m0}"' in text, (name, text)
+    assert readers == 2
+
+
 def test_no_kernel_of_these_keeps_registers_in_memory():
     """The compiler may store a vector register before the lanes that a loop left behind are on again, so that they
     read back what was there before: seen where a kernel of these had more values than registers."""
