@@ -34,7 +34,11 @@ constexpr uint32_t kSlots = 2 * kComputeUnits;  // workgroups that run at once
 // What looking at masks costs a chunk, in steps: the last chunk gets so many fewer (64
 // nodes behind 1,024 positions 22.1 us, with equal chunks 24.3; nothing behind 4,096 and more).
 constexpr uint32_t kMaskedSteps = 3;
-constexpr float kSlack = 8;   // powers of two that weights may grow to before their reference follows
+constexpr float kSlack = 8;   // powers of two that weights may grow by before their reference follows
+// Powers of two by which the reference stays below the largest score of an E4M3 cache: the
+// weights become FP16, whose numbers end 2^-25 below 1 and 2^15 above.  A row's largest
+// weight is 2^7 to 2^15, and what gets lost is 2^-32 of it, not 2^-25.
+constexpr float kLift = 7;
 
 struct TreeParams {
     Pages k, v;
@@ -362,20 +366,21 @@ __device__ __forceinline__ void load_v_rows(const TreeParams &p, const Chunk &c,
 }
 
 // The running softmax of a lane's row over its wave's positions: weights are
-// exp2(s scale - ref), where ref follows the maximum as soon as it is left more
-// than kSlack behind.
-template <int kPiece>
+// exp2(s scale - ref), where ref follows the maximum (less the lift) as soon as it is
+// left more than kSlack behind.
+template <int kPiece, bool kE4M3>
 struct Running {
+    static constexpr float kBelow = kE4M3 ? kLift : 0.0f;
     float ref = -INFINITY, sum = 0;  // sum: over this lane's positions
     f4 acc[kPiece] = {};
 
     // Takes the largest of some scores (of this lane's; scale > 0) into the reference.
     __device__ __forceinline__ void follow(float top, float scale) {
-        const bool behind = top > -INFINITY && !(top * scale <= ref + kSlack);
+        const bool behind = top > -INFINITY && !(top * scale <= ref + (kSlack + kBelow));
         if (__builtin_expect(__any(behind), 0)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float to = top > -INFINITY ? fmaxf(ref, top * scale) : ref;
+            const float to = top > -INFINITY ? fmaxf(ref, top * scale - kBelow) : ref;
             const float fade = to == ref ? 1.0f : exp2_(ref - to);
             ref = to;
             sum *= fade;
@@ -466,7 +471,7 @@ __device__ __forceinline__ void transpose(const uint32_t (&pair)[8], v4u (&vt)[2
 // tile j are those of d = 16 j + r, otherwise of d = r kDim / 16 + j.
 template <int kDim, bool kE4M3, int kTiles, bool kStrided>
 __device__ __forceinline__ void add_counts(const TreeParams &p, const Work &work, const Rows &rows, const Row (&row)[kTiles], const uint64_t *s_first,
-                                           const uint8_t *vb, const int32_t *s_page, const Chunk &c, int32_t p0, Running<kDim / 16> (&run)[kTiles]) {
+                                           const uint8_t *vb, const int32_t *s_page, const Chunk &c, int32_t p0, Running<kDim / 16, kE4M3> (&run)[kTiles]) {
     constexpr int kPiece = kDim / 16;
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t first = static_cast<uint32_t>(c.c0) >> p.page_shift, in_page = (1u << p.page_shift) - 1;
@@ -596,7 +601,7 @@ tree_few_kernel(TreeParams p) {
     typename Piece<kVWords>::Value vr[8];
     auto load_v = [&](int32_t p0) { load_v_rows<kVWords>(p, c, s_page, vb, p0, r, q, vr); };
 
-    Running<kPiece> run[kTiles];
+    Running<kPiece, kE4M3> run[kTiles];
     uint32_t odd = 0;  // whether some value of V was left out of masked steps
     auto step = [&](int32_t p0, int32_t next) {
         f4 s[kTiles][2] = {};
@@ -956,7 +961,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
             qf[t][i] = __builtin_bit_cast(bf8, w ^ turned);
         }
 
-    Running<kPiece> run[kTiles];
+    Running<kPiece, kE4M3> run[kTiles];
     constexpr int kSteps = kStage / (kStep * kGroups);  // of a wave in a stage
     // Where a lane reads in a stage: rows 16 and 32 further on take their pieces in the
     // same order, so that steps and stages are constants of the instructions.  Unknown

@@ -61,10 +61,10 @@ typedef struct df11_tree {
  * and zeros and -infinity where nothing is left and for nodes i >= counts[b].
  * What positions masked for a node hold, NaN and infinities included, does not
  * matter to it.  Scores, sums and the weighted values are held in 32 bits (the
- * latter may reach 256 times the sum of the values' magnitudes before the
- * division); the weights exp(s_j) enter the product as two BF16 parts (16 bits)
- * with BF16 pages, rounded to FP16 (11 bits, 2^-25 of the largest at least) with
- * E4M3 pages.  An infinity in v_j behaves as in df11_paged_attention.  Every
+ * latter may reach 256 times, with E4M3 pages 2^15 times, the sum of the values'
+ * magnitudes before the division); the weights exp(s_j) enter the product as two
+ * BF16 parts (16 bits) with BF16 pages, rounded to FP16 (11 bits, 2^-32 of the
+ * largest at least) with E4M3 pages.  An infinity in v_j behaves as in df11_paged_attention.  Every
  * sum has a fixed order.  workspace: df11_paged_tree_attention_workspace_bytes
  * bytes of device memory, 16-byte aligned (NULL when that is 0), not kept
  * between calls; calls that run at the same time need one each.  batch = 0 or

@@ -504,3 +504,36 @@ def test_no_nodes_behind_long_tables(torch, batch):
     for tree in (None, torch.zeros(batch, 0, 0, dtype=torch.int64, device="cuda")):
         out, lse = hdb.df11_paged_tree_attention(q, kp, kp, table, lens, tree)
         assert out.shape == (batch, 0, 32, 128) and lse.shape == (batch, 0, 32)
+
+
+@pytest.mark.parametrize("dim,group,nodes,wide", [(64, 1, 9, False), (128, 4, 8, False), (256, 2, 5, False), (64, 8, 8, False), (128, 4, 12, False), (256, 4, 12, False),
+                                                  (64, 16, 9, True), (128, 4, 20, True), (128, 4, 40, True), (64, 4, 40, True)])
+def test_small_weights_of_e4m3(torch, dim, group, nodes, wide):
+    """Positions 18 (26 powers of two) behind the one that a row mostly reads, whose value is zero: all that there is.
+    A weight is off by 2^-11 of itself or, below FP16's normal numbers, by 2^-32 of the largest (1 here); scores are
+    whole numbers up to 16, an exponential off by 2^-18; the values' sum by 2^-22 for each of 128 terms at most."""
+    say(f"small weights dim {dim} group {group} nodes {nodes} wide={wide}")
+    length, page = 80, 16
+    a, reads = build(torch, [length, length // 2], nodes, 2, group, dim, page, True, chain=True)
+    code = lambda x: torch.tensor(float(x)).to(torch.float8_e4m3fn).view(torch.uint8).item()  # noqa: E731
+    k, v, table = a["k_pages"].view(torch.uint8), a["v_pages"].view(torch.uint8), a["page_table"]
+    k.zero_()
+    k[..., 0] = code(-2)
+    v.bitwise_and_(0x77)  # positive numbers of up to 240
+    for b, at in enumerate((37, 3)):
+        k[int(table[b, at // page]), :, at % page, 0] = code(16)
+        v[int(table[b, at // page]), :, at % page] = 0
+    a["q"].zero_()
+    a["q"][..., 0] = 1
+    a["scale"], a["k_scale"] = 1.0, torch.ones(2, device="cuda")
+    if wide:
+        a["page_table"] = torch.full((2, 1 << 15), -1, dtype=torch.int32, device="cuda")
+        a["page_table"][:, :table.shape[1]] = table
+    (out, lse), (ref, ref_lse, _, lse_bound) = hdb.df11_paged_tree_attention(**a), reference(torch, a, reads)
+    assert bool(((lse.double() - ref_lse).abs() <= lse_bound).all())
+    size = (a["lens"].view(2, 1, 1, 1) + torch.arange(1, nodes + 1, device="cuda").view(1, nodes, 1, 1)).double()
+    v_max = 240 * a["v_scale"].double().repeat_interleave(group).view(1, 1, -1, 1)
+    bound = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * ref + 2.0 ** -32 * size * v_max
+    assert float(ref.min()) >= 0 and float((ref > 4 * bound).double().mean()) > 0.9, "the bound leaves nothing to see"
+    over = (out.double() - ref).abs() - bound
+    assert float(over.max()) <= 0, float(((out.double() - ref).abs() / bound.clamp_min(1e-30)).max())
