@@ -526,9 +526,9 @@ tile_kernel(MulParams p) {
         w = next;
         flip = other;
     }
+    f4 *sum = reinterpret_cast<f4 *>(s_all) + (wave * 64 + lane);
     if (kGroups > 1) {  // the other groups' sums through LDS to the first
         static_assert((kGroups - 1) * kRowsM * kRowsN * 4 <= kGroups * kGroupBytes, "the groups' sums fit");
-        f4 *sum = reinterpret_cast<f4 *>(s_all) + (wave * 64 + lane);
         __syncthreads();
         if (group > 0) {
 #pragma unroll
@@ -538,12 +538,6 @@ tile_kernel(MulParams p) {
         }
         __syncthreads();
         if (group > 0) return;
-#pragma unroll
-        for (int g = 0; g < kGroups - 1; ++g)
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) acc[m][i] += sum[((g * kTiles + m) * kCols + i) * 64 * kTileWaves];
     }
 
     // a lane: 4 kCols columns of the wave's 16 kCols, row r of each tile
@@ -553,6 +547,11 @@ tile_kernel(MulParams p) {
         const uint32_t row = m0 + 16 * m + r;
         if (row >= p.m || col >= p.n) continue;
         uint16_t *to = p.y + uint64_t{row} * p.y_stride + col;
+        // a tile's sums as they are needed: all at once take more registers than there are
+#pragma unroll
+        for (int g = 0; g < kGroups - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[m][i] += sum[((g * kTiles + m) * kCols + i) * 64 * kTileWaves];
         uint32_t o[2 * kCols];
 #pragma unroll
         for (int i = 0; i < 2 * kCols; ++i) o[i] = pack2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);

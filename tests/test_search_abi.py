@@ -225,3 +225,17 @@ def test_no_kernel_of_these_keeps_registers_in_memory():
         assert count.group(1) == b"\0", m.group(1)
     assert {"tree_few_kernel", "tree_many_kernel", "tree_join_kernel", "beam_part_kernel", "beam_choose_kernel", "fork_plan_kernel",
             "fork_table_kernel", "copy_kernel", "compact_kernel"} <= seen
+
+
+def test_no_kernel_of_the_library_keeps_registers_in_memory():
+    built = open(hdb.LIB_PATH, "rb").read()
+    seen = set()
+    for m in re.finditer(rb"(_ZN12_GLOBAL__N_1\w+)\.kd", built):
+        count = re.compile(rb"\.vgpr_spill_count(.)", re.S).search(built, m.end())
+        if count is None or count.start() - m.end() > 400:
+            continue  # a name elsewhere than in the kernel's description
+        seen.add(m.group(1))
+        assert count.group(1) == b"\0", m.group(1)
+    for name in (b"tile_kernel", b"token_kernel", b"attend_kernel", b"df11_decode_kernel", b"run_pack_kernel", b"tree_few_kernel", b"beam_part_kernel"):
+        assert any(name in s for s in seen), name
+    assert len(seen) > 90
