@@ -308,8 +308,8 @@ def df11_paged_fork(parents, page_table, lens, refs, page_size: int, room: int =
     _tensor(refs, "refs", i32, 1, dev)
     _dense(refs, "refs")
     page_size, room = int(page_size), int(room)
-    if page_size < 0 or room < 0:
-        raise ValueError("page_size and room must not be negative")
+    if not 0 <= page_size < 1 << 32 or not 0 <= room < 1 << 64:  # what their C types hold
+        raise ValueError("page_size must fit 32 bits and room 64, neither negative")
     handle, ctx = _place(dev, stream)
     if ctx is None:
         return _fork(parents, page_table, lens, refs, page_size, room, workspace, dev, handle)

@@ -411,3 +411,16 @@ def test_refusals(torch):
     assert e.value.status == hdb.DF11_E_BUFFER_TOO_SMALL
     assert int(hdb.df11_paged_fork(i[:0], table[:0], i[:0], refs, 16)[3]) == 0
     assert int(refs.sum()) == 0 and int(table.sum()) == 0
+
+
+def test_fork_sizes_past_their_types(torch):
+    """Numbers that C would cut off to allowed ones are refused, and nothing changes."""
+    say("fork sizes past 32 and 64 bits")
+    table = torch.tensor([[0, 1], [2, -1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20, 5], dtype=torch.int32, device="cuda")
+    refs = torch.tensor([1, 1, 1, 0, 0], dtype=torch.int32, device="cuda")
+    parents = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    for page_size, room in (((1 << 32) + 16, 1), (16 - (1 << 32), 1), (16, (1 << 64) + 1), (16, 1 - (1 << 64))):
+        with pytest.raises(ValueError):
+            hdb.df11_paged_fork(parents, table, lens, refs, page_size, room=room)
+    assert table.tolist() == [[0, 1], [2, -1]] and lens.tolist() == [20, 5] and refs.tolist() == [1, 1, 1, 0, 0]
