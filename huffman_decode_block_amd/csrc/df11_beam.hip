@@ -20,16 +20,22 @@ using namespace df11p;
 // chooses among all parts' best ones.
 //
 // 32 searches of 8 beams over 128,256 BF16 logits, 16 chosen (52 MB of beams that
-// go on): 24 us for the first kernel, 11 for the second.  The first is bound by its workgroups' chains
-// (load, maxima, threshold, ranks: two rounds of four on a compute unit), 2.2 TB/s;
-// with twice as many parts of half the size it takes 23 and the second 15.  One search
-// of 4 beams over 32,000: 4.5 + 4.5, a kernel's start and end and one chain each.
+// go on): 19.6 us for the first kernel, 8.9 for the second.  The first is bound by its workgroups' chains
+// (load, maxima, threshold, ranks: two rounds of four on a compute unit), 2.7 TB/s.
+// One search of 4 beams over 32,000: 4.4 + 5.2, a kernel's start and end and one chain
+// each; of 16 beams over 160,000, the best 32: 9.3 + 16.5, 40,448 candidates in one workgroup.
 //
-// Choosing k of n: with t the k-th largest of 64 lanes' largest values, at least
-// k values reach t, and few more do; they go to LDS in any order, and each counts
-// those before it (eight at a time: one at a time the reads from LDS, each waited for,
-// were a third of both kernels).  t is sought bit by bit, half of the bits (a value that is
-// lower than the k-th largest only lets more values through).
+// Choosing k of n: with t the k-th largest of the largest values of 256 sets, at least
+// k values reach t, and few more do if the largest ones are spread over the sets; they
+// go to LDS in any order, and each counts those before it (eight at a time: one at a time
+// the reads from LDS, each waited for, were a third of both kernels).  t is sought bit
+// by bit, some of the bits (a value that is lower than the k-th largest only lets more
+// values through).  Only where more values than LDS has room for are equal, or nearly so,
+// are the best sought one after the other.  The sets are the threads' values in the first
+// kernel; of one wave's lanes the 64th largest value is the smallest, which too many
+// reach.  In the second a list's places go to different sets: as they lie,
+// a thread would have one place of each list where k divides 256, its best or its worst
+// (16 beams over 160,000: k = 32 1,896 us in place of 27, 64 7,346 in place of 48).
 
 constexpr uint32_t kThreads = 256, kWaves = kThreads / 64;
 constexpr uint32_t kMaxK = 64;
@@ -59,16 +65,34 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 __device__ __forceinline__ float of_key(uint32_t k) { return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-// A value that at least k lanes' reach (-infinity where fewer have more), near the k-th largest.
-__device__ __forceinline__ float reached_by(float x, uint32_t k) {
-    const uint32_t key = key_of(x);
+constexpr uint32_t kTops = 256;  // values among which the k-th largest is sought
+
+// Of the keys of kTops values, in LDS, kPer in each lane: the largest of groups.
+template <int kPer, int kBits>
+__device__ __forceinline__ float reached(const uint32_t *keys, uint32_t k) {
+    uint32_t key[kPer] = {};
+#pragma unroll
+    for (uint32_t i = 0; i < kTops / 64; ++i) key[i % kPer] = max(key[i % kPer], keys[i * 64 + (threadIdx.x & 63u)]);
+    const auto reaching = [&](uint32_t t) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n += __popcll(__ballot(key[i] >= t));
+        return n;
+    };
     uint32_t t = 0;
 #pragma unroll
-    for (int bit = 31; bit >= 16; --bit) {
+    for (int bit = 31; bit > 31 - kBits; --bit) {
         const uint32_t with = t | 1u << bit;
-        if (__popcll(__ballot(key >= with)) >= k) t = with;
+        if (reaching(with) >= k) t = with;
     }
     return fmaxf(of_key(t), -INFINITY);  // NaN for keys below that of -infinity
+}
+
+// A value that at least k of them reach (-infinity where fewer are more), near the k-th
+// largest: kBits of it.  Groups as large as leave four for each of the k.
+template <int kBits>
+__device__ __forceinline__ float reached_by(const uint32_t *keys, uint32_t k) {
+    return k <= kTops / 16 ? reached<1, kBits>(keys, k) : k <= kTops / 8 ? reached<2, kBits>(keys, k) : reached<4, kBits>(keys, k);
 }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -127,7 +151,8 @@ __device__ __forceinline__ Eight<kF32> load_logits(const void *row, uint32_t at,
 
 template <bool kF32, int kLoads>
 __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
-    __shared__ float s_max[kWaves], s_sum[kWaves], s_reach[kWaves];
+    __shared__ float s_max[kWaves], s_sum[kWaves];
+    __shared__ uint32_t s_top[kTops];
     __shared__ __attribute__((aligned(16))) float s_x[kRoom + kAtOnce];
     __shared__ __attribute__((aligned(16))) uint32_t s_at[kRoom + kAtOnce];
     __shared__ uint32_t s_n;
@@ -153,19 +178,16 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamParams p) {
         for (int j = 1; j < static_cast<int>(kEach); ++j) tops[i] = fmaxf(tops[i], x[i][j]);
         top = fmaxf(top, tops[i]);
     }
-    const float reach = reached_by(top, p.k), wave_top = wave_max(top);
-    if (lane == 0) {
-        s_max[wave] = wave_top;
-        s_reach[wave] = reach;
-    }
+    const float wave_top = wave_max(top);
+    static_assert(kTops == kThreads, "each thread's largest");
+    s_top[threadIdx.x] = key_of(top);
+    if (lane == 0) s_max[wave] = wave_top;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    float m = s_max[0], t = s_reach[0];
+    const float t = reached_by<16>(s_top, p.k);
+    float m = s_max[0];
 #pragma unroll
-    for (uint32_t w = 1; w < kWaves; ++w) {
-        m = fmaxf(m, s_max[w]);
-        t = fmaxf(t, s_reach[w]);
-    }
+    for (uint32_t w = 1; w < kWaves; ++w) m = fmaxf(m, s_max[w]);
     // unpacked anew each time: kept, the floats would take twice the registers
     const auto as_loaded = [&] {
 #pragma unroll
@@ -310,20 +332,23 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
     __shared__ __attribute__((aligned(16))) double s_score[kRoom + kAtOnce];
     __shared__ __attribute__((aligned(16))) float s_x[kRoom + kAtOnce];
     __shared__ __attribute__((aligned(16))) uint32_t s_beam[kRoom + kAtOnce], s_token[kRoom + kAtOnce];
-    __shared__ float s_reach[kWaves];
-    __shared__ uint32_t s_n;
+    __shared__ uint32_t s_top[2][kTops];
+    __shared__ uint32_t s_list[kRoom];
+    __shared__ uint32_t s_n, s_lists;
     const uint32_t b = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint64_t row0 = uint64_t{b} * p.beams;
 
-    // candidate c: place c % k of part c / k of a beam; a beam that has ended has one,
-    // its first.  A thread's first ones are on their way while the beams' sums are
-    // added; what a beam without tokens has there is not looked at.
-    const uint32_t per_beam = p.parts * p.k, all = per_beam * p.beams;
+    // candidate c: place c % k of list c / k, a part of a beam, best first; a beam that
+    // has ended has one, its first.  All of them, or the first of each list, are on
+    // their way while the beams' sums are added; what a beam without tokens has there is
+    // not looked at.
+    const uint32_t lists = p.parts * p.beams, per_beam = p.parts * p.k, all = lists * p.k;
+    const bool few = all <= kHeld * kThreads;
     float held_x[kHeld];
     int32_t held_at[kHeld];
 #pragma unroll
     for (uint32_t h = 0; h < kHeld; ++h) {
-        const uint32_t c = min(h * kThreads + threadIdx.x, all - 1);
+        const uint32_t i = h * kThreads + threadIdx.x, c = few ? min(i, all - 1) : min(i, lists - 1) * p.k;
         held_x[h] = p.best[row0 * per_beam + c];
         held_at[h] = p.at[row0 * per_beam + c];
     }
@@ -360,7 +385,8 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
             s_done[i] = done;
         }
     }
-    if (threadIdx.x == 0) s_n = 0;
+    s_top[0][threadIdx.x] = s_top[1][threadIdx.x] = key_of(-INFINITY);
+    if (threadIdx.x == 0) s_n = s_lists = 0;
     __syncthreads();
 
     const auto of = [&](uint32_t c, float x, int32_t token, Candidate &out) {
@@ -382,24 +408,71 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
         const uint64_t at = row0 * per_beam + c;
         return of(c, p.best[at], p.at[at], out);
     };
-    float top = -INFINITY;
+    const auto show = [&](uint32_t *tops, uint32_t at, double score) {
+        if (score > -INFINITY) atomicMax(&tops[at % kTops], key_of(static_cast<float>(score)));
+    };
+    // Of many lists those that may hold one of the k best: their first ones reach the
+    // k-th largest of all lists'.  Where more do than LDS names, all are looked at.
+    uint32_t there = lists;
+    bool named = false;
+    if (!few) {
+        float first[kHeld];
+#pragma unroll
+        for (uint32_t h = 0; h < kHeld; ++h) {
+            const uint32_t list = h * kThreads + threadIdx.x;
+            Candidate x;
+            first[h] = list < lists && of(list * p.k, held_x[h], held_at[h], x) ? static_cast<float>(x.score) : NAN;
+            show(s_top[0], list, first[h]);
+        }
+        for (uint32_t list = kHeld * kThreads + threadIdx.x; list < lists; list += kThreads) {
+            Candidate x;
+            if (candidate(list * p.k, x)) show(s_top[0], list, x.score);
+        }
+        __syncthreads();
+        const float least = reached_by<20>(s_top[0], p.k);
+        const auto note = [&](uint32_t list) {
+            const uint32_t n = atomicAdd(&s_lists, 1u);
+            if (n < kRoom) s_list[n] = list;
+        };
+#pragma unroll
+        for (uint32_t h = 0; h < kHeld; ++h)
+            if (first[h] >= least) note(h * kThreads + threadIdx.x);
+        for (uint32_t list = kHeld * kThreads + threadIdx.x; list < lists; list += kThreads) {
+            Candidate x;
+            if (candidate(list * p.k, x) && static_cast<float>(x.score) >= least) note(list);
+        }
+        __syncthreads();
+        named = s_lists <= kRoom;
+        if (named) there = s_lists;
+    }
+    // Those lists' candidates: at least k of them reach the k-th largest of the largest
+    // in kTops sets, and few more.  Places of one list, and lists at one place, are of
+    // different sets.
+    const uint32_t size = there * p.k, apart = there | 1;
+    const bool fit = size <= kHeld * kThreads;
+    const auto place = [&](uint32_t i) { return named ? s_list[i / p.k] * p.k + i % p.k : i; };
+    if (named && fit && size) {
+#pragma unroll
+        for (uint32_t h = 0; h < kHeld; ++h) {
+            const uint64_t at = row0 * per_beam + place(min(h * kThreads + threadIdx.x, size - 1));
+            held_x[h] = p.best[at];
+            held_at[h] = p.at[at];
+        }
+    }
     Candidate held[kHeld];
 #pragma unroll
     for (uint32_t h = 0; h < kHeld; ++h) {
-        const uint32_t c = h * kThreads + threadIdx.x;
-        if (c >= all || !of(c, held_x[h], held_at[h], held[h])) held[h].score = -INFINITY;
-        top = fmaxf(top, static_cast<float>(held[h].score));
+        const uint32_t i = h * kThreads + threadIdx.x;
+        if (!fit || i >= size || !of(place(i), held_x[h], held_at[h], held[h])) held[h].score = -INFINITY;
+        show(s_top[1], i / p.k + i % p.k * apart, held[h].score);
     }
-    for (uint32_t c = kHeld * kThreads + threadIdx.x; c < all; c += kThreads) {
-        Candidate x;
-        if (candidate(c, x)) top = fmaxf(top, static_cast<float>(x.score));
-    }
-    const float reach = reached_by(top, p.k);
-    if (lane == 0) s_reach[wave] = reach;
+    if (!fit)
+        for (uint32_t i = threadIdx.x; i < size; i += kThreads) {
+            Candidate x;
+            if (candidate(place(i), x)) show(s_top[1], i / p.k + i % p.k * apart, x.score);
+        }
     __syncthreads();
-    float t = s_reach[0];
-#pragma unroll
-    for (uint32_t w = 1; w < kWaves; ++w) t = fmaxf(t, s_reach[w]);
+    const float t = reached_by<20>(s_top[1], p.k);
     const auto keep = [&](const Candidate &x) {
         const uint32_t n = atomicAdd(&s_n, 1u);
         if (n < kRoom) {
@@ -412,10 +485,11 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(BeamParams p) {
 #pragma unroll
     for (uint32_t h = 0; h < kHeld; ++h)
         if (held[h].score > -INFINITY && static_cast<float>(held[h].score) >= t) keep(held[h]);
-    for (uint32_t c = kHeld * kThreads + threadIdx.x; c < all; c += kThreads) {
-        Candidate x;
-        if (candidate(c, x) && static_cast<float>(x.score) >= t) keep(x);
-    }
+    if (!fit)
+        for (uint32_t i = threadIdx.x; i < size; i += kThreads) {
+            Candidate x;
+            if (candidate(place(i), x) && static_cast<float>(x.score) >= t) keep(x);
+        }
     __syncthreads();
     const uint32_t n = s_n;
     const uint64_t out = uint64_t{b} * p.k;
@@ -486,7 +560,8 @@ struct Cut {
 
 // Parts as large as leave eight workgroups for each compute unit, of 1, 2, 4 or 8 loads.
 // A large part pays once for its threshold and ranks and gives the second kernel fewer
-// candidates; with sixteen for each (above) the sum was 38 us in place of 35.
+// candidates.  32 x 8 beams over 128,256 take 28.4 us so, with sixteen for each 27.9,
+// with four 28.6; 8 x 4 beams, the best 8, 15.5, 15.2 and 13.5.
 Cut cut_of(uint64_t rows, uint64_t vocab) {
     Cut c = {8, 0, 0};
     while (c.loads > 1 && rows * ((vocab + c.loads * kThreads * kEach - 1) / (c.loads * kThreads * kEach)) < kWantGroups) c.loads /= 2;

@@ -234,3 +234,54 @@ def test_refusals(torch):
     with pytest.raises(hdb.DF11Error):
         hdb.df11_beam_select(x[:, :, :0], s, 4)
     assert hdb.df11_beam_select(x[:0], s[:0], 4)[1].shape == (0, 4)
+
+
+@pytest.mark.parametrize("batch,beams,vocab", [(1, 16, 160000), (1, 64, 32000), (1, 4, 128256), (32, 8, 128256), (64, 4, 50000)])
+def test_many_continuations_are_not_sought_one_by_one(torch, batch, beams, vocab):
+    """64 continuations take at most ten times as long as 8 of the same logits, also 32, of which a workgroup's threads
+    are a multiple: sought one after the other they took up to 170 times as long."""
+    say(f"beam {batch}x{beams} of {vocab}: time by k")
+    x, s = make(torch, batch, beams, vocab, torch.bfloat16, seed=3)
+    took = {}
+    for k in (8, 32, 64):
+        for _ in range(2):
+            hdb.df11_beam_select(x, s, k)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                hdb.df11_beam_select(x, s, k)
+        times = []
+        for _ in range(7):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            graph.replay()
+            end.record()
+            torch.cuda.synchronize()
+            times.append(begin.elapsed_time(end))
+        took[k] = sorted(times)[3]
+    assert took[32] <= 10 * took[8] and took[64] <= 10 * took[8], took
+
+
+@pytest.mark.parametrize("k", [1, 8, 16, 32, 33, 64])
+@pytest.mark.parametrize("batch,beams,vocab", [(2, 3, 20000), (1, 16, 70001), (1, 300, 9000), (2, 1000, 300), (3, 2, 700)])
+def test_lists_of_many_kinds(torch, batch, beams, vocab, k):
+    """One beam far ahead of the others, its best tokens next to each other; beams with a token or two; ended ones; all alike."""
+    say(f"beam {batch}x{beams} of {vocab}, best {k}: uneven beams")
+    x, s = make(torch, batch, beams, vocab, torch.float32, seed=vocab + k)
+    ahead = s.clone()
+    ahead[:, beams // 2] += 40
+    x[:, beams // 2, vocab // 3:vocab // 3 + 100] += 20
+    check(torch, x, ahead, k)
+    y = x.clone()
+    y[:, ::2, 2:] = -math.inf
+    check(torch, y, s, k, pad=5)
+    y[:, 1::2, 40:] = -math.inf
+    done = torch.zeros(batch, beams, dtype=torch.bool, device="cuda")
+    done[:, beams // 3:] = True
+    check(torch, y, s, k, done=done, pad=7)
+    same = torch.full_like(s, -1.0)
+    check(torch, torch.zeros(batch, beams, vocab, device="cuda"), same, k, equal=True)
+    z = torch.zeros(batch, beams, vocab, device="cuda")
+    z[:, beams // 2, ::2] = 1.0
+    check(torch, z, same, k, equal=True)
