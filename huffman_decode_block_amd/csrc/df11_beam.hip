@@ -20,9 +20,9 @@ using namespace df11p;
 // chooses among all parts' best ones.
 //
 // 32 searches of 8 beams over 128,256 BF16 logits, 16 chosen (52 MB of beams that
-// go on): 19.6 us for the first kernel, 8.9 for the second.  The first is bound by its workgroups' chains
-// (load, maxima, threshold, ranks: two rounds of four on a compute unit), 2.7 TB/s.
-// One search of 4 beams over 32,000: 4.4 + 5.2, a kernel's start and end and one chain
+// go on): 20 us for the first kernel, 8.8 for the second.  The first is bound by its workgroups' chains
+// (load, maxima, threshold, ranks: two rounds of four on a compute unit), 2.6 TB/s.
+// One search of 4 beams over 32,000: 4.4 + 5.0, a kernel's start and end and one chain
 // each; of 16 beams over 160,000, the best 32: 9.3 + 16.5, 40,448 candidates in one workgroup.
 //
 // Choosing k of n: with t the k-th largest of the largest values of 256 sets, at least

@@ -32,7 +32,8 @@ constexpr uint32_t kChunkPages = kMaxChunk / kMinPage + 1;
 constexpr uint32_t kPad = 4;  // floats between rows in LDS: they start in different banks
 constexpr uint32_t kSlots = 2 * kComputeUnits;  // workgroups that run at once
 // What looking at masks costs a chunk, in steps: the last chunk gets so many fewer (64
-// nodes behind 1,024 positions 22.1 us, with equal chunks 24.3; nothing behind 4,096 and more).
+// nodes behind 1,024 positions 22.8 us, with equal chunks 24.8; 4,096 30.1 and 30.6; 8,192
+// 33.1 and 32.9).
 constexpr uint32_t kMaskedSteps = 3;
 constexpr float kSlack = 8;   // powers of two that weights may grow by before their reference follows
 // Powers of two by which the reference stays below the largest score of an E4M3 cache: the
@@ -150,10 +151,10 @@ __device__ __forceinline__ int32_t length_of(const TreeParams &p, uint32_t b) {
 // A batch of different lengths: chunks as long as each other, so that a long sequence
 // has more of them.  Lane b counts those of sequence b: the steps of all are shared
 // among as many chunks as run at once, less half of one for each sequence's last
-// (less a quarter: 45 us for the first below).  Against as many chunks for each sequence:
-// 16 ragged up to 2,048 with 25 nodes 37.5 us in place of 42.6, 8 up to 8,192 49 (63), 32
-// up to 4,096 with 8 nodes 66 (76); equal lengths pay for the scans, 16 x 2,048 52.6 us
-// (50.6).
+// (less a quarter: 43.0 us for the first below).  Against as many chunks for each sequence:
+// 16 ragged up to 2,048 with 25 nodes 35.9 us in place of 42.2, 8 up to 8,192 47.1 (62.0), 32
+// up to 4,096 with 8 nodes 64.2 (75.3); equal lengths pay for the scans and the ends, 16 x
+// 2,048 with 25 nodes 49.9 us (49.2), 8 x 32,768 E4M3 with 16 nodes of 64 heads 181 (175).
 __device__ __forceinline__ void ragged_work(const TreeParams &p, uint32_t chunk, Work &w) {
     const uint32_t lane = threadIdx.x & 63u, b = min(lane, p.batch - 1);
     const int32_t len = length_of(p, b), start = p.starts ? min(max(p.starts[b * p.starts_batch], 0), len) : 0;
@@ -513,8 +514,8 @@ constexpr int waves_for(int dim) { return dim == 64 ? 3 : dim == 128 ? 2 : 1; }
 // memory, each once; they join in LDS.  No barrier stands in the loop, and a step's
 // loads are on their way while the one before is computed.  Bound by HBM and, for short
 // sequences, by start and end: 16 sequences of 4,096 with 8 nodes of 32 heads (268 MB)
-// 58 us, 4.6 TB/s; 1 x 8,192 with 8 nodes 19 us.  Through LDS (below) those two take 63
-// and 20.  Heads of 256 take one tile of rows: two need more registers than there are.
+// 59 us, 4.6 TB/s, E4M3 34, 4.0; 1 x 8,192 with 8 nodes 19 us.  Through LDS (below) those
+// take 64, 39 and 21.  Heads of 256 take one tile of rows: two need more registers than there are.
 template <int kDim, bool kE4M3, int kTiles>
 __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_for(kDim))))
 tree_few_kernel(TreeParams p) {
@@ -737,9 +738,10 @@ tree_few_kernel(TreeParams p) {
 // instructions.  64 KiB of stages (two of BF16, four of E4M3) leave place for two
 // workgroups, whose waves fill each other's waits.  Bound by the vector and the matrix unit,
 // which overlap little: a step of 32 rows and 32 positions of 128 takes a SIMD about 1,800
-// cycles, 768 of them matrix instructions.  8 x 32,768 with 16 nodes of 64 heads: BF16 254
-// us (4.2 TB/s, 540 TFLOP/s), E4M3 197 (698 TFLOP/s); 1 x 8,192 with 64 nodes of 32 heads
-// 35, of which start and end are about 10; chains of 509 over heads of 256 41.
+// cycles, 768 of them matrix instructions.  8 x 32,768 with 16 nodes of 64 heads: BF16 257
+// us (4.2 TB/s, 536 TFLOP/s), E4M3 178 (773 TFLOP/s); 1 x 8,192 with 64 nodes of 32 heads
+// 32, of which start and end are about 10; chains of 509 over heads of 256 39 (the joins
+// among them).
 constexpr uint32_t kManyWaves = 4;
 
 template <int kDim>
@@ -1178,7 +1180,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, 2) tree_many_kernel(TreeParam
 
 // Joins the chunks: kDim / 4 lanes, four values each, for every `share`-th chunk of
 // a row (a power of two); LDS joins those.  Bound by latency: a lane has four
-// chunks' values on their way.  About 4 us behind 1 x 8,192 with 64 nodes (8 chunks);
+// chunks' values on their way.  About 5 us behind 1 x 8,192 with 64 nodes (16 chunks);
 // with one lane for all chunks of a row, one after the other, 1 x 8,192 with 8 nodes (64
 // chunks) took 53 us in place of 20.
 constexpr uint32_t kJoinThreads = 256;
@@ -1254,8 +1256,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams p, u
 
 // Tiles of 128 rows read K and V half as often as those of 64, but are half as many
 // workgroups: they are taken where each still has this many positions.  64 nodes of 32 heads:
-// 1 x 32,768 78 us against 82 with 64 rows, 1 x 65,536 E4M3 106 against 112, 8 x 8,192 with
-// half the nodes 79 against 90; with fewer positions there are not enough workgroups.
+// 1 x 32,768 73 us against 80 with 64 rows, 1 x 65,536 E4M3 93 against 98; 8 up to 8,192 with
+// 25 nodes 46.9 against 50.2; with fewer positions there are not enough workgroups.
 constexpr uint64_t kLargeChunk = 1024;
 
 struct Shape {
@@ -1266,7 +1268,10 @@ struct Shape {
 };
 
 // Sequences are cut where there are fewer workgroups than run at once (two for each
-// compute unit), into chunks of 128 positions at least, a step for each wave.
+// compute unit), into chunks of 128 positions at least, a step for each wave.  17 to 32
+// rows over heads of 256 take tiles of 64, of which half stay empty: in two tiles of 16,
+// which read K and V twice, 1 x 8,192 takes 24.9 us (20.2), 16 x 4,096 71 (66), 8 x 32,768
+// E4M3 122 (113), 64 up to 1,000 51 (37), each with 4 cache heads for 8.
 Shape shape_of(uint64_t batch, uint64_t nodes, uint32_t group, uint32_t kv_heads, uint32_t dim, uint64_t positions) {
     const uint64_t rows = nodes * group;
     Shape s;

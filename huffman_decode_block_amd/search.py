@@ -108,9 +108,11 @@ def df11_paged_tree_attention(q, k_pages, v_pages, page_table, lens, tree=None, 
     tree        int64 [batch, nodes, ceil(nodes / 64)]: bit a % 64 of word a / 64 of node i says whether i reads
                 node a (itself only if named); None: a chain, nodes 0..i
     nodes       int32 [batch]: how many nodes each sequence has; None: all
-    starts      int32 [batch, nodes]: a node reads positions [start, lens[b]) and nodes; None: from 0
+    starts      int32 [batch, nodes]: a node reads positions [start, lens[b]) and nodes; None: from 0.  A start cuts
+                nothing of the nodes: a chain longer than its window needs a tree
     scale       of the scores; None: head_dim ** -0.5
-    tree and starts may have any strides but for the words of a node, 0 among them (one tree for all sequences).
+    tree and starts may have any strides, 0 among them (one tree for all sequences), but the words of a node lie next
+    to each other and nodes share none.
     Returns (out, lse): BF16 like q and float32 [batch, nodes, q_heads]; rows that read nothing get zeros and -inf."""
     torch = _torch or _load()
     i32 = torch.int32

@@ -64,10 +64,12 @@ typedef struct df11_tree {
  * latter may reach 256 times, with E4M3 pages 2^15 times, the sum of the values'
  * magnitudes before the division); the weights exp(s_j) enter the product as two
  * BF16 parts (16 bits) with BF16 pages, rounded to FP16 (11 bits, 2^-32 of the
- * largest at least) with E4M3 pages.  An infinity in v_j behaves as in df11_paged_attention.  Every
- * sum has a fixed order.  workspace: df11_paged_tree_attention_workspace_bytes
- * bytes of device memory, 16-byte aligned (NULL when that is 0), not kept
- * between calls; calls that run at the same time need one each.  batch = 0 or
+ * largest at least) with E4M3 pages.  An infinity in v_j behaves as in
+ * df11_paged_attention, but may give an infinity, too, where exp(s_j) is below
+ * 2^-126 of the largest (there NaN).  Every sum has a fixed order.  workspace:
+ * df11_paged_tree_attention_workspace_bytes bytes of device memory, 16-byte
+ * aligned (NULL when that is 0), not kept between calls; calls that run at the
+ * same time need one each.  batch = 0 or
  * nodes = 0 is a no-op.  Errors: DF11_E_INVALID_ARG (null or misaligned
  * pointers; sizes and strides as for df11_paged_attention, and 2^30 positions
  * or more in a table; positions of a page 256 MiB apart; mask_node_stride below
